@@ -28,7 +28,9 @@ EXPORTED = ("diffattn_status_string", "diffattn_lambda", "diffattn_fwd", "diffat
             "diffattn_kv_append_paged_fp8", "diffattn_decode_noalloc_read_error",
             "diffattn_selftest_timeout", "diffattn_gemm_residual", "diffattn_gemm_swiglu", "diffattn_fwd_host",
             "diffattn_fwd_host_buffer_size", "diffattn_train_saved_size", "diffattn_fwd_train",
-            "diffattn_bwd_saved")
+            "diffattn_bwd_saved", "diffattn_rope_freqs", "diffattn_rope", "diffattn_kv_append_chunk_paged",
+            "diffattn_kv_append_chunk_paged_fp8", "diffattn_chunk_paged", "diffattn_chunk_paged_fp8",
+            "diffattn_chunk_workspace_size")
 
 
 class DiffAttnError(RuntimeError):
@@ -41,6 +43,12 @@ class Tensor4(ctypes.Structure):
     """diffattn_tensor: pointer plus (b, h, n) strides in elements."""
     _fields_ = [("ptr", ctypes.c_void_p), ("stride_b", ctypes.c_int64), ("stride_h", ctypes.c_int64),
                 ("stride_n", ctypes.c_int64)]
+
+
+class Rotation(ctypes.Structure):
+    """diffattn_rotation: the frequency table on the device, rotated channels, pairing, magnitude."""
+    _fields_ = [("freqs", ctypes.c_void_p), ("rotary_dim", ctypes.c_int), ("interleaved", ctypes.c_int),
+                ("magnitude", ctypes.c_float)]
 
 
 _lib = None
@@ -117,6 +125,24 @@ def load_library(path: str = LIB_PATH) -> ctypes.CDLL:
     lib.diffattn_bwd_saved.restype = i32
     lib.diffattn_bwd_saved.argtypes = ([Tensor4] * 5 + [vp, vp] + [i32] * 6 + [f32] * 3 + [i32, vp, sz] + [vp] * 7 +
                                        [vp, sz, vp])
+    f64, rp = ctypes.c_double, ctypes.POINTER(Rotation)
+    lib.diffattn_rope_freqs.restype = i32
+    lib.diffattn_rope_freqs.argtypes = [i32, f64, i32, f64, i32, f64, f64, vp, fp]
+    lib.diffattn_rope.restype = i32
+    lib.diffattn_rope.argtypes = [ctypes.POINTER(Tensor4)] * 2 + [ctypes.POINTER(i32), i32, vp, i32, i32, i32, rp, i32, i32,
+                                                                  i32, vp]
+    append = [Tensor4] * 3 + [i32] + [Tensor4] * 3 + [vp, i32, i32, vp, vp, rp] + [i32] * 5
+    lib.diffattn_kv_append_chunk_paged.restype = i32
+    lib.diffattn_kv_append_chunk_paged.argtypes = append + [vp]
+    lib.diffattn_kv_append_chunk_paged_fp8.restype = i32
+    lib.diffattn_kv_append_chunk_paged_fp8.argtypes = append + [f32] * 3 + [vp]
+    chunk = [Tensor4] * 5 + [vp, i32, i32, vp, vp, i32, vp, vp] + [i32] * 6 + [f32] * 3
+    lib.diffattn_chunk_paged.restype = i32
+    lib.diffattn_chunk_paged.argtypes = chunk + [i32, vp, sz, vp]
+    lib.diffattn_chunk_paged_fp8.restype = i32
+    lib.diffattn_chunk_paged_fp8.argtypes = chunk + [f32] * 3 + [i32, vp, sz, vp]
+    lib.diffattn_chunk_workspace_size.restype = i32
+    lib.diffattn_chunk_workspace_size.argtypes = [i32] * 7 + [ctypes.POINTER(sz)]
     fpp = ctypes.POINTER(ctypes.c_float)
     lib.diffattn_lambda_bwd.restype = i32
     lib.diffattn_lambda_bwd.argtypes = [fpp] * 4 + [i32, f32] + [fpp] * 4
@@ -411,6 +437,240 @@ def diffattn_kv_append_paged(k1_new, k2_new, v_new, k1_pages, k2_pages, v_pages,
                "diffattn_kv_append_paged_fp8")
     else:
         _check(lib.diffattn_kv_append_paged(*args, _stream_ptr(stream)), "diffattn_kv_append_paged")
+
+
+# ------------------------------------------------------------------ rotary positions, ragged serving
+class RopePlan:
+    """A rotation as diffattn_rope and diffattn_kv_append_chunk_paged take it (made by rope_plan): the
+    frequency table on one device, kept for as long as the plan is."""
+
+    def __init__(self, freqs: torch.Tensor, rotary_dim: int, interleaved: bool, magnitude: float):
+        self.freqs, self.rotary_dim, self.interleaved, self.magnitude = freqs, rotary_dim, interleaved, magnitude
+        self._c = Rotation(freqs.data_ptr(), rotary_dim, int(interleaved), magnitude)
+
+    @property
+    def device(self):
+        return self.freqs.device
+
+
+_ROPE_SCALING = {"none": 0, "linear": 1, "ramp": 2}
+
+
+def rope_freqs(rotary_dim: int, base: float = 10000.0, scaling: str = "none", factor: float = 1.0,
+               original_length: int = 0, beta_fast: float = 32.0, beta_slow: float = 1.0):
+    """(table, magnitude) on the host: turns per position of each pair as 0.64 fixed-point values (an int64
+    tensor of the bits, [rotary_dim / 2]) and the factor of the rotated channels."""
+    if scaling not in _ROPE_SCALING:
+        raise ValueError("scaling must be 'none', 'linear' or 'ramp'")
+    table = torch.zeros(max(int(rotary_dim) // 2, 1), dtype=torch.int64)
+    magnitude = ctypes.c_float()
+    _check(load_library().diffattn_rope_freqs(int(rotary_dim), float(base), _ROPE_SCALING[scaling], float(factor),
+                                              int(original_length), float(beta_fast), float(beta_slow),
+                                              ctypes.c_void_p(table.data_ptr()), ctypes.byref(magnitude)),
+           "diffattn_rope_freqs")
+    return table, magnitude.value
+
+
+def rope_plan(rotary_dim: int, base: float = 10000.0, interleaved: bool = False, scaling: str = "none",
+              factor: float = 1.0, original_length: int = 0, beta_fast: float = 32.0, beta_slow: float = 1.0,
+              magnitude: float | None = None, device=None) -> RopePlan:
+    """A rotation of the first rotary_dim channels (a multiple of 8) of each query and key half: pair j turns by
+    base^(-2j / rotary_dim) per position. interleaved: pairs (2j, 2j + 1), else (j, j + rotary_dim / 2).
+    scaling: "none"; "linear" (frequencies / factor); "ramp" (pairs that turn fewer than beta_slow times in
+    original_length positions are interpolated by factor, those that turn more than beta_fast times are
+    not, and in between linearly; magnitude 0.1 ln(factor) + 1). magnitude overrides the factor of the
+    rotated channels. Made once and kept, like a weight."""
+    table, m = rope_freqs(rotary_dim, base, scaling, factor, original_length, beta_fast, beta_slow)
+    dev = torch.device("cuda", torch.cuda.current_device()) if device is None else torch.device(device)
+    return RopePlan(table.to(dev), int(rotary_dim), bool(interleaved), m if magnitude is None else float(magnitude))
+
+
+def _same_device(dev, *tensors):
+    for t in tensors:
+        if t is not None and t.device != dev:
+            raise ValueError("all tensors must be on one CUDA device")
+
+
+def _elsewhere(dev, stream):
+    """None when `dev` is the current device and no other stream is asked for; else a context that makes
+    both current, so that buffers are allocated on the stream that uses them."""
+    if dev.type != "cuda":
+        raise ValueError("all tensors must be on one CUDA device")
+    if stream is None and dev.index == torch.cuda.current_device():
+        return None
+    return torch.cuda.stream(stream if stream is not None else torch.cuda.current_stream(dev))
+
+
+def _int32(dev, shape, what, *tensors):
+    for t in tensors:
+        if t.dtype != torch.int32 or t.device != dev or not t.is_contiguous() or tuple(t.shape) != tuple(shape):
+            raise ValueError(f"{what} must be a contiguous int32 tensor of shape {list(shape)} on the operands' device")
+
+
+_serving_ws: dict = {}
+
+
+def _serving_workspace(nbytes: int, dev) -> torch.Tensor:
+    """Workspace of the current stream: kept per stream, so that calls on two streams share none. During
+    a graph capture a new one from the graph's own memory, so that two graphs share none either."""
+    capturing = torch.cuda.is_current_stream_capturing()
+    key = (dev.index, torch.cuda.current_stream(dev).cuda_stream)
+    buf = None if capturing else _serving_ws.get(key)
+    if buf is None or buf.numel() < nbytes:
+        buf = torch.empty(nbytes + 256, dtype=torch.uint8, device=dev)
+        buf = buf[(-buf.data_ptr()) % 256:]
+        buf[:256].zero_()  # the control block: the rest needs no initialisation
+        if not capturing:
+            _serving_ws[key] = buf
+    return buf
+
+
+def diffattn_rope(tensors, rope: RopePlan, positions=None, backward: bool = False, out=None, out_dtype=None,
+                  stream=None):
+    """Rotates up to four operands [B, H_i, N, d] of one dtype (Q1, Q2, K1, K2: last dimension contiguous,
+    any 16-byte strides) in one launch; with backward=True the transpose, which takes gradients of the
+    rotated operands to gradients of the operands. positions: int32 [B, N] or None (row n at position n).
+    out: tensors to write (the operands themselves rotate in place), else new ones of out_dtype (default:
+    the operands') in the operands' memory order. Returns them as a tuple."""
+    tensors = tuple(tensors)
+    x = tensors[0]
+    ctx = _elsewhere(x.device, stream)
+    if ctx is not None:
+        with ctx:
+            return diffattn_rope(tensors, rope, positions, backward, out, out_dtype)
+    dev = x.device
+    _same_device(dev, *tensors, rope.freqs)
+    if not 1 <= len(tensors) <= 4 or any(t.dim() != 4 for t in tensors):
+        raise ValueError("one to four operands [B, H, N, d]")
+    B, _, N, d = x.shape
+    if any(t.dtype != x.dtype or t.shape[0] != B or t.shape[2] != N or t.shape[3] != d for t in tensors):
+        raise ValueError("operands must share dtype, batch, rows and width")
+    if positions is not None:
+        _int32(dev, (B, N), "positions", positions)
+    if out is None:
+        out = tuple(torch.empty_like(t, dtype=out_dtype) for t in tensors)
+    else:
+        out = tuple(out)
+        _same_device(dev, *out)
+        if len(out) != len(tensors) or any(o.shape != t.shape or o.dtype != out[0].dtype for o, t in zip(out, tensors)):
+            raise ValueError("out must match the operands' shapes and share one dtype")
+        if out_dtype is not None and out_dtype != out[0].dtype:
+            raise ValueError("out_dtype does not match out")
+    n = len(tensors)
+    arr, heads = Tensor4 * n, (ctypes.c_int * n)(*(t.shape[1] for t in tensors))
+    _check(load_library().diffattn_rope(arr(*(_t4(t) for t in tensors)), arr(*(_t4(t) for t in out)), heads, n,
+                                        None if positions is None else positions.data_ptr(), B, N, d,
+                                        ctypes.byref(rope._c), int(bool(backward)), _dtype_code(x.dtype),
+                                        _dtype_code(out[0].dtype), torch.cuda.current_stream(dev).cuda_stream),
+           "diffattn_rope")
+    return out
+
+
+def _t3(t: torch.Tensor) -> Tensor4:
+    """[T, H, width] rows with a contiguous last dimension -> diffattn_tensor (stride_b unused)."""
+    if t.dim() != 3 or t.stride(2) != 1:
+        raise ValueError("ragged rows must be [T, H, width] with a contiguous last dimension")
+    return Tensor4(t.data_ptr(), 0, t.stride(1), t.stride(0))
+
+
+def _paged_args(dev, pages, block_table, q_start, seq_lens, scales):
+    k1, k2, v = pages
+    fp8 = _is_fp8(k1)
+    if fp8 != (scales is not None) or any(_is_fp8(t) != fp8 for t in (k2, v)):
+        raise ValueError("fp8 pages (all three) go with scales, bf16 pages without")
+    if not fp8 and any(t.dtype != torch.bfloat16 for t in pages):
+        raise ValueError("pages must be bf16 or fp8 (e4m3)")
+    _same_device(dev, *pages)
+    if any(t.dim() != 4 or t.shape[2] != 64 or t.shape[:2] != k1.shape[:2] for t in pages) or k1.shape != k2.shape:
+        raise ValueError("pages must be [num_pages, H_kv, 64, width] with common pages and heads")
+    B = seq_lens.shape[0]
+    _int32(dev, (B,), "seq_lens", seq_lens)
+    _int32(dev, (B + 1,), "q_start", q_start)
+    if block_table.dim() != 2:
+        raise ValueError("block_table must be [B, max_pages]")
+    _int32(dev, (B, block_table.shape[1]), "block_table", block_table)
+    return fp8, B
+
+
+def diffattn_kv_append_chunk_paged(k1_new, k2_new, v_new, k1_pages, k2_pages, v_pages, block_table, q_start, seq_lens,
+                                   rope: RopePlan | None = None, scales=None, stream=None) -> None:
+    """Writes the new tokens of many sequences ([T, H_kv, *] bf16 or fp16 rows, sequence b's are
+    q_start[b] .. q_start[b + 1] - 1 and the last of its seq_lens[b] tokens) into the paged cache (pages
+    [num_pages, H_kv, 64, *], block_table [B, max_pages]), K1 and K2 rotated by `rope` at their positions.
+    fp8 pages take scales = (k1_scale, k2_scale, v_scale) and store e4m3(x / scale)."""
+    dev = k1_new.device
+    ctx = _elsewhere(dev, stream)
+    if ctx is not None:
+        with ctx:
+            return diffattn_kv_append_chunk_paged(k1_new, k2_new, v_new, k1_pages, k2_pages, v_pages, block_table,
+                                                  q_start, seq_lens, rope, scales)
+    fp8, B = _paged_args(dev, (k1_pages, k2_pages, v_pages), block_table, q_start, seq_lens, scales)
+    _same_device(dev, k1_new, k2_new, v_new, None if rope is None else rope.freqs)
+    T, Hk, d = k1_new.shape
+    Dv = v_new.shape[2]
+    if k2_new.shape != k1_new.shape or v_new.shape[:2] != (T, Hk) or any(t.dtype != k1_new.dtype for t in (k2_new, v_new)):
+        raise ValueError("k1_new, k2_new [T, H_kv, d] and v_new [T, H_kv, Dv] of one dtype")
+    if k1_pages.shape[1] != Hk or k1_pages.shape[3] != d or v_pages.shape[3] != Dv:
+        raise ValueError("the pages' heads and widths must be the new rows'")
+    lib, args = load_library(), (_t3(k1_new), _t3(k2_new), _t3(v_new), _dtype_code(k1_new.dtype), _t4(k1_pages),
+                                 _t4(k2_pages), _t4(v_pages), block_table.data_ptr(), block_table.shape[1],
+                                 k1_pages.shape[0], q_start.data_ptr(), seq_lens.data_ptr(),
+                                 None if rope is None else ctypes.byref(rope._c), T, B, Hk, d, Dv)
+    st = torch.cuda.current_stream(dev).cuda_stream
+    if fp8:
+        _check(lib.diffattn_kv_append_chunk_paged_fp8(*args, *scales, st), "diffattn_kv_append_chunk_paged_fp8")
+    else:
+        _check(lib.diffattn_kv_append_chunk_paged(*args, st), "diffattn_kv_append_chunk_paged")
+
+
+def chunk_workspace_bytes(T, B, H, kv_group, L, d, Dv) -> int:
+    n = ctypes.c_size_t()
+    _check(load_library().diffattn_chunk_workspace_size(T, B, H, kv_group, L, d, Dv, ctypes.byref(n)),
+           "diffattn_chunk_workspace_size")
+    return n.value
+
+
+def diffattn_chunk_paged(q1, q2, k1_pages, k2_pages, v_pages, block_table, q_start, seq_lens, lam: float, lam_init: float,
+                         L: int, kv_group: int = 1, eps: float = 1e-5, norm_weight=None, out_dtype=torch.float32, out=None,
+                         ws=None, stream=None, scales=None) -> torch.Tensor:
+    """Differential attention of the new tokens of many sequences over a paged cache that already holds
+    them. q1, q2: [T, H, d] bf16 rows, sequence b's q_start[b] .. q_start[b + 1] - 1, the last of its
+    seq_lens[b] tokens; each sees its sequence up to itself. Pages, block_table, kv_group and scales as for
+    diffattn_decode_paged; L = the largest length. Returns [T, H, Dv]; rows of no sequence are left as
+    they are. Calls on different streams use workspaces of their own unless `ws` is given."""
+    dev = q1.device
+    ctx = _elsewhere(dev, stream)
+    if ctx is not None:
+        with ctx:
+            return diffattn_chunk_paged(q1, q2, k1_pages, k2_pages, v_pages, block_table, q_start, seq_lens, lam, lam_init, L,
+                                        kv_group, eps, norm_weight, out_dtype, out, ws, None, scales)
+    fp8, B = _paged_args(dev, (k1_pages, k2_pages, v_pages), block_table, q_start, seq_lens, scales)
+    _same_device(dev, q1, q2, norm_weight, out)
+    T, H, d = q1.shape
+    Dv = v_pages.shape[3]
+    if q2.shape != q1.shape or q1.dtype != torch.bfloat16 or q2.dtype != torch.bfloat16:
+        raise ValueError("q1 and q2 must be [T, H, d] bf16 tensors of one shape")
+    if k1_pages.shape[1] * kv_group != H or k1_pages.shape[3] != d:
+        raise ValueError("the pages must have H / kv_group heads of the query's width")
+    if norm_weight is not None and (norm_weight.dtype != torch.float32 or norm_weight.shape != (Dv,)
+                                    or not norm_weight.is_contiguous()):
+        raise ValueError("norm_weight must be a contiguous fp32 [Dv] tensor")
+    if out is None:
+        out = torch.empty((T, H, Dv), dtype=out_dtype, device=dev)
+    elif out.shape != (T, H, Dv) or not out.is_contiguous():
+        raise ValueError("out must be a contiguous [T, H, Dv] tensor")
+    if ws is None:
+        ws = _serving_workspace(chunk_workspace_bytes(T, B, H, kv_group, L, d, Dv), dev)
+    args = (_t3(q1), _t3(q2), _t4(k1_pages), _t4(k2_pages), _t4(v_pages), block_table.data_ptr(), block_table.shape[1],
+            k1_pages.shape[0], q_start.data_ptr(), seq_lens.data_ptr(), L, out.data_ptr(),
+            None if norm_weight is None else norm_weight.data_ptr(), T, B, H, kv_group, d, Dv, lam, lam_init, eps)
+    tail = (_dtype_code(out.dtype), ws.data_ptr(), ws.numel(), torch.cuda.current_stream(dev).cuda_stream)
+    lib = load_library()
+    if fp8:
+        _check(lib.diffattn_chunk_paged_fp8(*args, *scales, *tail), "diffattn_chunk_paged_fp8")
+    else:
+        _check(lib.diffattn_chunk_paged(*args, *tail), "diffattn_chunk_paged")
+    return out
 
 
 def add_rmsnorm(x, z=None, weight=None, eps: float = 1e-5, want_y: bool = False, want_n: bool = True,

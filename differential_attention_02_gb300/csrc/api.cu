@@ -804,6 +804,319 @@ diffattn_status diffattn_decode_paged_fp8(const void* q1, const void* q2, diffat
                         out_dtype, workspace, workspace_bytes, stream);
 }
 
+// ---------------------------------------------------------------- rotary positions
+diffattn_status diffattn_rope_freqs(int rotary_dim, double base, int scaling, double factor, int original_length,
+                                    double beta_fast, double beta_slow, uint64_t* freqs, float* magnitude) {
+    if (!freqs || !magnitude || rotary_dim < 8 || rotary_dim % 8 || !(base >= 1.0) || !std::isfinite(base))
+        return DIFFATTN_ERR_INVALID_ARG;
+    if (scaling != DIFFATTN_ROPE_PLAIN && scaling != DIFFATTN_ROPE_LINEAR && scaling != DIFFATTN_ROPE_RAMP)
+        return DIFFATTN_ERR_INVALID_ARG;
+    if (scaling != DIFFATTN_ROPE_PLAIN && (!(factor >= 1.0) || !std::isfinite(factor))) return DIFFATTN_ERR_INVALID_ARG;
+    if (scaling == DIFFATTN_ROPE_RAMP &&
+        (original_length < 1 || !(beta_slow >= 0.0) || !(beta_fast > beta_slow) || !std::isfinite(beta_fast)))
+        return DIFFATTN_ERR_INVALID_ARG;
+    const double two_pi = 6.283185307179586476925;
+    for (int j = 0; j < rotary_dim / 2; ++j) {
+        double f = pow(base, -2.0 * j / rotary_dim);  // radians per position, in (0, 1]
+        if (scaling == DIFFATTN_ROPE_LINEAR) f /= factor;
+        if (scaling == DIFFATTN_ROPE_RAMP) {
+            const double turns = original_length * f / two_pi;
+            const double g = std::min(1.0, std::max(0.0, (turns - beta_slow) / (beta_fast - beta_slow)));
+            f = f / factor * (1.0 - g) + f * g;
+        }
+        freqs[j] = (uint64_t)(f / two_pi * 0x1p64);  // below 2^62: f <= 1
+    }
+    *magnitude = scaling == DIFFATTN_ROPE_RAMP ? (float)(0.1 * log(factor) + 1.0) : 1.f;
+    return DIFFATTN_OK;
+}
+
+}  // extern "C"
+
+namespace {
+// The rotation's arguments against a row width; fills the kernels' table.
+bool check_rotation(const diffattn_rotation& r, int d, RopeTable* t) {
+    if (r.rotary_dim < 8 || r.rotary_dim % 8 || r.rotary_dim > d || !std::isfinite(r.magnitude)) return false;
+    if (r.freqs == nullptr || (reinterpret_cast<uintptr_t>(r.freqs) & 7u)) return false;
+    t->freqs = r.freqs;
+    t->rotary = r.rotary_dim;
+    t->interleaved = r.interleaved != 0;
+    t->magnitude = r.magnitude;
+    return true;
+}
+}  // namespace
+
+extern "C" {
+
+diffattn_status diffattn_rope(const diffattn_tensor* in, const diffattn_tensor* out, const int* heads, int count,
+                              const int32_t* positions, int B, int N, int d, const diffattn_rotation* rotation,
+                              int backward, int in_dtype, int out_dtype, void* stream) {
+    if (!in || !out || !heads || !rotation || count < 1 || count > 4 || B < 0 || N < 0 || d < 8 || d % 8 || d > 256)
+        return DIFFATTN_ERR_INVALID_ARG;
+    for (int dt : {in_dtype, out_dtype})
+        if (dt != DIFFATTN_F32 && dt != DIFFATTN_BF16 && dt != DIFFATTN_F16) return DIFFATTN_ERR_INVALID_ARG;
+    RopeParams p{};
+    if (!check_rotation(*rotation, d, &p.table)) return DIFFATTN_ERR_INVALID_ARG;
+    int64_t rows = 0;
+    for (int i = 0; i < count; ++i) {
+        if (heads[i] < 0) return DIFFATTN_ERR_INVALID_ARG;
+        rows += heads[i];
+    }
+    if (rows > INT32_MAX / 2 || (int64_t)B * N > INT32_MAX) return DIFFATTN_ERR_INVALID_ARG;
+    if (B == 0 || N == 0 || rows == 0) return DIFFATTN_OK;
+    for (int i = 0; i < count; ++i) {
+        p.heads[i] = heads[i];
+        if (heads[i] == 0) continue;
+        if (!check_operand(in[i], d, in_dtype == DIFFATTN_F32 ? 4 : 2) ||
+            !check_operand(out[i], d, out_dtype == DIFFATTN_F32 ? 4 : 2))
+            return DIFFATTN_ERR_INVALID_ARG;
+        const bool in_place = in[i].ptr == out[i].ptr;
+        if (in_place && (in_dtype != out_dtype || in[i].stride_b != out[i].stride_b || in[i].stride_h != out[i].stride_h ||
+                         in[i].stride_n != out[i].stride_n))
+            return DIFFATTN_ERR_INVALID_ARG;
+        p.in[i] = in[i].ptr;
+        p.out[i] = const_cast<void*>(out[i].ptr);
+        p.in_stride[i][0] = in[i].stride_b; p.in_stride[i][1] = in[i].stride_h; p.in_stride[i][2] = in[i].stride_n;
+        p.out_stride[i][0] = out[i].stride_b; p.out_stride[i][1] = out[i].stride_h; p.out_stride[i][2] = out[i].stride_n;
+    }
+    p.rows = (int)rows;
+    p.positions = positions;
+    p.B = B; p.N = N; p.d = d;
+    p.in_dtype = in_dtype == DIFFATTN_F32 ? 0 : in_dtype == DIFFATTN_BF16 ? 1 : 2;
+    p.out_dtype = out_dtype == DIFFATTN_F32 ? 0 : out_dtype == DIFFATTN_BF16 ? 1 : 2;
+    p.backward = backward != 0;
+    return cuda_status(launch_rope(p, static_cast<cudaStream_t>(stream)));
+}
+
+}  // extern "C"
+
+namespace {
+diffattn_status append_chunk(bool fp8, const float* scales, diffattn_tensor k1_new, diffattn_tensor k2_new,
+                             diffattn_tensor v_new, int in_dtype, diffattn_tensor k1_pages, diffattn_tensor k2_pages,
+                             diffattn_tensor v_pages, const int32_t* block_table, int max_pages, int num_pages,
+                             const int32_t* q_start, const int32_t* seq_lens, const diffattn_rotation* rotation, int T,
+                             int B, int H_kv, int d, int Dv, void* stream) {
+    if (T < 0 || B < 0 || H_kv < 0 || d < 8 || Dv < 8 || d % 8 || Dv % 8 || max_pages < 1 || num_pages < 1)
+        return DIFFATTN_ERR_INVALID_ARG;
+    if (in_dtype != DIFFATTN_BF16 && in_dtype != DIFFATTN_F16) return DIFFATTN_ERR_INVALID_ARG;
+    if (fp8 && !(valid_scale(scales[0]) && valid_scale(scales[1]) && valid_scale(scales[2])))
+        return DIFFATTN_ERR_INVALID_ARG;
+    AppendChunkParams p{};
+    if (rotation != nullptr && !check_rotation(*rotation, d, &p.table)) return DIFFATTN_ERR_INVALID_ARG;
+    if (T == 0 || B == 0 || H_kv == 0) return DIFFATTN_OK;
+    if (!block_table || !q_start || !seq_lens) return DIFFATTN_ERR_INVALID_ARG;
+    const diffattn_tensor in[3] = {k1_new, k2_new, v_new}, pages[3] = {k1_pages, k2_pages, v_pages};
+    for (int i = 0; i < 3; ++i) {
+        const int w = i == 2 ? Dv : d;
+        if (!check_operand(in[i], w, 2) || !check_operand(pages[i], w, fp8 ? 1 : 2)) return DIFFATTN_ERR_INVALID_ARG;
+        p.in[i] = in[i].ptr;
+        p.in_stride_t[i] = in[i].stride_n;
+        p.in_stride_h[i] = in[i].stride_h;
+        p.pages[i] = const_cast<void*>(pages[i].ptr);
+        p.page_stride[i] = pages[i].stride_b;
+        p.head_stride[i] = pages[i].stride_h;
+        p.row_stride[i] = pages[i].stride_n;
+        p.scale[i] = fp8 ? scales[i] : 1.f;
+    }
+    p.block_table = block_table;
+    p.q_start = q_start;
+    p.seq_lens = seq_lens;
+    p.max_pages = max_pages; p.num_pages = num_pages;
+    p.T = T; p.B = B; p.H_kv = H_kv; p.d = d; p.Dv = Dv;
+    p.in_f16 = in_dtype == DIFFATTN_F16;
+    p.fp8 = fp8;
+    return cuda_status(launch_append_chunk(p, static_cast<cudaStream_t>(stream)));
+}
+}  // namespace
+
+extern "C" {
+
+diffattn_status diffattn_kv_append_chunk_paged(diffattn_tensor k1_new, diffattn_tensor k2_new, diffattn_tensor v_new,
+                                               int in_dtype, diffattn_tensor k1_pages, diffattn_tensor k2_pages,
+                                               diffattn_tensor v_pages, const int32_t* block_table, int max_pages,
+                                               int num_pages, const int32_t* q_start, const int32_t* seq_lens,
+                                               const diffattn_rotation* rotation, int T, int B, int H_kv, int d, int Dv,
+                                               void* stream) {
+    return append_chunk(false, nullptr, k1_new, k2_new, v_new, in_dtype, k1_pages, k2_pages, v_pages, block_table,
+                        max_pages, num_pages, q_start, seq_lens, rotation, T, B, H_kv, d, Dv, stream);
+}
+
+diffattn_status diffattn_kv_append_chunk_paged_fp8(diffattn_tensor k1_new, diffattn_tensor k2_new,
+                                                   diffattn_tensor v_new, int in_dtype, diffattn_tensor k1_pages,
+                                                   diffattn_tensor k2_pages, diffattn_tensor v_pages,
+                                                   const int32_t* block_table, int max_pages, int num_pages,
+                                                   const int32_t* q_start, const int32_t* seq_lens,
+                                                   const diffattn_rotation* rotation, int T, int B, int H_kv, int d,
+                                                   int Dv, float k1_scale, float k2_scale, float v_scale, void* stream) {
+    const float scales[3] = {k1_scale, k2_scale, v_scale};
+    return append_chunk(true, scales, k1_new, k2_new, v_new, in_dtype, k1_pages, k2_pages, v_pages, block_table,
+                        max_pages, num_pages, q_start, seq_lens, rotation, T, B, H_kv, d, Dv, stream);
+}
+
+}  // extern "C"
+
+namespace {
+// Bounds of the plan's lists and the workspace regions of the chunk attention. They follow from
+// the sizes alone (chunk_plan.cu gives the argument), whatever the lengths on the device.
+struct ChunkLayout {
+    int tm, rows, ctas, max_tiles, max_entries, max_slots, max_merges;
+    size_t tiles, entries, merges, stats, o, total;
+};
+bool chunk_layout(int B, int H, int kv_group, int T, int L, int d, int Dv, ChunkLayout* l) {
+    const int64_t H_kv = H / kv_group;
+    const int n_sm = device_sm_count();
+    const int sms = n_sm > 0 ? n_sm : 152;
+    l->ctas = d == 64 ? sms : sms / 2;  // one CTA per SM; a pair per work item for the wide heads
+    l->tm = kChunkRows / kv_group;
+    l->rows = std::min(l->tm, T) * kv_group;
+    const int64_t tiles = (int64_t)T / l->tm + std::min(B, T);
+    // Splitting needs a tile of at least two key tiles.
+    const int64_t extra = L > kChunkKeys ? (2 * l->ctas + H_kv - 1) / H_kv : 0;
+    const int64_t entries = tiles + extra;
+    if (entries * H_kv * 2 > INT32_MAX) return false;
+    l->max_tiles = (int)tiles;
+    l->max_entries = (int)entries;
+    l->max_slots = (int)(2 * extra);
+    l->max_merges = (int)extra;
+    l->tiles = round256(kControlBytes + sizeof(ChunkPlan));
+    l->entries = l->tiles + round256(tiles * sizeof(ChunkTile));
+    l->merges = l->entries + round256(entries * sizeof(ChunkEntry));
+    l->stats = l->merges + round256(extra * sizeof(ChunkMerge));
+    const size_t states = (size_t)l->max_slots * H_kv * 2 * l->rows;
+    l->o = l->stats + round256(states * 2 * sizeof(float));
+    l->total = l->o + round256(states * Dv * sizeof(float));
+    return true;
+}
+
+// 4-D map over the query halves, [H_kv][T][group][d]: boxes of 64 channels x group x tm tokens.
+bool encode_chunk_q(CUtensorMap* m, const diffattn_tensor& q, int d, int H_kv, int group, int T, int tm) {
+    auto enc = tensor_map_encoder();
+    if (!enc) return false;
+    // Strides of size-1 dimensions are never used: any valid one will do.
+    const int64_t sh = group > 1 || H_kv > 1 ? q.stride_h : d, sn = T > 1 ? q.stride_n : (int64_t)d * group;
+    cuuint64_t dims[4] = {(cuuint64_t)d, (cuuint64_t)group, (cuuint64_t)T, (cuuint64_t)H_kv};
+    cuuint64_t strides[3] = {(cuuint64_t)(sh * 2), (cuuint64_t)(sn * 2), (cuuint64_t)(sh * group * 2)};
+    cuuint32_t box[4] = {64, (cuuint32_t)group, (cuuint32_t)tm, 1};
+    cuuint32_t es[4] = {1, 1, 1, 1};
+    return enc(m, CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, 4, const_cast<void*>(q.ptr), dims, strides, box, es,
+               CU_TENSOR_MAP_INTERLEAVE_NONE, CU_TENSOR_MAP_SWIZZLE_128B, CU_TENSOR_MAP_L2_PROMOTION_L2_256B,
+               CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
+}
+
+diffattn_status chunk_paged(bool fp8, const float* scales, diffattn_tensor q1, diffattn_tensor q2,
+                            diffattn_tensor k1_pages, diffattn_tensor k2_pages, diffattn_tensor v_pages,
+                            const int32_t* block_table, int max_pages, int num_pages, const int32_t* q_start,
+                            const int32_t* seq_lens, int L, void* out, const float* norm_weight, int T, int B, int H,
+                            int kv_group, int d, int Dv, float lambda, float lambda_init, float eps, int out_dtype,
+                            void* workspace, size_t workspace_bytes, void* stream) {
+    if (T < 0 || B < 0 || H < 0 || L < 1 || d < 1 || Dv < 1 || kv_group < 1 || max_pages < 1 || num_pages < 1)
+        return DIFFATTN_ERR_INVALID_ARG;
+    if (out_dtype != DIFFATTN_F32 && out_dtype != DIFFATTN_BF16 && out_dtype != DIFFATTN_F16)
+        return DIFFATTN_ERR_INVALID_ARG;
+    if (!isfinite(lambda) || !isfinite(lambda_init) || !(eps >= 0.f) || !isfinite(eps)) return DIFFATTN_ERR_INVALID_ARG;
+    if (fp8 && !(valid_scale(scales[0]) && valid_scale(scales[1]) && valid_scale(scales[2])))
+        return DIFFATTN_ERR_INVALID_ARG;
+    if (T == 0 || B == 0 || H == 0) return DIFFATTN_OK;
+    if (H % kv_group != 0 || L > (int64_t)64 * max_pages) return DIFFATTN_ERR_INVALID_ARG;
+    if (!out || !aligned16(out) || !block_table || !q_start || !seq_lens) return DIFFATTN_ERR_INVALID_ARG;
+    if (!check_operand(q1, d, 2) || !check_operand(q2, d, 2)) return DIFFATTN_ERR_INVALID_ARG;
+    const int eb = fp8 ? 1 : 2;
+    if (!check_operand(k1_pages, d, eb) || !check_operand(k2_pages, d, eb) || !check_operand(v_pages, Dv, eb))
+        return DIFFATTN_ERR_INVALID_ARG;
+    if (norm_weight != nullptr && !aligned16(norm_weight)) return DIFFATTN_ERR_INVALID_ARG;
+    if (!((d == 64 && Dv == 128) || (d == 128 && Dv == 256)) || kv_group > kChunkRows) return DIFFATTN_ERR_UNSUPPORTED;
+    ChunkLayout l;
+    if (!chunk_layout(B, H, kv_group, T, L, d, Dv, &l)) return DIFFATTN_ERR_UNSUPPORTED;
+    if (workspace == nullptr || workspace_bytes < l.total || (reinterpret_cast<uintptr_t>(workspace) & 255u))
+        return DIFFATTN_ERR_WORKSPACE;
+    const int H_kv = H / kv_group;
+    ChunkParams p{};
+    bool ok = encode_chunk_q(&p.tm_q1, q1, d, H_kv, kv_group, T, l.tm) &&
+              encode_chunk_q(&p.tm_q2, q2, d, H_kv, kv_group, T, l.tm);
+    if (fp8) {  // raw rows, converted in the kernel
+        const CUtensorMapDataType u8 = CU_TENSOR_MAP_DATA_TYPE_UINT8;
+        const CUtensorMapSwizzle none = CU_TENSOR_MAP_SWIZZLE_NONE;
+        ok = ok && encode_4d(&p.tm_k1, k1_pages, d, 64, H_kv, num_pages, d, 64, none, u8) &&
+             encode_4d(&p.tm_k2, k2_pages, d, 64, H_kv, num_pages, d, 64, none, u8) &&
+             encode_4d(&p.tm_v, v_pages, Dv, 64, H_kv, num_pages, Dv, 64, none, u8);
+    } else {
+        const CUtensorMapSwizzle sw = CU_TENSOR_MAP_SWIZZLE_128B;
+        ok = ok && encode_4d(&p.tm_k1, k1_pages, d, 64, H_kv, num_pages, 64, 64, sw) &&
+             encode_4d(&p.tm_k2, k2_pages, d, 64, H_kv, num_pages, 64, 64, sw) &&
+             encode_4d(&p.tm_v, v_pages, Dv, 64, H_kv, num_pages, 64, 64, sw);
+    }
+    if (!ok) return DIFFATTN_ERR_INVALID_ARG;
+    p.block_table = block_table;
+    p.q_start = q_start;
+    p.seq_lens = seq_lens;
+    p.max_pages = max_pages; p.num_pages = num_pages;
+    p.T = T; p.B = B; p.H = H; p.H_kv = H_kv; p.group = kv_group; p.tm = l.tm; p.d = d; p.Dv = Dv; p.L = L;
+    p.kv_fp8 = fp8;
+    p.out = out;
+    p.out_bf16 = out_dtype == DIFFATTN_BF16;
+    p.out_f16 = out_dtype == DIFFATTN_F16;
+    p.norm_w = norm_weight;
+    p.lambda = lambda; p.lambda_init = lambda_init; p.eps = eps;
+    const double sl2 = 1.4426950408889634 / sqrt((double)d);
+    p.scale1_log2 = (float)(sl2 * (fp8 ? scales[0] : 1.f));
+    p.scale2_log2 = (float)(sl2 * (fp8 ? scales[1] : 1.f));
+    p.v_scale = fp8 ? scales[2] : 1.f;
+    uint8_t* ws = static_cast<uint8_t*>(workspace);
+    p.err = err_word(workspace);
+    p.plan = reinterpret_cast<ChunkPlan*>(ws + kControlBytes);
+    p.tiles = reinterpret_cast<ChunkTile*>(ws + l.tiles);
+    p.entries = reinterpret_cast<ChunkEntry*>(ws + l.entries);
+    p.merges = reinterpret_cast<ChunkMerge*>(ws + l.merges);
+    p.part_stats = reinterpret_cast<float*>(ws + l.stats);
+    p.part_o = reinterpret_cast<float*>(ws + l.o);
+    p.max_tiles = l.max_tiles; p.max_entries = l.max_entries; p.max_slots = l.max_slots; p.max_merges = l.max_merges;
+    p.rows = l.rows;
+    p.ctas = l.ctas;
+    cudaStream_t st = static_cast<cudaStream_t>(stream);
+    cudaError_t e = launch_chunk_plan(p, st);
+    if (e == cudaSuccess) e = d == 64 ? launch_chunk_64(p, st) : launch_chunk_pair(p, st);
+    if (e == cudaSuccess && p.max_merges > 0) e = launch_chunk_merge(p, st);
+    return cuda_status(e);
+}
+}  // namespace
+
+extern "C" {
+
+diffattn_status diffattn_chunk_workspace_size(int T, int B, int H, int kv_group, int L, int d, int Dv, size_t* bytes) {
+    if (!bytes || T < 0 || B < 0 || H < 0 || L < 1 || d < 1 || Dv < 1 || kv_group < 1) return DIFFATTN_ERR_INVALID_ARG;
+    *bytes = kControlBytes;
+    if (T == 0 || B == 0 || H == 0) return DIFFATTN_OK;
+    if (H % kv_group != 0) return DIFFATTN_ERR_INVALID_ARG;
+    if (kv_group > kChunkRows) return DIFFATTN_ERR_UNSUPPORTED;
+    ChunkLayout l;
+    if (!chunk_layout(B, H, kv_group, T, L, d, Dv, &l)) return DIFFATTN_ERR_UNSUPPORTED;
+    *bytes = l.total;
+    return DIFFATTN_OK;
+}
+
+diffattn_status diffattn_chunk_paged(diffattn_tensor q1, diffattn_tensor q2, diffattn_tensor k1_pages,
+                                     diffattn_tensor k2_pages, diffattn_tensor v_pages, const int32_t* block_table,
+                                     int max_pages, int num_pages, const int32_t* q_start, const int32_t* seq_lens, int L,
+                                     void* out, const float* norm_weight, int T, int B, int H, int kv_group, int d, int Dv,
+                                     float lambda, float lambda_init, float eps, int out_dtype, void* workspace,
+                                     size_t workspace_bytes, void* stream) {
+    return chunk_paged(false, nullptr, q1, q2, k1_pages, k2_pages, v_pages, block_table, max_pages, num_pages, q_start,
+                       seq_lens, L, out, norm_weight, T, B, H, kv_group, d, Dv, lambda, lambda_init, eps, out_dtype,
+                       workspace, workspace_bytes, stream);
+}
+
+diffattn_status diffattn_chunk_paged_fp8(diffattn_tensor q1, diffattn_tensor q2, diffattn_tensor k1_pages,
+                                         diffattn_tensor k2_pages, diffattn_tensor v_pages, const int32_t* block_table,
+                                         int max_pages, int num_pages, const int32_t* q_start, const int32_t* seq_lens,
+                                         int L, void* out, const float* norm_weight, int T, int B, int H, int kv_group,
+                                         int d, int Dv, float lambda, float lambda_init, float eps, float k1_scale,
+                                         float k2_scale, float v_scale, int out_dtype, void* workspace,
+                                         size_t workspace_bytes, void* stream) {
+    const float scales[3] = {k1_scale, k2_scale, v_scale};
+    return chunk_paged(true, scales, q1, q2, k1_pages, k2_pages, v_pages, block_table, max_pages, num_pages, q_start,
+                       seq_lens, L, out, norm_weight, T, B, H, kv_group, d, Dv, lambda, lambda_init, eps, out_dtype,
+                       workspace, workspace_bytes, stream);
+}
+
 // ---------------------------------------------------------------- decode without caller workspace
 // Scratch for diffattn_decode_noalloc: error word, then the split partial
 // states, exactly as in a diffattn_decode workspace. Host code must not use the

@@ -103,6 +103,86 @@ struct KvAppendParams {
 };
 cudaError_t launch_kv_append_paged(const KvAppendParams& p, cudaStream_t stream);
 
+// Rotary positions: angle of pair j at position p = p * freqs[j] (0.64 fixed-point turns).
+struct RopeTable {
+    const uint64_t* freqs;  // [rotary / 2]
+    int rotary;             // rotated channels (the first ones of a row), a multiple of 8; 0 = no rotation
+    int interleaved;        // pairs (2j, 2j + 1), else (j, j + rotary / 2)
+    float magnitude;
+};
+struct RopeParams {
+    const void* in[4];  // [B, heads, N, d] each; dtypes 0 fp32, 1 bf16, 2 fp16
+    void* out[4];
+    int64_t in_stride[4][3], out_stride[4][3];  // b, h, n strides in elements
+    int heads[4], rows;                         // heads of each operand (0: none) and their sum
+    const int32_t* positions;                   // [B, N], or null: position n
+    int B, N, d, in_dtype, out_dtype, backward;
+    RopeTable table;
+};
+cudaError_t launch_rope(const RopeParams& p, cudaStream_t stream);
+struct AppendChunkParams {
+    const void* in[3];                                     // K1, K2 [T, H_kv, d] and V [T, H_kv, Dv], bf16 or fp16 (in_f16)
+    int64_t in_stride_t[3], in_stride_h[3];                // elements
+    void* pages[3];                                        // [pages, H_kv, 64, width], bf16 or e4m3 (fp8)
+    int64_t page_stride[3], head_stride[3], row_stride[3];  // elements
+    const int32_t *block_table, *q_start, *seq_lens;       // [B][max_pages], [B + 1], [B]
+    int max_pages, num_pages, T, B, H_kv, d, Dv, in_f16, fp8;
+    float scale[3];                                        // cache value = stored value * scale
+    RopeTable table;                                       // rotation of K1 and K2 (rotary 0: none)
+    int head_splits;                                       // warps per token, set by the launcher
+};
+cudaError_t launch_append_chunk(AppendChunkParams p, cudaStream_t stream);
+
+// Attention of ragged new tokens over a paged cache (chunk_plan.cu, chunk_tcgen05.cu, chunk_pair_tcgen05.cu).
+//
+// A tile is up to 128 query rows of one sequence: `tm` consecutive tokens x the `group` query
+// heads that share one KV head. An entry is a tile and a range of its key tiles (128 keys each);
+// every entry stands for H_kv work items, one per KV head. A tile whose keys are split over
+// several entries leaves partial states in slots, which the merge kernel joins.
+struct ChunkTile {
+    int b, t0, ntok, pos0;  // sequence, first token row, tokens, position of the first token (may be negative)
+};
+struct ChunkEntry {
+    ChunkTile tile;
+    int kt0, nkt;  // key tiles [kt0, kt0 + nkt)
+    int slot;      // partial-state slot, or -1: the entry finishes its tile
+    int pad;
+};
+struct ChunkMerge {
+    ChunkTile tile;
+    int slot, count;  // slots [slot, slot + count)
+    int pad[2];
+};
+struct ChunkPlan {
+    int tiles, entries, merges, keys_per_entry;
+};
+struct ChunkParams {
+    CUtensorMap tm_q1, tm_q2;        // 4-D maps [H_kv][T][group][d], boxes of 64 channels x group x tm
+    CUtensorMap tm_k1, tm_k2, tm_v;  // 4-D maps [pages][H_kv][64][width]
+    const int32_t *block_table, *q_start, *seq_lens;
+    int max_pages, num_pages, T, B, H, H_kv, group, tm, d, Dv, L, kv_fp8;
+    void* out;  // [T, H, Dv]
+    int out_bf16, out_f16;
+    const float* norm_w;
+    float lambda, lambda_init, eps;
+    float scale1_log2, scale2_log2, v_scale;  // score scales of the maps in log2 units (times the K scales); V's scale
+    int32_t* err;
+    // Plan and partial states in the workspace, and their host-known bounds.
+    ChunkPlan* plan;
+    ChunkTile* tiles;
+    ChunkEntry* entries;
+    ChunkMerge* merges;
+    float* part_stats;  // [slot][H_kv][2][rows][2]: running max (log2 units) and sum of each map
+    float* part_o;      // [slot][H_kv][2][Dv / 4][rows][4]
+    int max_tiles, max_entries, max_slots, max_merges, rows, ctas;  // ctas: work items that run at once
+};
+constexpr int kChunkRows = 128, kChunkKeys = 128;
+constexpr float kChunkNoMax = -1e30f;  // running maximum (log2 units) of a row that has seen no key
+cudaError_t launch_chunk_plan(const ChunkParams& p, cudaStream_t stream);
+cudaError_t launch_chunk_64(const ChunkParams& p, cudaStream_t stream);     // d = 64, Dv = 128
+cudaError_t launch_chunk_pair(const ChunkParams& p, cudaStream_t stream);   // d = 128, Dv = 256
+cudaError_t launch_chunk_merge(const ChunkParams& p, cudaStream_t stream);
+
 struct AddNormParams {
     const void* x;        // [M, N] bf16 or fp32 (x_f32)
     int x_f32;

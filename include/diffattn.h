@@ -320,6 +320,145 @@ diffattn_status diffattn_kv_append_paged_fp8(const void* k1_new, const void* k2_
                                              float k1_scale, float k2_scale, float v_scale, void* stream);
 
 /*
+ * Rotary positions. The pages take Q and K as given; the rotation is what a model
+ * applies to them first, so each query and key half is rotated here like a head of
+ * width d. Pair j of a row at position p is turned by the angle p f_j and multiplied
+ * by the magnitude m: (a, b) -> m (a cos - b sin, a sin + b cos). The first rotary_dim
+ * channels of a row take part, paired (2j, 2j + 1) when interleaved, else
+ * (j, j + rotary_dim / 2); the channels behind them are copied.
+ *
+ * diffattn_rope_freqs — on the host, the table of f_j = base^(-2j / rotary_dim):
+ *   DIFFATTN_ROPE_PLAIN   as they are;
+ *   DIFFATTN_ROPE_LINEAR  f_j / factor (positions interpolated);
+ *   DIFFATTN_ROPE_RAMP    f_j (1 - g) / factor + f_j g with
+ *                         g = clamp((original_length f_j / 2 pi - beta_slow) / (beta_fast - beta_slow), 0, 1):
+ *                         pairs that turn often within the original context keep their
+ *                         frequency, slow ones are interpolated; magnitude 0.1 ln(factor) + 1.
+ * freqs: HOST pointer to rotary_dim / 2 values, each f_j / 2 pi (turns per position) as a
+ *   0.64 fixed-point fraction, so that position x value, modulo 2^64, is the fraction of
+ *   a turn whatever the position. The caller copies them to the device.
+ * magnitude: HOST pointer; 1 except for the ramp. Multiplied by the caller's own if any.
+ * rotary_dim a multiple of 8; base >= 1, factor >= 1 (scaled kinds), original_length >= 1
+ * and 0 <= beta_slow < beta_fast (ramp); else INVALID_ARG.
+ */
+#define DIFFATTN_ROPE_PLAIN 0
+#define DIFFATTN_ROPE_LINEAR 1
+#define DIFFATTN_ROPE_RAMP 2
+diffattn_status diffattn_rope_freqs(int rotary_dim, double base, int scaling, double factor, int original_length,
+                                    double beta_fast, double beta_slow, uint64_t* freqs, float* magnitude);
+
+/* A rotation as the entry points below take it. freqs: DEVICE pointer to rotary_dim / 2
+ * values from diffattn_rope_freqs, 8-byte aligned; rotary_dim a multiple of 8, 8 .. d. */
+typedef struct {
+    const uint64_t* freqs;
+    int rotary_dim;
+    int interleaved;
+    float magnitude;
+} diffattn_rotation;
+
+/*
+ * diffattn_rope — rotates up to four operands (Q1, Q2, K1, K2, or any of them) in one
+ * launch; with backward != 0 the transpose (angles negated, the same magnitude), which
+ * takes the gradients of the rotated operands to those of the operands.
+ *
+ * in, out: HOST arrays of `count` (1..4) operands [B, heads[i], N, d] (as for diffattn_fwd),
+ *   of in_dtype / out_dtype (f32, bf16 or f16 each; arithmetic in fp32, one rounding).
+ *   out[i] may be in[i] itself (the same pointer, strides and type); any other overlap
+ *   is not allowed.
+ * heads: HOST array; an operand with heads[i] == 0 is skipped.
+ * positions: device int32 [B, N] contiguous (any value, negative ones included), or NULL:
+ *   row n of every sequence stands at position n.
+ * d a multiple of 8, at most 256. B, N or all heads 0: DIFFATTN_OK.
+ */
+diffattn_status diffattn_rope(const diffattn_tensor* in, const diffattn_tensor* out, const int* heads, int count,
+                              const int32_t* positions, int B, int N, int d, const diffattn_rotation* rotation,
+                              int backward, int in_dtype, int out_dtype, void* stream);
+
+/*
+ * diffattn_kv_append_chunk_paged — diffattn_kv_append_paged for any number of new tokens
+ * per sequence, with the position rotation of K1 and K2 applied on the way. The new
+ * tokens of all sequences lie one after another in T rows: those of sequence b are rows
+ * q_start[b] .. q_start[b + 1] - 1, and they are the last of its seq_lens[b] tokens, so
+ * row q_start[b] + i goes to position seq_lens[b] - n_b + i (n_b rows) of the cache.
+ *
+ * k1_new, k2_new: [T, H_kv, d], v_new: [T, H_kv, Dv], in_dtype bf16 or f16, given by token
+ *   stride (stride_n) and head stride (stride_h), e.g. column blocks of one projection's
+ *   output; stride_b is not used.
+ * k1_pages, k2_pages, v_pages, block_table, max_pages, num_pages: as for
+ *   diffattn_decode_paged (bf16).
+ * q_start: device int32 [B + 1], non-decreasing, q_start[0] >= 0. Rows before q_start[0]
+ *   and from q_start[B] on belong to no sequence and are not written anywhere.
+ * seq_lens: device int32 [B]. A row whose position or page falls outside the table or the
+ *   pool is skipped. Two rows that share a cache entry leave one of them.
+ * rotation: HOST pointer, or NULL: K1 and K2 are copied.
+ * d and Dv multiples of 8. T, B or H_kv equal to 0: DIFFATTN_OK.
+ */
+diffattn_status diffattn_kv_append_chunk_paged(diffattn_tensor k1_new, diffattn_tensor k2_new, diffattn_tensor v_new,
+                                               int in_dtype, diffattn_tensor k1_pages, diffattn_tensor k2_pages,
+                                               diffattn_tensor v_pages, const int32_t* block_table, int max_pages,
+                                               int num_pages, const int32_t* q_start, const int32_t* seq_lens,
+                                               const diffattn_rotation* rotation, int T, int B, int H_kv, int d, int Dv,
+                                               void* stream);
+
+/* diffattn_kv_append_chunk_paged_fp8 — the same into fp8 e4m3 pages: each value, rotated in
+ * fp32, is stored as e4m3(x / scale) as by diffattn_kv_append_paged_fp8. */
+diffattn_status diffattn_kv_append_chunk_paged_fp8(diffattn_tensor k1_new, diffattn_tensor k2_new,
+                                                   diffattn_tensor v_new, int in_dtype, diffattn_tensor k1_pages,
+                                                   diffattn_tensor k2_pages, diffattn_tensor v_pages,
+                                                   const int32_t* block_table, int max_pages, int num_pages,
+                                                   const int32_t* q_start, const int32_t* seq_lens,
+                                                   const diffattn_rotation* rotation, int T, int B, int H_kv, int d,
+                                                   int Dv, float k1_scale, float k2_scale, float v_scale, void* stream);
+
+/*
+ * diffattn_chunk_paged — differential attention of the new tokens of many sequences over a
+ * paged KV cache that already holds them: a piece of a prompt, a few drafted tokens or a
+ * single one per sequence, mixed freely in one call. Rows as for
+ * diffattn_kv_append_chunk_paged: row q_start[b] + i stands at position
+ * p = seq_lens[b] - n_b + i of sequence b and sees cache entries 0 .. p. The computation per
+ * row is that of diffattn_decode_paged, on the tensor cores (P rounded to bf16, or to f16
+ * over an fp8 cache).
+ *
+ * q1, q2: [T, H, d] bf16, given by token stride (stride_n) and head stride (stride_h).
+ * k1_pages .. num_pages, kv_group: as for diffattn_decode_paged; kv_group at most 128.
+ *   A table entry that is outside the pool reads zeros. Bytes of the cache behind a
+ *   sequence's length are never part of a result, whatever they hold; entries before it
+ *   have to be finite (a row does not see later tokens of its chunk, but 0 x NaN of
+ *   their V rows would reach it).
+ * q_start: device int32 [B + 1], non-decreasing, 0 <= q_start[b] <= T; rows of `out` outside
+ *   [q_start[0], q_start[B]) are left as they are.
+ * seq_lens: device int32 [B], clamped to [0, L]. A row at a negative position sees no key
+ *   and gives zeros.
+ * L: the largest sequence length (<= 64 * max_pages).
+ * out: [T, H, Dv] contiguous, out_dtype f32, bf16 or f16.
+ * The lengths are read on the device: a captured call replays with new ones, as long as
+ * they keep to T, B and L. Results do not depend on scheduling (no atomics on data).
+ * Supported: (d, Dv) = (64, 128) or (128, 256). T, B or H equal to 0: DIFFATTN_OK.
+ * workspace: at least diffattn_chunk_workspace_size() bytes, 256-byte aligned; its first 4
+ *   bytes are the error word, as for diffattn_decode; the rest needs no initialisation.
+ *   Calls that may run at the same time need workspaces of their own.
+ */
+diffattn_status diffattn_chunk_paged(diffattn_tensor q1, diffattn_tensor q2, diffattn_tensor k1_pages,
+                                     diffattn_tensor k2_pages, diffattn_tensor v_pages, const int32_t* block_table,
+                                     int max_pages, int num_pages, const int32_t* q_start, const int32_t* seq_lens, int L,
+                                     void* out, const float* norm_weight, int T, int B, int H, int kv_group, int d, int Dv,
+                                     float lambda, float lambda_init, float eps, int out_dtype, void* workspace,
+                                     size_t workspace_bytes, void* stream);
+
+/* diffattn_chunk_paged_fp8 — the same over a paged cache of e4m3 values with one scale per
+ * tensor, as for diffattn_decode_paged_fp8. */
+diffattn_status diffattn_chunk_paged_fp8(diffattn_tensor q1, diffattn_tensor q2, diffattn_tensor k1_pages,
+                                         diffattn_tensor k2_pages, diffattn_tensor v_pages, const int32_t* block_table,
+                                         int max_pages, int num_pages, const int32_t* q_start, const int32_t* seq_lens,
+                                         int L, void* out, const float* norm_weight, int T, int B, int H, int kv_group,
+                                         int d, int Dv, float lambda, float lambda_init, float eps, float k1_scale,
+                                         float k2_scale, float v_scale, int out_dtype, void* workspace,
+                                         size_t workspace_bytes, void* stream);
+
+/* Workspace bytes of diffattn_chunk_paged and diffattn_chunk_paged_fp8 for these sizes. */
+diffattn_status diffattn_chunk_workspace_size(int T, int B, int H, int kv_group, int L, int d, int Dv, size_t* bytes);
+
+/*
  * diffattn_bwd — gradients of diffattn_fwd (the backward pass). The pages train
  * DIFF Transformers ("Differential Transformer: Transformer que cancela ruído
  * de atenção", section "Eficiência e estabilidade de treinamento") but print no
