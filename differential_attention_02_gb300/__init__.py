@@ -485,10 +485,9 @@ def rope_plan(rotary_dim: int, base: float = 10000.0, interleaved: bool = False,
     return RopePlan(table.to(dev), int(rotary_dim), bool(interleaved), m if magnitude is None else float(magnitude))
 
 
-def _same_device(dev, *tensors):
-    for t in tensors:
-        if t is not None and t.device != dev:
-            raise ValueError("all tensors must be on one CUDA device")
+# The checks below run on every serving step, where a call's host time can exceed its kernels':
+# plain loops, one attribute access each, and the raw stream handle.
+_raw_stream = torch._C._cuda_getCurrentRawStream
 
 
 def _elsewhere(dev, stream):
@@ -501,10 +500,15 @@ def _elsewhere(dev, stream):
     return torch.cuda.stream(stream if stream is not None else torch.cuda.current_stream(dev))
 
 
-def _int32(dev, shape, what, *tensors):
+def _on_device(dev, *tensors):
     for t in tensors:
-        if t.dtype != torch.int32 or t.device != dev or not t.is_contiguous() or tuple(t.shape) != tuple(shape):
-            raise ValueError(f"{what} must be a contiguous int32 tensor of shape {list(shape)} on the operands' device")
+        if t is not None and t.device != dev:
+            raise ValueError("all tensors must be on one CUDA device")
+
+
+def _int32(t, dev, shape, what):
+    if t.dtype != torch.int32 or t.shape != shape or t.device != dev or not t.is_contiguous():
+        raise ValueError(f"{what} must be a contiguous int32 tensor of shape {list(shape)} on the operands' device")
 
 
 _serving_ws: dict = {}
@@ -514,7 +518,7 @@ def _serving_workspace(nbytes: int, dev) -> torch.Tensor:
     """Workspace of the current stream: kept per stream, so that calls on two streams share none. During
     a graph capture a new one from the graph's own memory, so that two graphs share none either."""
     capturing = torch.cuda.is_current_stream_capturing()
-    key = (dev.index, torch.cuda.current_stream(dev).cuda_stream)
+    key = (dev.index, _raw_stream(dev.index))
     buf = None if capturing else _serving_ws.get(key)
     if buf is None or buf.numel() < nbytes:
         buf = torch.empty(nbytes + 256, dtype=torch.uint8, device=dev)
@@ -532,64 +536,80 @@ def diffattn_rope(tensors, rope: RopePlan, positions=None, backward: bool = Fals
     rotated operands to gradients of the operands. positions: int32 [B, N] or None (row n at position n).
     out: tensors to write (the operands themselves rotate in place), else new ones of out_dtype (default:
     the operands') in the operands' memory order. Returns them as a tuple."""
-    tensors = tuple(tensors)
     x = tensors[0]
-    ctx = _elsewhere(x.device, stream)
+    dev, dtype = x.device, x.dtype
+    ctx = _elsewhere(dev, stream)
     if ctx is not None:
         with ctx:
             return diffattn_rope(tensors, rope, positions, backward, out, out_dtype)
-    dev = x.device
-    _same_device(dev, *tensors, rope.freqs)
-    if not 1 <= len(tensors) <= 4 or any(t.dim() != 4 for t in tensors):
+    n = len(tensors)
+    if n > 4 or x.dim() != 4:
         raise ValueError("one to four operands [B, H, N, d]")
     B, _, N, d = x.shape
-    if any(t.dtype != x.dtype or t.shape[0] != B or t.shape[2] != N or t.shape[3] != d for t in tensors):
-        raise ValueError("operands must share dtype, batch, rows and width")
+    if rope.freqs.device != dev:
+        raise ValueError("all tensors must be on one CUDA device")
     if positions is not None:
-        _int32(dev, (B, N), "positions", positions)
-    if out is None:
-        out = tuple(torch.empty_like(t, dtype=out_dtype) for t in tensors)
-    else:
-        out = tuple(out)
-        _same_device(dev, *out)
-        if len(out) != len(tensors) or any(o.shape != t.shape or o.dtype != out[0].dtype for o, t in zip(out, tensors)):
-            raise ValueError("out must match the operands' shapes and share one dtype")
-        if out_dtype is not None and out_dtype != out[0].dtype:
-            raise ValueError("out_dtype does not match out")
-    n = len(tensors)
-    arr, heads = Tensor4 * n, (ctypes.c_int * n)(*(t.shape[1] for t in tensors))
-    _check(load_library().diffattn_rope(arr(*(_t4(t) for t in tensors)), arr(*(_t4(t) for t in out)), heads, n,
-                                        None if positions is None else positions.data_ptr(), B, N, d,
-                                        ctypes.byref(rope._c), int(bool(backward)), _dtype_code(x.dtype),
-                                        _dtype_code(out[0].dtype), torch.cuda.current_stream(dev).cuda_stream),
-           "diffattn_rope")
-    return out
+        _int32(positions, dev, (B, N), "positions")
+    src, dst, heads, fresh = [], [], [], out is None
+    if fresh:
+        out = [torch.empty_like(t, dtype=out_dtype) for t in tensors]
+    odt = out[0].dtype
+    if len(out) != n or (out_dtype is not None and out_dtype != odt):
+        raise ValueError("out must match the operands and out_dtype")
+    rows = (B, N, d)
+    for t, o in zip(tensors, out):
+        b, h, m, w = shape = t.shape
+        s, r = t.stride(), o.stride()
+        if (b, m, w) != rows or t.dtype != dtype or s[3] != 1 or t.device != dev:
+            raise ValueError("operands must share device, dtype, batch, rows and width, the last dimension contiguous")
+        if not fresh and (o.shape != shape or o.dtype != odt or r[3] != 1 or o.device != dev):
+            raise ValueError("out must match the operands' shapes and share one dtype and the device")
+        heads.append(h)
+        src.append(Tensor4(t.data_ptr(), s[0], s[1], s[2]))
+        dst.append(Tensor4(o.data_ptr(), r[0], r[1], r[2]))
+    arr = _TENSORS[n]
+    _check((_lib or load_library()).diffattn_rope(
+        arr(*src), arr(*dst), _INTS[n](*heads), n, None if positions is None else positions.data_ptr(), B, N, d, rope._c,
+        1 if backward else 0, _dtype_code(dtype), _dtype_code(odt), _raw_stream(dev.index)), "diffattn_rope")
+    return tuple(out)
 
 
-def _t3(t: torch.Tensor) -> Tensor4:
+_TENSORS = [Tensor4 * n for n in range(5)]
+_INTS = [ctypes.c_int * n for n in range(5)]
+
+
+def _t3(t: torch.Tensor, T: int, H: int, width: int) -> Tensor4:
     """[T, H, width] rows with a contiguous last dimension -> diffattn_tensor (stride_b unused)."""
-    if t.dim() != 3 or t.stride(2) != 1:
-        raise ValueError("ragged rows must be [T, H, width] with a contiguous last dimension")
-    return Tensor4(t.data_ptr(), 0, t.stride(1), t.stride(0))
+    s = t.stride()
+    if t.shape != (T, H, width) or s[2] != 1:
+        raise ValueError(f"ragged rows must be [{T}, {H}, {width}] with a contiguous last dimension")
+    return Tensor4(t.data_ptr(), 0, s[1], s[0])
 
 
-def _paged_args(dev, pages, block_table, q_start, seq_lens, scales):
-    k1, k2, v = pages
-    fp8 = _is_fp8(k1)
-    if fp8 != (scales is not None) or any(_is_fp8(t) != fp8 for t in (k2, v)):
+def _paged_args(dev, k1, k2, v, H_kv, d, block_table, q_start, seq_lens, scales):
+    """The pages as diffattn_tensors, the table's sizes, whether the cache is fp8, and the sequences."""
+    dt, shape = k1.dtype, k1.shape
+    fp8 = scales is not None
+    if fp8 != (dt == torch.float8_e4m3fn or dt == torch.uint8) or _is_fp8(k2) != fp8 or _is_fp8(v) != fp8:
         raise ValueError("fp8 pages (all three) go with scales, bf16 pages without")
-    if not fp8 and any(t.dtype != torch.bfloat16 for t in pages):
+    if not fp8 and not (dt == k2.dtype == v.dtype == torch.bfloat16):
         raise ValueError("pages must be bf16 or fp8 (e4m3)")
-    _same_device(dev, *pages)
-    if any(t.dim() != 4 or t.shape[2] != 64 or t.shape[:2] != k1.shape[:2] for t in pages) or k1.shape != k2.shape:
-        raise ValueError("pages must be [num_pages, H_kv, 64, width] with common pages and heads")
+    P = shape[0]
+    if shape != (P, H_kv, 64, d) or k2.shape != shape or v.dim() != 4 or v.shape[:3] != shape[:3]:
+        raise ValueError("pages must be [num_pages, H_kv, 64, width] with the rows' heads and widths")
+    s1, s2, sv = k1.stride(), k2.stride(), v.stride()
+    if s1[3] != 1 or s2[3] != 1 or sv[3] != 1:
+        raise ValueError("pages must have a contiguous last dimension")
+    if k1.device != dev or k2.device != dev or v.device != dev:
+        raise ValueError("all tensors must be on one CUDA device")
     B = seq_lens.shape[0]
-    _int32(dev, (B,), "seq_lens", seq_lens)
-    _int32(dev, (B + 1,), "q_start", q_start)
-    if block_table.dim() != 2:
-        raise ValueError("block_table must be [B, max_pages]")
-    _int32(dev, (B, block_table.shape[1]), "block_table", block_table)
-    return fp8, B
+    _int32(seq_lens, dev, (B,), "seq_lens")
+    _int32(q_start, dev, (B + 1,), "q_start")
+    max_pages = block_table.shape[-1]
+    _int32(block_table, dev, (B, max_pages), "block_table")
+    return (Tensor4(k1.data_ptr(), s1[0], s1[1], s1[2]), Tensor4(k2.data_ptr(), s2[0], s2[1], s2[2]),
+            Tensor4(v.data_ptr(), sv[0], sv[1], sv[2]), block_table.data_ptr(), max_pages, P, q_start.data_ptr(),
+            seq_lens.data_ptr()), fp8, B
 
 
 def diffattn_kv_append_chunk_paged(k1_new, k2_new, v_new, k1_pages, k2_pages, v_pages, block_table, q_start, seq_lens,
@@ -598,34 +618,31 @@ def diffattn_kv_append_chunk_paged(k1_new, k2_new, v_new, k1_pages, k2_pages, v_
     q_start[b] .. q_start[b + 1] - 1 and the last of its seq_lens[b] tokens) into the paged cache (pages
     [num_pages, H_kv, 64, *], block_table [B, max_pages]), K1 and K2 rotated by `rope` at their positions.
     fp8 pages take scales = (k1_scale, k2_scale, v_scale) and store e4m3(x / scale)."""
-    dev = k1_new.device
+    dev, dtype = k1_new.device, k1_new.dtype
     ctx = _elsewhere(dev, stream)
     if ctx is not None:
         with ctx:
             return diffattn_kv_append_chunk_paged(k1_new, k2_new, v_new, k1_pages, k2_pages, v_pages, block_table,
                                                   q_start, seq_lens, rope, scales)
-    fp8, B = _paged_args(dev, (k1_pages, k2_pages, v_pages), block_table, q_start, seq_lens, scales)
-    _same_device(dev, k1_new, k2_new, v_new, None if rope is None else rope.freqs)
     T, Hk, d = k1_new.shape
-    Dv = v_new.shape[2]
-    if k2_new.shape != k1_new.shape or v_new.shape[:2] != (T, Hk) or any(t.dtype != k1_new.dtype for t in (k2_new, v_new)):
-        raise ValueError("k1_new, k2_new [T, H_kv, d] and v_new [T, H_kv, Dv] of one dtype")
-    if k1_pages.shape[1] != Hk or k1_pages.shape[3] != d or v_pages.shape[3] != Dv:
-        raise ValueError("the pages' heads and widths must be the new rows'")
-    lib, args = load_library(), (_t3(k1_new), _t3(k2_new), _t3(v_new), _dtype_code(k1_new.dtype), _t4(k1_pages),
-                                 _t4(k2_pages), _t4(v_pages), block_table.data_ptr(), block_table.shape[1],
-                                 k1_pages.shape[0], q_start.data_ptr(), seq_lens.data_ptr(),
-                                 None if rope is None else ctypes.byref(rope._c), T, B, Hk, d, Dv)
-    st = torch.cuda.current_stream(dev).cuda_stream
+    Dv = v_pages.shape[-1]
+    paged, fp8, B = _paged_args(dev, k1_pages, k2_pages, v_pages, Hk, d, block_table, q_start, seq_lens, scales)
+    if k2_new.dtype != dtype or v_new.dtype != dtype:
+        raise ValueError("k1_new, k2_new and v_new must share one dtype")
+    _on_device(dev, k2_new, v_new, None if rope is None else rope.freqs)
+    lib = _lib or load_library()
+    args = (_t3(k1_new, T, Hk, d), _t3(k2_new, T, Hk, d), _t3(v_new, T, Hk, Dv), _dtype_code(dtype), *paged,
+            None if rope is None else rope._c, T, B, Hk, d, Dv)
     if fp8:
-        _check(lib.diffattn_kv_append_chunk_paged_fp8(*args, *scales, st), "diffattn_kv_append_chunk_paged_fp8")
+        _check(lib.diffattn_kv_append_chunk_paged_fp8(*args, *scales, _raw_stream(dev.index)),
+               "diffattn_kv_append_chunk_paged_fp8")
     else:
-        _check(lib.diffattn_kv_append_chunk_paged(*args, st), "diffattn_kv_append_chunk_paged")
+        _check(lib.diffattn_kv_append_chunk_paged(*args, _raw_stream(dev.index)), "diffattn_kv_append_chunk_paged")
 
 
 def chunk_workspace_bytes(T, B, H, kv_group, L, d, Dv) -> int:
     n = ctypes.c_size_t()
-    _check(load_library().diffattn_chunk_workspace_size(T, B, H, kv_group, L, d, Dv, ctypes.byref(n)),
+    _check((_lib or load_library()).diffattn_chunk_workspace_size(T, B, H, kv_group, L, d, Dv, ctypes.byref(n)),
            "diffattn_chunk_workspace_size")
     return n.value
 
@@ -644,28 +661,28 @@ def diffattn_chunk_paged(q1, q2, k1_pages, k2_pages, v_pages, block_table, q_sta
         with ctx:
             return diffattn_chunk_paged(q1, q2, k1_pages, k2_pages, v_pages, block_table, q_start, seq_lens, lam, lam_init, L,
                                         kv_group, eps, norm_weight, out_dtype, out, ws, None, scales)
-    fp8, B = _paged_args(dev, (k1_pages, k2_pages, v_pages), block_table, q_start, seq_lens, scales)
-    _same_device(dev, q1, q2, norm_weight, out)
     T, H, d = q1.shape
-    Dv = v_pages.shape[3]
-    if q2.shape != q1.shape or q1.dtype != torch.bfloat16 or q2.dtype != torch.bfloat16:
-        raise ValueError("q1 and q2 must be [T, H, d] bf16 tensors of one shape")
-    if k1_pages.shape[1] * kv_group != H or k1_pages.shape[3] != d:
-        raise ValueError("the pages must have H / kv_group heads of the query's width")
-    if norm_weight is not None and (norm_weight.dtype != torch.float32 or norm_weight.shape != (Dv,)
-                                    or not norm_weight.is_contiguous()):
-        raise ValueError("norm_weight must be a contiguous fp32 [Dv] tensor")
+    Dv = v_pages.shape[-1]
+    if q1.dtype != torch.bfloat16 or q2.dtype != torch.bfloat16 or q2.device != dev:
+        raise ValueError("q1 and q2 must be [T, H, d] bf16 tensors on one device")
+    if kv_group < 1 or H % kv_group:
+        raise ValueError("kv_group must divide the query heads")
+    paged, fp8, B = _paged_args(dev, k1_pages, k2_pages, v_pages, H // kv_group, d, block_table, q_start, seq_lens, scales)
+    w = None
+    if norm_weight is not None:
+        if (norm_weight.dtype != torch.float32 or norm_weight.shape != (Dv,) or not norm_weight.is_contiguous()
+                or norm_weight.device != dev):
+            raise ValueError("norm_weight must be a contiguous fp32 [Dv] tensor on the operands' device")
+        w = norm_weight.data_ptr()
     if out is None:
         out = torch.empty((T, H, Dv), dtype=out_dtype, device=dev)
-    elif out.shape != (T, H, Dv) or not out.is_contiguous():
-        raise ValueError("out must be a contiguous [T, H, Dv] tensor")
+    elif out.shape != (T, H, Dv) or not out.is_contiguous() or out.device != dev:
+        raise ValueError("out must be a contiguous [T, H, Dv] tensor on the operands' device")
     if ws is None:
         ws = _serving_workspace(chunk_workspace_bytes(T, B, H, kv_group, L, d, Dv), dev)
-    args = (_t3(q1), _t3(q2), _t4(k1_pages), _t4(k2_pages), _t4(v_pages), block_table.data_ptr(), block_table.shape[1],
-            k1_pages.shape[0], q_start.data_ptr(), seq_lens.data_ptr(), L, out.data_ptr(),
-            None if norm_weight is None else norm_weight.data_ptr(), T, B, H, kv_group, d, Dv, lam, lam_init, eps)
-    tail = (_dtype_code(out.dtype), ws.data_ptr(), ws.numel(), torch.cuda.current_stream(dev).cuda_stream)
-    lib = load_library()
+    lib = _lib or load_library()
+    args = (_t3(q1, T, H, d), _t3(q2, T, H, d), *paged, L, out.data_ptr(), w, T, B, H, kv_group, d, Dv, lam, lam_init, eps)
+    tail = (_dtype_code(out.dtype), ws.data_ptr(), ws.numel(), _raw_stream(dev.index))
     if fp8:
         _check(lib.diffattn_chunk_paged_fp8(*args, *scales, *tail), "diffattn_chunk_paged_fp8")
     else:

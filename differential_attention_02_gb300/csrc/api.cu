@@ -969,19 +969,19 @@ bool chunk_layout(int B, int H, int kv_group, int T, int L, int d, int Dv, Chunk
     l->tm = kChunkRows / kv_group;
     l->rows = std::min(l->tm, T) * kv_group;
     const int64_t tiles = (int64_t)T / l->tm + std::min(B, T);
-    // Splitting needs a tile of at least two key tiles.
-    const int64_t extra = L > kChunkKeys ? (2 * l->ctas + H_kv - 1) / H_kv : 0;
-    const int64_t entries = tiles + extra;
-    if (entries * H_kv * 2 > INT32_MAX) return false;
+    // Cutting needs an item of at least two key tiles.
+    const int64_t extra = L > kChunkKeys ? l->ctas : 0;
+    const int64_t entries = tiles * H_kv + extra;
+    if (entries * 2 > INT32_MAX) return false;
     l->max_tiles = (int)tiles;
     l->max_entries = (int)entries;
     l->max_slots = (int)(2 * extra);
     l->max_merges = (int)extra;
     l->tiles = round256(kControlBytes + sizeof(ChunkPlan));
     l->entries = l->tiles + round256(tiles * sizeof(ChunkTile));
-    l->merges = l->entries + round256(entries * sizeof(ChunkEntry));
+    l->merges = l->entries + round256(2 * entries * sizeof(ChunkEntry));
     l->stats = l->merges + round256(extra * sizeof(ChunkMerge));
-    const size_t states = (size_t)l->max_slots * H_kv * 2 * l->rows;
+    const size_t states = (size_t)l->max_slots * 2 * l->rows;
     l->o = l->stats + round256(states * 2 * sizeof(float));
     l->total = l->o + round256(states * Dv * sizeof(float));
     return true;

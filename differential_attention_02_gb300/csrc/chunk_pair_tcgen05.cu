@@ -156,9 +156,11 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(Cfg<FP8>::kThreads, 
     cluster_sync_start();
     pdl_trigger();
     pdl_wait();  // the plan, Q and the newest cache rows come from earlier kernels
-    const int item = (int)(blockIdx.x >> 1), ei = item / p.H_kv, hk = item % p.H_kv;
-    if (ei >= p.plan->entries) return;  // every thread of both CTAs
-    const ChunkEntry e = p.entries[ei];
+    const ChunkPlan plan = *p.plan;
+    const int ei = (int)(blockIdx.x >> 1);
+    if (ei >= plan.upto[3]) return;  // every thread of both CTAs
+    const ChunkEntry e = p.entries[chunk_entry(plan.upto, p.max_entries, ei)];
+    const int hk = e.hk;
     if (warp == 1) {
         tmem_alloc(&bars->tmem_base, C::kTmemCols);
         tmem_relinquish();
@@ -362,9 +364,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(Cfg<FP8>::kThreads, 
             const float m_new = fmax3(fmaxf(mx0, mx1), mx2, mx3) * sl2;
             float alpha = 1.f;
             bool rescale = false;
-            if (j == 0) {
-                m_used = fmaxf(m_new, kChunkNoMax);
-            } else if (r < rows && m_new > m_used + kRescaleThreshold) {
+            if (m_new > m_used + kRescaleThreshold) {
                 alpha = fast_exp2(m_used - m_new);
                 m_used = m_new;
                 rescale = true;
@@ -503,7 +503,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(Cfg<FP8>::kThreads, 
     if (e.slot >= 0) {
         // Partial state of this CTA's map: the thread's row.
         if (epi && ok) {
-            const int64_t it = (int64_t)e.slot * p.H_kv + hk;
+            const int64_t it = e.slot;
             float* o = p.part_o + (it * 2 + rank) * (DV / 4) * p.rows * 4 + r * 4;
 #pragma unroll 1
             for (int c = 0; c < DV / 32; ++c) {
@@ -641,7 +641,7 @@ cudaError_t launch_t(const ChunkParams& p, cudaStream_t stream) {
     using C = Cfg<FP8>;
     const cudaError_t e = prepare_once<chunk_pair_kernel<FP8>>((int)C::kSmem);
     if (e != cudaSuccess) return e;
-    return launch_pdl(chunk_pair_kernel<FP8>, dim3((unsigned)(2 * p.max_entries * p.H_kv)), dim3(C::kThreads), C::kSmem,
+    return launch_pdl(chunk_pair_kernel<FP8>, dim3((unsigned)(2 * p.max_entries)), dim3(C::kThreads), C::kSmem,
                       stream, p);
 }
 

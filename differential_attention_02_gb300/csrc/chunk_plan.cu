@@ -1,20 +1,23 @@
 // Work plan and merge of the attention of ragged new tokens over a paged cache.
 //
 // The chunk starts and lengths live on the device (a captured graph replays with new
-// ones), so the device cuts the work: one block lists the query tiles, chooses how
-// many key tiles one entry takes, and writes the list of entries that the attention
-// kernel's CTAs index. A few microseconds, most of them overlapped with the launch of
-// the attention kernel (a programmatic dependent).
+// ones), so the device cuts the work: one block lists the query tiles, chooses how many
+// key tiles one entry takes and writes the list of entries that the attention kernel's
+// CTAs index, longest first.
 //
-// Why a split length chosen from the batch: one sequence's last 16 tokens have one
-// tile per KV head and fill the GPU only if their keys are split; four prompts'
-// chunks have thousands of tiles, and splitting them only costs partial states; a
-// batch of both has a few long tiles that would run on alone. With entries of at most
-// k key tiles, W key tiles in all and C work items at a time, k >= W / (2 C) bounds
-// the number of extra entries by 2 C and the slots of split tiles by 4 C (a tile of
-// n > k key tiles has ceil(n / k) <= 2 n / k entries), which sizes the workspace on
-// the host. Among the k that cut the longest tile into 1 .. 64 parts, the one with the
-// shortest estimated makespan is taken.
+// Why a split length chosen from the batch: one sequence's last 16 tokens have one item
+// (a tile and a KV head) per head and fill the GPU only if their keys are split; four
+// prompts' chunks have a thousand items, and splitting them only costs partial states.
+// Of the lengths that cut the longest item into 1 .. 64 parts, the one with the shortest
+// estimated makespan is taken, at a fixed cost per entry (start and epilogue: about 4 us
+// against 1.3 us a key tile) and a further one per partial state. With W key tiles in all
+// and C entries at a time, a length k >= W / C adds at most C entries and leaves at most
+// 2 C of them partial (an item of n > k key tiles has ceil(n / k) <= 2 n / k parts), which
+// sizes the lists and the workspace on the host. Shorter ones would not pay: cutting the
+// whole row of items at every multiple of W / C, which balances any batch within an
+// entry, was measured against the whole items of larger batches and was no faster (four
+// prompts' chunks 592 against 586 us, a mixed batch 110 against 104 us), since every cut
+// costs a partial state of 128 KB and its merge.
 #include <math.h>
 
 #include "common.cuh"
@@ -23,18 +26,17 @@
 namespace da {
 namespace {
 
-constexpr int kPlanThreads = 1024;
+constexpr int kPlanThreads = 512, kPlanWarps = kPlanThreads / 32;
 constexpr int kMaxParts = 64;
-// Fixed cost of an entry (start, epilogue) and of one that leaves a partial state, in
-// key tiles: about 4 us and 1.3 us a key tile.
-constexpr float kEntryCost = 3.f, kSplitCost = 5.f;
+constexpr int kTilesInSmem = 2048;  // longer lists are read back from the workspace
+constexpr float kEntryCost = 3.f;
 
 __device__ __forceinline__ int tile_keys(const ChunkTile& t) {  // key tiles that the tile's last token sees
     const int keys = t.pos0 + t.ntok;
     return keys > 0 ? (keys + kChunkKeys - 1) / kChunkKeys : 0;
 }
 
-// Exclusive sum over the block of one int per thread; *total gets the whole sum.
+// Exclusive sum over the block of one value per thread; *total gets the whole sum.
 __device__ __forceinline__ int block_scan(int v, int* warp_sums, int* total) {
     const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
     int x = v;
@@ -46,193 +48,265 @@ __device__ __forceinline__ int block_scan(int v, int* warp_sums, int* total) {
     __syncthreads();  // earlier readers of warp_sums are done
     if (lane == 31) warp_sums[warp] = x;
     __syncthreads();
-    if (warp == 0) {
-        const int w = warp_sums[lane];
-        int y = w;
+    // Every warp adds up the warps' sums itself: one barrier less than handing them out.
+    const int w = lane < kPlanWarps ? warp_sums[lane] : 0;
+    int y = w;
 #pragma unroll
-        for (int o = 1; o < 32; o <<= 1) {
-            const int z = __shfl_up_sync(0xffffffffu, y, o);
-            if (lane >= o) y += z;
-        }
-        warp_sums[lane] = y - w;
-        if (lane == 31) warp_sums[32] = y;
+    for (int o = 1; o < kPlanWarps; o <<= 1) {
+        const int z = __shfl_up_sync(0xffffffffu, y, o);
+        if (lane >= o) y += z;
     }
-    __syncthreads();
-    *total = warp_sums[32];
-    return warp_sums[warp] + x - v;
+    *total = __shfl_sync(0xffffffffu, y, kPlanWarps - 1);
+    return __shfl_sync(0xffffffffu, y - w, warp) + x - v;
 }
 
 __global__ void __launch_bounds__(kPlanThreads) chunk_plan_kernel(const __grid_constant__ ChunkParams p) {
-    __shared__ int warp_sums[33];
-    __shared__ long long work_sum;
-    __shared__ int work_max;
+    __shared__ int warp_sums[kPlanWarps];
     __shared__ float est[kMaxParts];
+    __shared__ int keys_s[kTilesInSmem];
+    __shared__ int count[5];  // entries of each class of length, merges
+    __shared__ int longest_s;
+    __shared__ unsigned long long row_s;  // key tiles of all tiles
     pdl_trigger();
-    pdl_wait();  // the lengths may be the previous kernel's output, and it may still read this workspace
     const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
-    if (tid == 0) {
-        work_sum = 0;
-        work_max = 0;
-    }
+    if (tid < 5) count[tid] = 0;
+    if (tid == 5) longest_s = 0;
+    if (tid == 6) row_s = 0;
+    pdl_wait();  // the lengths may be the previous kernel's output, and it may still read this workspace
     // 1. Query tiles, each sequence's last (longest) one first.
     int n_tiles = 0;
     for (int b0 = 0; b0 < p.B; b0 += kPlanThreads) {
         const int b = b0 + tid;
         int first = 0, n = 0, len = 0;
         if (b < p.B) {
-            first = min(max(p.q_start[b], 0), p.T);
-            n = min(max(p.q_start[b + 1], first), p.T) - first;
-            len = min(max(p.seq_lens[b], 0), p.L);
+            first = p.q_start[b];
+            const int next = p.q_start[b + 1], m = p.seq_lens[b];
+            first = min(max(first, 0), p.T);
+            n = min(max(next, first), p.T) - first;
+            len = min(max(m, 0), p.L);
         }
         const int nt = (n + p.tm - 1) / p.tm;
         int sum;
         const int at = n_tiles + block_scan(nt, warp_sums, &sum);
+        unsigned long long keys = 0;
+        int most = 0;
         for (int i = 0; i < nt && at + i < p.max_tiles; ++i) {
             const int k = nt - 1 - i;
-            p.tiles[at + i] = ChunkTile{b, first + k * p.tm, min(p.tm, n - k * p.tm), len - n + k * p.tm};
+            const ChunkTile t{b, first + k * p.tm, min(p.tm, n - k * p.tm), len - n + k * p.tm};
+            p.tiles[at + i] = t;
+            const int q = tile_keys(t);
+            if (at + i < kTilesInSmem) keys_s[at + i] = q;
+            keys += q;
+            most = max(most, q);
+        }
+        if (most > 0) {
+            atomicAdd(&row_s, keys);
+            atomicMax(&longest_s, most);
         }
         n_tiles += sum;
     }
     n_tiles = min(n_tiles, p.max_tiles);  // only starts that are not sorted exceed it
     __syncthreads();
-    // 2. Key tiles in all, and of the longest tile.
-    long long w = 0;
-    int wm = 0;
-    for (int i = tid; i < n_tiles; i += kPlanThreads) {
-        const int k = tile_keys(p.tiles[i]);
-        w += k;
-        wm = max(wm, k);
-    }
-#pragma unroll
-    for (int o = 16; o > 0; o >>= 1) {
-        w += __shfl_xor_sync(0xffffffffu, w, o);
-        wm = max(wm, __shfl_xor_sync(0xffffffffu, wm, o));
-    }
-    if (lane == 0) {
-        atomicAdd(reinterpret_cast<unsigned long long*>(&work_sum), (unsigned long long)w);
-        atomicMax(&work_max, wm);
-    }
-    __syncthreads();
-    const long long W = work_sum * p.H_kv;
-    const int longest = max(work_max, 1);
-    // 3. Key tiles per entry: a warp estimates one candidate at a time.
-    const int least = max(1, (int)((W + 2 * p.ctas - 1) / (2 * p.ctas)));
-    for (int s = 1 + warp; s <= kMaxParts; s += kPlanThreads / 32) {
-        const int k = (longest + s - 1) / s;
-        float e = INFINITY;
-        if (s == 1 || (k >= least && p.max_slots > 0)) {
-            float items = 0.f, split = 0.f;
-            for (int i = lane; i < n_tiles; i += 32) {
-                const int n = tile_keys(p.tiles[i]), parts = max(1, (n + k - 1) / k);
-                items += (float)parts;
-                if (parts > 1) split += (float)parts;
+    auto keys_of = [&](int i) { return i < kTilesInSmem ? keys_s[i] : tile_keys(p.tiles[i]); };
+    const int longest = max(longest_s, 1), n_items = n_tiles * p.H_kv;
+    const long long W = (long long)row_s * p.H_kv;
+    // 2. Key tiles per entry: a warp estimates one number of parts at a time. Batches of two rounds of
+    // items and more stay whole.
+    int k = longest;
+    const bool may_split = p.max_slots > 0 && W > 0 && n_items < 2 * p.ctas;
+    if (may_split) {
+        const int least = (int)((W + p.ctas - 1) / p.ctas);  // at most `longest`, or nothing is split
+        const float split_cost = kEntryCost + 5.f * (float)p.rows / kChunkRows, ctas = (float)p.ctas;
+        for (int s = 1 + warp; s <= kMaxParts; s += kPlanWarps) {
+            const int ks = (longest + s - 1) / s;
+            float e = INFINITY;
+            if (s == 1 || ks >= least) {
+                int items = 0, split = 0;
+                for (int i = lane; i < n_tiles; i += 32) {
+                    const int n = keys_of(i), parts = n > ks ? (n + ks - 1) / ks : 1;
+                    items += parts;
+                    split += parts > 1 ? parts : 0;
+                }
+                const float all_items = (float)__reduce_add_sync(0xffffffffu, items) * (float)p.H_kv;
+                const float all_split = (float)__reduce_add_sync(0xffffffffu, split) * (float)p.H_kv;
+                const float cost = (float)ks + (s > 1 ? split_cost : kEntryCost);
+                const float all = (float)W + kEntryCost * all_items + (split_cost - kEntryCost) * all_split;
+                e = fminf(ceilf(all_items / ctas) * cost, all / ctas + 0.5f * cost);
             }
-            items = warp_sum(items) * (float)p.H_kv;
-            split = warp_sum(split) * (float)p.H_kv;
-            const float ctas = (float)p.ctas, cost = (float)k + (s > 1 ? kSplitCost : kEntryCost);
-            const float all = (float)W + kEntryCost * items + (kSplitCost - kEntryCost) * split;
-            e = fminf(ceilf(items / ctas) * cost, all / ctas + 0.5f * cost);
+            if (lane == 0) est[s - 1] = e;
         }
-        if (lane == 0) est[s - 1] = e;
+        __syncthreads();
+        // Every warp finds the same minimum; the fewest parts among equals.
+        const float a = est[lane], b = est[lane + 32];
+        float e = fminf(a, b);
+        int s = a <= b ? lane + 1 : lane + 33;
+#pragma unroll
+        for (int o = 16; o > 0; o >>= 1) {
+            const float e2 = __shfl_xor_sync(0xffffffffu, e, o);
+            const int s2 = __shfl_xor_sync(0xffffffffu, s, o);
+            if (e2 < e || (e2 == e && s2 < s)) {
+                e = e2;
+                s = s2;
+            }
+        }
+        k = (longest + s - 1) / s;
     }
-    __syncthreads();
-    int best = 1;
-    for (int s = 2; s <= kMaxParts; ++s)
-        if (est[s - 1] < est[best - 1]) best = s;
-    const int k = (longest + best - 1) / best;
-    // 4. Entries, slots and merges.
-    int n_entries = 0, n_slots = 0, n_merges = 0;
-    for (int i0 = 0; i0 < n_tiles; i0 += kPlanThreads) {
+    // 3. Entries by class of length (over 1/2, 1/4, 1/8 of the longest, shorter) and their slots.
+    // Two lists of two classes each, one from the front and one from the back, so that one pass places
+    // them. The place within a class depends on the order of the atomics; the slots, and with them
+    // every sum, do not.
+    int n_slots = 0;
+    for (int i0 = 0; i0 < n_items; i0 += kPlanThreads) {
         const int i = i0 + tid;
         ChunkTile t{};
-        int n = 0, parts = 0;
-        if (i < n_tiles) {
-            t = p.tiles[i];
+        int n = 0, parts = 0, hk = 0;
+        if (i < n_items) {
+            const int ti = (unsigned)i / (unsigned)p.H_kv;
+            hk = i - ti * p.H_kv;
+            t = p.tiles[ti];
             n = tile_keys(t);
-            parts = max(1, (n + k - 1) / k);
+            parts = n > k ? (n + k - 1) / k : 1;
         }
-        int se, ss, sm;
-        const int ae = n_entries + block_scan(parts, warp_sums, &se);
-        const int as = n_slots + block_scan(parts > 1 ? parts : 0, warp_sums, &ss);
-        const int am = n_merges + block_scan(parts > 1 ? 1 : 0, warp_sums, &sm);
-        // The bounds hold for every batch (see the top); the checks keep the writes inside all the same.
-        for (int j = 0; j < parts && ae + j < p.max_entries; ++j) {
-            const int lo = (int)((long long)n * j / parts), hi = (int)((long long)n * (j + 1) / parts);
-            const int slot = parts > 1 && as + j < p.max_slots ? as + j : -1;
-            p.entries[ae + j] = ChunkEntry{t, lo, hi - lo, slot, 0};
+        int as = 0;
+        if (k < longest) {
+            int sum;
+            as = n_slots + block_scan(parts > 1 ? parts : 0, warp_sums, &sum);
+            n_slots += sum;
+            if (parts > 1 && as + parts <= p.max_slots) {
+                const int m = atomicAdd(&count[4], 1);
+                if (m < p.max_merges) p.merges[m] = ChunkMerge{t, as, parts, hk, 0};
+            }
         }
-        if (parts > 1 && am < p.max_merges && as + parts <= p.max_slots) p.merges[am] = ChunkMerge{t, as, parts, {0, 0}};
-        n_entries += se;
-        n_slots += ss;
-        n_merges += sm;
+        const int most = __reduce_max_sync(0xffffffffu, parts);
+        for (int j = 0; j < most; ++j) {
+            int lo = 0, hi = 0, c = 4;
+            if (j < parts) {
+                lo = (int)((unsigned)(n * j) / (unsigned)parts);  // n < 2^25 (L < 2^31), parts <= 64
+                hi = (int)((unsigned)(n * (j + 1)) / (unsigned)parts);
+                const int len = hi - lo;
+                c = 2 * len > k ? 0 : 4 * len > k ? 1 : 8 * len > k ? 2 : 3;
+            }
+            // One atomic per warp and class.
+            int place = 0;
+#pragma unroll
+            for (int q = 0; q < 4; ++q) {
+                const unsigned m = __ballot_sync(0xffffffffu, c == q);
+                if (m == 0) continue;
+                int base = 0;
+                if (lane == 0) base = atomicAdd(&count[q], __popc(m));
+                base = __shfl_sync(0xffffffffu, base, 0);
+                if (c == q) place = base + __popc(m & ((1u << lane) - 1));
+            }
+            // The bounds hold for every batch (see the top); the checks keep the writes inside all the same.
+            if (j < parts && place < p.max_entries) {
+                const int slot = parts > 1 && as + j < p.max_slots ? as + j : -1;
+                const int at = (c & 1) ? p.max_entries - 1 - place : place;
+                p.entries[(int64_t)(c >> 1) * p.max_entries + at] = ChunkEntry{t, lo, hi - lo, slot, hk};
+            }
+        }
     }
-    if (tid == 0) *p.plan = ChunkPlan{n_tiles, min(n_entries, p.max_entries), min(n_merges, p.max_merges), k};
+    __syncthreads();
+    if (tid == 0) {
+        const int c0 = count[0], c1 = c0 + count[1], c2 = c1 + count[2], c3 = c2 + count[3];
+        *p.plan = ChunkPlan{{c0, c1, c2, c3}, n_tiles, min(count[4], p.max_merges), k, 0};
+    }
 }
 
-// Joins the partial states of a split tile: block (merge, KV head) x eight rows; a thread
-// owns four output columns of one row. Then the combination, the row's RMSNorm and the
-// (1 - lambda_init) scale, as the attention kernels' own epilogues. The slots are
-// added in the order of their keys.
-constexpr int kMergeRows = 8;
+// Joins the partial states of the split items. What each entry left per row and map is
+// the unnormalised accumulator, the running maximum and the sum; the parts are added
+// in the order of their keys, then the combination, the row's RMSNorm and the
+// (1 - lambda_init) scale, as in the attention kernels' own epilogues. A kernel of its
+// own because one SM takes about 10 us to read the two states of a 128-row item, which
+// the last of the item's CTAs would add to its run (measured: 35 us on a batch of 100
+// such items); spread over the GPU they are read at the L2's rate.
+//
+// A block takes 32 rows of an item: lane = row, warp w column quartets 4 w .. 4 w + 3, so that
+// every load of a warp is 512 contiguous bytes, as the states were stored.
+constexpr int kMergeRows = 32;
 
 template <int DV>
-__global__ void __launch_bounds__(kMergeRows * DV / 4) chunk_merge_kernel(const __grid_constant__ ChunkParams p) {
-    constexpr int CG = DV / 4;
-    __shared__ float red[CG][kMergeRows + 1];
+__global__ void __launch_bounds__(DV * 2) chunk_merge_kernel(const __grid_constant__ ChunkParams p) {
+    constexpr int CG = DV / 4, WARPS = CG / 4;
+    __shared__ float red[WARPS][kMergeRows];
     pdl_trigger();
     pdl_wait();
-    const int m = blockIdx.x / p.H_kv, hk = blockIdx.x % p.H_kv;
-    if (m >= p.plan->merges) return;
-    const ChunkMerge g = p.merges[m];
-    const int row = blockIdx.y * kMergeRows + threadIdx.x % kMergeRows, cg = threadIdx.x / kMergeRows;
-    const int rows = g.tile.ntok * p.group;
-    if (blockIdx.y * kMergeRows >= rows) return;
-    const bool live = row < rows;
-    const int r = live ? row : 0;
-    float M[2] = {kChunkNoMax, kChunkNoMax}, l[2] = {0.f, 0.f};
-    float o[2][4] = {};
-    for (int s = 0; s < g.count; ++s) {
-        const int64_t item = (int64_t)(g.slot + s) * p.H_kv + hk;
+    const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
+    const int blocks = (p.rows + kMergeRows - 1) / kMergeRows, work = p.plan->merges * blocks;
+    for (int w = blockIdx.x; w < work; w += gridDim.x) {
+        const ChunkMerge g = p.merges[w / blocks];
+        const int row = w % blocks * kMergeRows + lane, rows = g.tile.ntok * p.group;
+        if (w % blocks * kMergeRows >= rows) continue;
+        const int r = min(row, rows - 1);
+        float M[2] = {kChunkNoMax, kChunkNoMax}, l[2] = {0.f, 0.f};
+        float4 o[2][4];
 #pragma unroll
-        for (int k = 0; k < 2; ++k) {
-            const float2 st = *reinterpret_cast<const float2*>(p.part_stats + ((item * 2 + k) * p.rows + r) * 2);
-            const float4 v = *reinterpret_cast<const float4*>(p.part_o + (((item * 2 + k) * CG + cg) * p.rows + r) * 4);
-            const float n = fmaxf(M[k], st.x), a = fast_exp2(M[k] - n), c = fast_exp2(st.x - n);
-            M[k] = n;
-            l[k] = l[k] * a + st.y * c;
-            o[k][0] = o[k][0] * a + v.x * c;
-            o[k][1] = o[k][1] * a + v.y * c;
-            o[k][2] = o[k][2] * a + v.z * c;
-            o[k][3] = o[k][3] * a + v.w * c;
+        for (int k = 0; k < 2; ++k)
+#pragma unroll
+            for (int c = 0; c < 4; ++c) o[k][c] = make_float4(0.f, 0.f, 0.f, 0.f);
+#pragma unroll 2
+        for (int s = 0; s < g.count; ++s) {
+            const int64_t item = g.slot + s;
+            float2 ml[2];
+            float4 v[2][4];
+#pragma unroll
+            for (int k = 0; k < 2; ++k) {
+                ml[k] = *reinterpret_cast<const float2*>(p.part_stats + ((item * 2 + k) * p.rows + r) * 2);
+#pragma unroll
+                for (int c = 0; c < 4; ++c)
+                    v[k][c] = *reinterpret_cast<const float4*>(
+                        p.part_o + (((item * 2 + k) * CG + warp * 4 + c) * p.rows + r) * 4);
+            }
+#pragma unroll
+            for (int k = 0; k < 2; ++k) {
+                const float n = fmaxf(M[k], ml[k].x), a = fast_exp2(M[k] - n), b = fast_exp2(ml[k].x - n);
+                M[k] = n;
+                l[k] = l[k] * a + ml[k].y * b;
+#pragma unroll
+                for (int c = 0; c < 4; ++c) {
+                    float4& x = o[k][c];
+                    x.x = x.x * a + v[k][c].x * b;
+                    x.y = x.y * a + v[k][c].y * b;
+                    x.z = x.z * a + v[k][c].z * b;
+                    x.w = x.w * a + v[k][c].w * b;
+                }
+            }
+        }
+        // A row that sees no key has l = 0 and gives zeros; a NaN sum stays one.
+        const float i1 = l[0] != 0.f ? p.v_scale / l[0] : 0.f, i2 = l[1] != 0.f ? p.lambda * p.v_scale / l[1] : 0.f;
+        float x[16], ss = 0.f;
+#pragma unroll
+        for (int c = 0; c < 4; ++c) {
+            x[4 * c] = o[0][c].x * i1 - o[1][c].x * i2;
+            x[4 * c + 1] = o[0][c].y * i1 - o[1][c].y * i2;
+            x[4 * c + 2] = o[0][c].z * i1 - o[1][c].z * i2;
+            x[4 * c + 3] = o[0][c].w * i1 - o[1][c].w * i2;
+        }
+#pragma unroll
+        for (int i = 0; i < 16; ++i) ss = fmaf(x[i], x[i], ss);
+        __syncthreads();  // the previous round's readers are done
+        red[warp][lane] = ss;
+        __syncthreads();
+        ss = 0.f;
+#pragma unroll
+        for (int i = 0; i < WARPS; ++i) ss += red[i][lane];
+        if (row >= rows) continue;
+        const float sc = ss == 0.f ? 0.f : (1.0f - p.lambda_init) / sqrtf(ss / (float)DV + p.eps);
+#pragma unroll
+        for (int i = 0; i < 16; ++i) x[i] *= p.norm_w ? sc * p.norm_w[warp * 16 + i] : sc;
+        const int64_t at = ((int64_t)(g.tile.t0 + r / p.group) * p.H + g.hk * p.group + r % p.group) * DV + warp * 16;
+        if (p.out_bf16 || p.out_f16) {
+            const bool f16 = p.out_f16 != 0;
+            uint4* dst = reinterpret_cast<uint4*>(static_cast<uint16_t*>(p.out) + at);
+#pragma unroll
+            for (int i = 0; i < 2; ++i)
+                dst[i] = make_uint4(pack_16x2(x[8 * i], x[8 * i + 1], f16), pack_16x2(x[8 * i + 2], x[8 * i + 3], f16),
+                                    pack_16x2(x[8 * i + 4], x[8 * i + 5], f16), pack_16x2(x[8 * i + 6], x[8 * i + 7], f16));
+        } else {
+            float4* dst = reinterpret_cast<float4*>(static_cast<float*>(p.out) + at);
+#pragma unroll
+            for (int i = 0; i < 4; ++i) dst[i] = make_float4(x[4 * i], x[4 * i + 1], x[4 * i + 2], x[4 * i + 3]);
         }
     }
-    // A row that sees no key has l = 0 and gives zeros.
-    const float i1 = l[0] > 0.f ? p.v_scale / l[0] : 0.f, i2 = l[1] > 0.f ? p.lambda * p.v_scale / l[1] : 0.f;
-    float x[4], ss = 0.f;
-#pragma unroll
-    for (int i = 0; i < 4; ++i) {
-        x[i] = o[0][i] * i1 - o[1][i] * i2;
-        ss = fmaf(x[i], x[i], ss);
-    }
-    red[cg][threadIdx.x % kMergeRows] = ss;
-    __syncthreads();
-    float tot = 0.f;
-#pragma unroll 8
-    for (int c = 0; c < CG; ++c) tot += red[c][threadIdx.x % kMergeRows];
-    if (!live) return;
-    const float sc = (1.0f - p.lambda_init) / sqrtf(tot / (float)DV + p.eps);
-#pragma unroll
-    for (int i = 0; i < 4; ++i) x[i] *= tot > 0.f ? sc : 0.f;
-    if (p.norm_w) {
-        const float4 wv = *reinterpret_cast<const float4*>(p.norm_w + cg * 4);
-        x[0] *= wv.x; x[1] *= wv.y; x[2] *= wv.z; x[3] *= wv.w;
-    }
-    const int64_t at = ((int64_t)(g.tile.t0 + row / p.group) * p.H + hk * p.group + row % p.group) * DV + cg * 4;
-    if (p.out_bf16 || p.out_f16)
-        *reinterpret_cast<uint2*>(static_cast<uint16_t*>(p.out) + at) =
-            make_uint2(pack_16x2(x[0], x[1], p.out_f16 != 0), pack_16x2(x[2], x[3], p.out_f16 != 0));
-    else
-        *reinterpret_cast<float4*>(static_cast<float*>(p.out) + at) = make_float4(x[0], x[1], x[2], x[3]);
 }
 
 }  // namespace
@@ -242,9 +316,13 @@ cudaError_t launch_chunk_plan(const ChunkParams& p, cudaStream_t stream) {
 }
 
 cudaError_t launch_chunk_merge(const ChunkParams& p, cudaStream_t stream) {
-    const dim3 grid(p.max_merges * p.H_kv, (p.rows + kMergeRows - 1) / kMergeRows);
-    if (p.Dv == 128) return launch_pdl(chunk_merge_kernel<128>, grid, dim3(kMergeRows * 32), 0, stream, p);
-    return launch_pdl(chunk_merge_kernel<256>, grid, dim3(kMergeRows * 64), 0, stream, p);
+    int sms = 0;
+    const cudaError_t e = device_sm_count(&sms);
+    if (e != cudaSuccess) return e;
+    const int64_t most = (int64_t)p.max_merges * ((p.rows + kMergeRows - 1) / kMergeRows);
+    const dim3 grid((unsigned)(most < 4 * sms ? most : 4 * sms));  // one resident round at most
+    return p.Dv == 128 ? launch_pdl(chunk_merge_kernel<128>, grid, dim3(256), 0, stream, p)
+                       : launch_pdl(chunk_merge_kernel<256>, grid, dim3(512), 0, stream, p);
 }
 
 }  // namespace da

@@ -7,9 +7,9 @@
 // then the head's RMSNorm and the (1 - lambda_init) scale; the mathematics, the two
 // running softmax states and their lazily moved maxima are those of fwd_tcgen05.cu.
 //
-// A CTA works on one entry of the plan (chunk_plan.cu) and one KV head: 128 query
-// rows = tm consecutive tokens x the query heads that share the KV head (row r is
-// token r / group, head r % group), and a range of 128-key tiles. Packing the heads
+// A CTA works on one entry of the plan (chunk_plan.cu): 128 query rows = tm
+// consecutive tokens x the query heads that share one KV head (row r is token
+// r / group, head r % group), and a range of 128-key tiles. Packing the heads
 // of a group into the rows reads each K/V tile once for all of them and fills the
 // 128 MMA rows with few tokens. Rows past the entry's tokens compute on whatever
 // follows in Q (rows are independent) and are not stored.
@@ -53,7 +53,7 @@ struct Cfg {
     // Register split (see fwd_tcgen05.cu): the softmax warpgroups' share plus the others' must
     // not exceed what the block was launched with, or setmaxnreg.inc would wait forever.
     static constexpr int kRegsLaunch = FP8 ? 128 : 168;
-    static constexpr int kRegsSoftmax = FP8 ? 192 : 224, kRegsOther = FP8 ? 64 : 56;
+    static constexpr int kRegsSoftmax = FP8 ? 192 : 208, kRegsOther = FP8 ? 64 : 88;
     static_assert(2 * 128 * kRegsSoftmax + (kThreads - 256) * kRegsOther <= kThreads * kRegsLaunch, "register split");
     static constexpr int kQBytes = BM * D * 2, kKBytes = BN * D * 2, kVBytes = BN * DV * 2;
     static constexpr int kBoxBytes = 128 * 128;   // [128 rows][64 16-bit values], 128-byte swizzle
@@ -80,6 +80,7 @@ struct Bars {
     uint64_t drain;
     uint32_t tmem_base;
     int abort;
+    ChunkEntry e;
 };
 static_assert(sizeof(Bars) <= 256, "barrier block fits its reserve");
 
@@ -152,9 +153,11 @@ __global__ void __launch_bounds__(Cfg<FP8>::kThreads, 1) chunk_kernel(const __gr
     }
     pdl_trigger();
     pdl_wait();  // the plan, Q and the newest cache rows come from earlier kernels
-    const int ei = blockIdx.x / p.H_kv, hk = blockIdx.x % p.H_kv;
-    if (ei >= p.plan->entries) return;  // every thread of the CTA
-    const ChunkEntry e = p.entries[ei];
+    const ChunkPlan plan = *p.plan;
+    const int ei = (int)(blockIdx.x);
+    if (ei >= plan.upto[3]) return;  // every thread of the CTA
+    // The entry lives in shared memory, so that the softmax loop keeps its registers for scores.
+    if (threadIdx.x == 0) bars->e = p.entries[chunk_entry(plan.upto, p.max_entries, ei)];
     if (warp == kWarpMma) {
         tmem_alloc(&bars->tmem_base, C::kTmemCols);
         tmem_relinquish();
@@ -163,17 +166,19 @@ __global__ void __launch_bounds__(Cfg<FP8>::kThreads, 1) chunk_kernel(const __gr
     __syncthreads();
     tc_fence_after();
     const uint32_t tmem = bars->tmem_base;
+    const ChunkEntry& e = bars->e;
 
     uint8_t* q1s = smem + C::kOffQ1;
     uint8_t* q2s = smem + C::kOffQ2;
     uint8_t* stages = smem + C::kOffStages;
     const int nkv = e.nkt;
-    const int key_end = e.tile.pos0 + e.tile.ntok;              // keys that the tile's last token sees
-    const int last = nkv - 1;
-    const int tail_row = key_end - (e.kt0 + last) * BN;          // first hidden row of the last key tile
-    const bool tail = nkv > 0 && tail_row < BN;
 
     if (warp >= 8) {
+        const int hk = e.hk;
+        const int key_end = e.tile.pos0 + e.tile.ntok;      // keys that the tile's last token sees
+        const int last = nkv - 1;
+        const int tail_row = key_end - (e.kt0 + last) * BN;  // first hidden row of the last key tile
+        const bool tail = nkv > 0 && tail_row < BN;
         setmaxnreg_dec<C::kRegsOther>();
         if (warp == kWarpProducer) {
             // ------------------------------------------------------------ producer
@@ -379,9 +384,10 @@ __global__ void __launch_bounds__(Cfg<FP8>::kThreads, 1) chunk_kernel(const __gr
         const uint32_t lane_base = tmem + ((uint32_t)(lg * 32) << 16);
         const uint32_t tS = lane_base + C::kColS + g * BN;
         const uint32_t tO = lane_base + C::kColO + g * DV;
-        const float sl2 = g == 0 ? p.scale1_log2 : p.scale2_log2;
-        const int rows = e.tile.ntok * p.group;
-        const int lim = r < rows ? e.tile.pos0 + r / p.group + 1 : 0;  // keys that this row sees
+        // (A bf16 cache has one score scale for both maps: a kernel constant in the loop's FMAs.)
+        const float sl2 = !FP8 || g == 0 ? p.scale1_log2 : p.scale2_log2;
+        const int pos0 = e.tile.pos0, kb0 = e.kt0 * BN;
+        const int lim = r < e.tile.ntok * p.group ? pos0 + r / p.group + 1 : 0;  // keys that this row sees
         float m_used = kChunkNoMax, l = 0.f;
         bool ok = true;
 
@@ -395,8 +401,8 @@ __global__ void __launch_bounds__(Cfg<FP8>::kThreads, 1) chunk_kernel(const __gr
 #pragma unroll
             for (int c = 0; c < BN / 32; ++c) tmem_ld32(tS + c * 32, sr + c * 32);
             tmem_ld_wait();
-            const int kbase = (e.kt0 + j) * BN;
-            if (kbase + BN - 1 > e.tile.pos0) {
+            const int kbase = kb0 + j * BN;
+            if (kbase + BN - 1 > pos0) {
 #pragma unroll
                 for (int i = 0; i < BN; ++i)
                     if (kbase + i >= lim) sr[i] = __float_as_uint(-INFINITY);
@@ -409,14 +415,13 @@ __global__ void __launch_bounds__(Cfg<FP8>::kThreads, 1) chunk_kernel(const __gr
                 mx2 = fmax3(mx2, __uint_as_float(sr[i + 4]), __uint_as_float(sr[i + 5]));
                 mx3 = fmax3(mx3, __uint_as_float(sr[i + 6]), __uint_as_float(sr[i + 7]));
             }
-            // A row that has seen no key keeps the finite floor kChunkNoMax, so that its weights
-            // are exp2(-inf) = 0 and a later maximum rescales its empty sums by 0.
+            // The maximum starts at the finite floor kChunkNoMax: a row that has seen no key keeps it,
+            // so that its weights are exp2(-inf) = 0, and its first real maximum rescales the empty
+            // sums by exp2(floor - max) = 0.
             const float m_new = fmax3(fmaxf(mx0, mx1), mx2, mx3) * sl2;
             float alpha = 1.f;
             bool rescale = false;
-            if (j == 0) {
-                m_used = fmaxf(m_new, kChunkNoMax);
-            } else if (r < rows && m_new > m_used + kRescaleThreshold) {
+            if (m_new > m_used + kRescaleThreshold) {
                 alpha = fast_exp2(m_used - m_new);
                 m_used = m_new;
                 rescale = true;
@@ -464,10 +469,11 @@ __global__ void __launch_bounds__(Cfg<FP8>::kThreads, 1) chunk_kernel(const __gr
                  mbar_wait_warp(&bars->o_done[1], (nkv - 1) & 1, abort_flag, p.err, 0x45);
         }
         tc_fence_after();
+        const int rows = e.tile.ntok * p.group, hk = e.hk;
         if (e.slot >= 0) {
             // Partial state of map g: this thread's row.
             if (ok) {
-                const int64_t item = (int64_t)e.slot * p.H_kv + hk;
+                const int64_t item = e.slot;
                 float* o = p.part_o + (item * 2 + g) * (DV / 4) * p.rows * 4 + r * 4;
 #pragma unroll 1
                 for (int c = 0; c < DV / 32; ++c) {
@@ -572,7 +578,7 @@ cudaError_t launch_t(const ChunkParams& p, cudaStream_t stream) {
     // The register split assumes the compiled per-thread count.
     const cudaError_t e = prepare_once<chunk_kernel<FP8>>((int)C::kSmem, C::kRegsLaunch);
     if (e != cudaSuccess) return e;
-    return launch_pdl(chunk_kernel<FP8>, dim3((unsigned)(p.max_entries * p.H_kv)), dim3(C::kThreads), C::kSmem, stream, p);
+    return launch_pdl(chunk_kernel<FP8>, dim3((unsigned)p.max_entries), dim3(C::kThreads), C::kSmem, stream, p);
 }
 
 }  // namespace

@@ -136,25 +136,26 @@ cudaError_t launch_append_chunk(AppendChunkParams p, cudaStream_t stream);
 // Attention of ragged new tokens over a paged cache (chunk_plan.cu, chunk_tcgen05.cu, chunk_pair_tcgen05.cu).
 //
 // A tile is up to 128 query rows of one sequence: `tm` consecutive tokens x the `group` query
-// heads that share one KV head. An entry is a tile and a range of its key tiles (128 keys each);
-// every entry stands for H_kv work items, one per KV head. A tile whose keys are split over
-// several entries leaves partial states in slots, which the merge kernel joins.
+// heads that share one KV head; an item is a tile and a KV head; an entry is an item and a range
+// of its key tiles (128 keys each), the work of one CTA (or CTA pair). An item whose keys are
+// split over several entries leaves partial states in slots, which the merge kernel joins.
 struct ChunkTile {
     int b, t0, ntok, pos0;  // sequence, first token row, tokens, position of the first token (may be negative)
 };
 struct ChunkEntry {
     ChunkTile tile;
     int kt0, nkt;  // key tiles [kt0, kt0 + nkt)
-    int slot;      // partial-state slot, or -1: the entry finishes its tile
-    int pad;
+    int slot;      // partial-state slot, or -1: the entry finishes its item
+    int hk;        // KV head
 };
 struct ChunkMerge {
     ChunkTile tile;
     int slot, count;  // slots [slot, slot + count)
-    int pad[2];
+    int hk, pad;
 };
 struct ChunkPlan {
-    int tiles, entries, merges, keys_per_entry;
+    int upto[4];  // entries of the longest class, of the two longest, ...; the last one: all
+    int tiles, merges, keys, pad;  // keys: key tiles per entry at most
 };
 struct ChunkParams {
     CUtensorMap tm_q1, tm_q2;        // 4-D maps [H_kv][T][group][d], boxes of 64 channels x group x tm
@@ -170,18 +171,26 @@ struct ChunkParams {
     // Plan and partial states in the workspace, and their host-known bounds.
     ChunkPlan* plan;
     ChunkTile* tiles;
-    ChunkEntry* entries;
+    ChunkEntry* entries;  // [2][max_entries]: two lists of two classes of length each (chunk_entry below)
     ChunkMerge* merges;
-    float* part_stats;  // [slot][H_kv][2][rows][2]: running max (log2 units) and sum of each map
-    float* part_o;      // [slot][H_kv][2][Dv / 4][rows][4]
-    int max_tiles, max_entries, max_slots, max_merges, rows, ctas;  // ctas: work items that run at once
+    float* part_stats;  // [slot][2][rows][2]: running max (log2 units) and sum of each map
+    float* part_o;      // [slot][2][Dv / 4][rows][4]
+    int max_tiles, max_entries, max_slots, max_merges, rows, ctas;  // ctas: entries that run at once
 };
+// Entry i of the plan, longest class first: each list holds one class from its front and one from
+// its back.
+__host__ __device__ __forceinline__ int64_t chunk_entry(const int* upto, int max_entries, int i) {
+    if (i < upto[0]) return i;
+    if (i < upto[1]) return max_entries - 1 - (i - upto[0]);
+    if (i < upto[2]) return (int64_t)max_entries + (i - upto[1]);
+    return 2 * (int64_t)max_entries - 1 - (i - upto[2]);
+}
 constexpr int kChunkRows = 128, kChunkKeys = 128;
 constexpr float kChunkNoMax = -1e30f;  // running maximum (log2 units) of a row that has seen no key
 cudaError_t launch_chunk_plan(const ChunkParams& p, cudaStream_t stream);
+cudaError_t launch_chunk_merge(const ChunkParams& p, cudaStream_t stream);
 cudaError_t launch_chunk_64(const ChunkParams& p, cudaStream_t stream);     // d = 64, Dv = 128
 cudaError_t launch_chunk_pair(const ChunkParams& p, cudaStream_t stream);   // d = 128, Dv = 256
-cudaError_t launch_chunk_merge(const ChunkParams& p, cudaStream_t stream);
 
 struct AddNormParams {
     const void* x;        // [M, N] bf16 or fp32 (x_f32)
