@@ -1057,9 +1057,10 @@ diffattn_status chunk_paged(bool fp8, const float* scales, diffattn_tensor q1, d
     p.norm_w = norm_weight;
     p.lambda = lambda; p.lambda_init = lambda_init; p.eps = eps;
     const double sl2 = 1.4426950408889634 / sqrt((double)d);
-    p.scale1_log2 = (float)(sl2 * (fp8 ? scales[0] : 1.f));
-    p.scale2_log2 = (float)(sl2 * (fp8 ? scales[1] : 1.f));
-    p.v_scale = fp8 ? scales[2] : 1.f;
+    // The fp8 kernels' operands are the stored values times 2^-8.
+    p.scale1_log2 = (float)(fp8 ? sl2 * scales[0] * 256.0 : sl2);
+    p.scale2_log2 = (float)(fp8 ? sl2 * scales[1] * 256.0 : sl2);
+    p.v_scale = fp8 ? (float)(scales[2] * 256.0) : 1.f;
     uint8_t* ws = static_cast<uint8_t*>(workspace);
     p.err = err_word(workspace);
     p.plan = reinterpret_cast<ChunkPlan*>(ws + kControlBytes);

@@ -1,0 +1,86 @@
+// What the chunk attention's kernels do for an fp8 (e4m3) cache. The operands of one
+// tensor-core product have one type; every e4m3 value is an fp16 value, and a bf16 query
+// row becomes one of fp16 times a power of two, which goes into the row's score scale.
+// So K and V are brought into shared memory raw and rewritten as fp16 by a warpgroup,
+// and P is fp16, eight times finer than bf16.
+//
+// As fp16 the bits s eeee mmm of an e4m3 value, the magnitude moved to bits 7 .. 13 and
+// the sign to bit 15, are the value times 2^-8, subnormals included (their exponent bias
+// differs by 8), so a pair takes four integer instructions and no arithmetic; the factor
+// 2^8 goes into the score scales and V's. (NaN codes come out as +-480: cached values are
+// finite.)
+//
+// What the path cost on the way, 16 sequences x 5 drafted tokens over 8192 keys, 16
+// query and 8 KV heads: K to bf16 beside a bf16 query 217 us, K to fp16 by the
+// conversion instruction 205, by integers 197, eight chunks of a thread loaded before the
+// first is stored 164, the same in loops small enough for the instruction cache 153, warps
+// without rows kept out 144. What bounds it now is shared memory: a key tile is written
+// raw (32 KB), read (32 KB), written as fp16 (64 KB) and read by the products (128 KB),
+// 2,000 of its 3,800 cycles at the full rate, with the products and the conversion
+// colliding; a bf16 cache's tile moves 192 KB in 2,500.
+#pragma once
+
+#include "common.cuh"
+
+namespace da {
+
+// fp8 cache: a query row of D bf16 values as fp16 values of the same row times 2^shift, in
+// place in its swizzled boxes, by the thread that owns the row; returns 2^-shift. The row's
+// largest exponent goes to 2^15, so nothing overflows, and what falls below fp16's normal
+// range is smaller than the row's maximum by 2^-29 and more: less than the fp32 sums of the
+// scores keep. (Rows below 2^-85 keep a factor of 2^100: their scores are 0 either way.)
+template <int D>
+__device__ __forceinline__ float q_row_to_f16(uint8_t* boxes, int r) {
+    uint32_t m = 0;  // largest magnitude of a packed pair's halves
+#pragma unroll
+    for (int c = 0; c < D / 8; ++c) {
+        const uint4 v = *reinterpret_cast<const uint4*>(boxes + (c >> 3) * (128 * 128) + sw128_offset(r, c & 7));
+        const uint32_t w[4] = {v.x, v.y, v.z, v.w};
+#pragma unroll
+        for (int i = 0; i < 4; ++i) m = max(m, max(w[i] & 0x7fffu, (w[i] >> 16) & 0x7fffu));
+    }
+    const int shift = min(142 - (int)(m >> 7), 100);
+    const float up = __uint_as_float((uint32_t)(127 + shift) << 23);
+#pragma unroll
+    for (int c = 0; c < D / 8; ++c) {
+        uint4* at = reinterpret_cast<uint4*>(boxes + (c >> 3) * (128 * 128) + sw128_offset(r, c & 7));
+        const uint4 v = *at;
+        *at = make_uint4(pack_f16x2(bf16lo_to_f32(v.x) * up, bf16hi_to_f32(v.x) * up),
+                         pack_f16x2(bf16lo_to_f32(v.y) * up, bf16hi_to_f32(v.y) * up),
+                         pack_f16x2(bf16lo_to_f32(v.z) * up, bf16hi_to_f32(v.z) * up),
+                         pack_f16x2(bf16lo_to_f32(v.w) * up, bf16hi_to_f32(v.w) * up));
+    }
+    fence_proxy_async_shared();  // before the score products read the row
+    return __uint_as_float((uint32_t)(127 - shift) << 23);
+}
+
+// Sixteen e4m3 values (raw chunk c of row r) as fp16 values times 2^-8, exactly, into their two
+// chunks of a swizzled box.
+__device__ __forceinline__ void put_e4m3x16(uint8_t* box, int r, int c, uint4 x) {
+    const uint32_t w[4] = {x.x, x.y, x.z, x.w};
+    uint32_t y[8];
+#pragma unroll
+    for (int i = 0; i < 4; ++i)
+#pragma unroll
+        for (int h = 0; h < 2; ++h) {
+            const uint32_t b = __byte_perm(w[i], 0, h ? 0x4342 : 0x4140);  // a byte in the low half of each 16 bits
+            y[2 * i + h] = (b + (b & 0x00800080u)) << 7;                   // the sign bit, doubled, moves one further
+        }
+    *reinterpret_cast<uint4*>(box + sw128_offset(r, 2 * c)) = make_uint4(y[0], y[1], y[2], y[3]);
+    *reinterpret_cast<uint4*>(box + sw128_offset(r, 2 * c + 1)) = make_uint4(y[4], y[5], y[6], y[7]);
+}
+
+// Four raw chunks, `step` bytes and `rows` rows apart, all loaded before the first is stored; rows
+// from `hidden` on become zeros.
+__device__ __forceinline__ void convert4(const uint8_t* raw, int step, uint8_t* box, int r, int rows, int c, int hidden) {
+    uint4 x[4];
+#pragma unroll
+    for (int u = 0; u < 4; ++u) x[u] = *reinterpret_cast<const uint4*>(raw + u * step);
+#pragma unroll
+    for (int u = 0; u < 4; ++u) {
+        if (r + u * rows >= hidden) x[u] = make_uint4(0, 0, 0, 0);
+        put_e4m3x16(box, r + u * rows, c, x[u]);
+    }
+}
+
+}  // namespace da

@@ -11,15 +11,15 @@
 //
 // Warps: 0 TMA producer, 1 MMA issuer, 2..5 softmax and epilogue, then with a bf16
 // cache 6 (clears V rows behind the last visible key), with an fp8 cache 6..9, which
-// convert e4m3 tiles (K to bf16, V to fp16, exactly).
+// convert e4m3 tiles to fp16 (chunk_fp8.cuh).
 //
 // fp8 cache: K tiles (two pages) and V half tiles (one page) are 16 KB raw units in
 // one ring, loaded and converted in the order in which the MMAs consume them:
 // K(0) K(1) V(0a) V(0b) K(2) V(1a) V(1b) K(3) ..; any other order could leave the
 // MMA warp waiting for a K tile behind a V tile whose buffer it has not freed yet.
-#include <cuda_fp8.h>
 #include <math.h>
 
+#include "chunk_fp8.cuh"
 #include "common.cuh"
 #include "kernels.h"
 
@@ -54,7 +54,7 @@ struct Cfg {
 };
 
 struct Bars {
-    uint64_t q_full;
+    uint64_t q_full, q_ready;  // landed; fp8: converted by the softmax warps
     uint64_t k_full[2], k_empty[2];
     uint64_t v_full[4], v_empty[4];
     uint64_t raw_full[4], raw_empty[4];
@@ -67,8 +67,9 @@ struct Bars {
 };
 static_assert(sizeof(Bars) <= 320, "barrier block");
 
+template <bool FP8>
 __device__ __forceinline__ void issue_qk(uint32_t s_tmem, uint64_t q_desc, uint64_t k_desc) {
-    constexpr uint32_t idesc = idesc_bf16_f32(BM, BN, 0, 0);
+    constexpr uint32_t idesc = idesc_kind_f16(BM, BN, 0, 0, FP8);
 #pragma unroll
     for (int kk = 0; kk < D / 16; ++kk) {
         const uint64_t off = (uint64_t)(((kk >> 2) * (128 * 128) + (kk & 3) * 32) >> 4);
@@ -84,22 +85,6 @@ __device__ __forceinline__ void issue_pv_half(uint32_t o_tmem, uint32_t p_tmem, 
     for (int k = 0; k < BN / 32; ++k) {
         const int kk = half * (BN / 32) + k;
         umma_ts(o_tmem, p_tmem + kk * 8, vh_desc + (uint64_t)(k * 128), idesc, (acc || kk > 0) ? 1u : 0u);
-    }
-}
-
-__device__ __forceinline__ void e4m3x4_to_f16(uint32_t w, uint32_t* out) {
-    const __half2_raw lo = __nv_cvt_fp8x2_to_halfraw2((__nv_fp8x2_storage_t)(w & 0xffffu), __NV_E4M3);
-    const __half2_raw hi = __nv_cvt_fp8x2_to_halfraw2((__nv_fp8x2_storage_t)(w >> 16), __NV_E4M3);
-    out[0] = (uint32_t)lo.x | ((uint32_t)lo.y << 16);
-    out[1] = (uint32_t)hi.x | ((uint32_t)hi.y << 16);
-}
-__device__ __forceinline__ void e4m3x4_to_bf16(uint32_t w, uint32_t* out) {
-    uint32_t h[2];
-    e4m3x4_to_f16(w, h);
-#pragma unroll
-    for (int i = 0; i < 2; ++i) {
-        const float2 f = __half22float2(*reinterpret_cast<const __half2*>(&h[i]));
-        out[i] = pack_bf16x2(f.x, f.y);
     }
 }
 
@@ -131,6 +116,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(Cfg<FP8>::kThreads, 
 
     if (threadIdx.x == 0) {
         mbar_init(&bars->q_full, 1);
+        mbar_init(&bars->q_ready, 4);
         for (int s = 0; s < 2; ++s) {
             mbar_init(&bars->k_full[s], FP8 ? 4 : 1);  // fp8: one arrival per converting warp
             mbar_init(&bars->k_empty[s], 1);
@@ -291,14 +277,14 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(Cfg<FP8>::kThreads, 
             if (!mbar_wait_warp(&bars->k_full[sk], (j / C::kKStages) & 1, abort_flag, p.err, 0x55)) return false;
             tc_fence_after();
             if (elect_one()) {
-                issue_qk(tS[j & 1], dq, dk0 + sk * kKStep);
+                issue_qk<FP8>(tS[j & 1], dq, dk0 + sk * kKStep);
                 umma_commit(&bars->s_full[j & 1]);
                 umma_commit(&bars->k_empty[sk]);
             }
             __syncwarp();
             return true;
         };
-        bool go = nkv > 0 && mbar_wait_warp(&bars->q_full, 0, abort_flag, p.err, 0x54) && issue_s(0) &&
+        bool go = nkv > 0 && mbar_wait_warp(FP8 ? &bars->q_ready : &bars->q_full, 0, abort_flag, p.err, 0x54) && issue_s(0) &&
                   (nkv < 2 || issue_s(1));
         for (int j = 0; go && j < nkv; ++j) {
             const int bf = j & 1;
@@ -332,14 +318,28 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(Cfg<FP8>::kThreads, 
         const int r = lg * 32 + lane;  // query row within the tile == TMEM lane
         const uint32_t lane_base = tmem + ((uint32_t)(lg * 32) << 16);
         const uint32_t tO = lane_base + C::kColO;
-        const float sl2 = rank ? p.scale2_log2 : p.scale1_log2;
+        float sl2 = rank ? p.scale2_log2 : p.scale1_log2;
+        if (FP8 && nkv > 0) {
+            ok = mbar_wait_warp(&bars->q_full, 0, abort_flag, p.err, 0x69);
+            if (ok) sl2 *= q_row_to_f16<D>(qs, r);
+            __syncwarp();
+            if (lane == 0) mbar_arrive(&bars->q_ready);
+        }
         const int lim = r < rows ? e.tile.pos0 + r / p.group + 1 : 0;  // keys that this row sees
-        for (int j = 0; j < nkv; ++j) {
+        const bool idle = lg * 32 >= rows;  // no row of the warp belongs to the entry: see chunk_tcgen05.cu
+        for (int j = 0; ok && j < nkv; ++j) {
             const int bf = j & 1;
             const uint32_t tS = lane_base + bf * BN;
             if (!mbar_wait_warp(&bars->s_full[bf], (j >> 1) & 1, abort_flag, p.err, 0x60)) {
                 ok = false;
                 break;
+            }
+            if (idle) {
+                if (lane == 0) {
+                    mbar_arrive(&bars->p_half[bf]);
+                    mbar_arrive(&bars->p_full[bf]);
+                }
+                continue;
             }
             tc_fence_after();
             uint32_t sr[BN];
@@ -426,7 +426,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(Cfg<FP8>::kThreads, 
             }
         }
     } else {
-        // ------------------------------------------------------------ e4m3 -> bf16 (K), fp16 (V)
+        // ------------------------------------------------------------ e4m3 -> fp16
         const int ct = (warp - kWarpExtra) * 32 + lane;
         int n = 0;
         auto raw_unit = [&]() -> const uint8_t* {
@@ -443,11 +443,6 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(Cfg<FP8>::kThreads, 
             }
             ++n;
         };
-        // 16 values of one row (raw chunk c of 16 bytes) as two swizzled 16-byte chunks of a box.
-        auto put = [&](uint8_t* box, int r, int c, const uint32_t* y) {
-            *reinterpret_cast<uint4*>(box + sw128_offset(r, 2 * c)) = make_uint4(y[0], y[1], y[2], y[3]);
-            *reinterpret_cast<uint4*>(box + sw128_offset(r, 2 * c + 1)) = make_uint4(y[4], y[5], y[6], y[7]);
-        };
         for_units(
             nkv,
             [&](int j) {
@@ -455,18 +450,12 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(Cfg<FP8>::kThreads, 
                 const int s = j % C::kKStages;
                 if (!raw || !mbar_wait_warp(&bars->k_empty[s], ((j / C::kKStages) & 1) ^ 1, abort_flag, p.err, 0x5e))
                     return false;
-                // [128 rows][128 bytes] -> two boxes of 64 channels. Lanes 4..7 of eight take the next
-                // row's other box: neither loads nor swizzled stores of a quarter warp meet in a bank.
-#pragma unroll 4
-                for (int i = ct; i < BN * 8; i += 128) {
-                    const int in = i % 16, box = (in / 4 + in / 8) & 1, r = 2 * (i / 16) + ((in / 4) & 1), c = in % 4;
-                    const uint4 x = *reinterpret_cast<const uint4*>(raw + r * D + box * 64 + c * 16);
-                    const uint32_t w[4] = {x.x, x.y, x.z, x.w};
-                    uint32_t y[8];
-#pragma unroll
-                    for (int k = 0; k < 4; ++k) e4m3x4_to_bf16(w[k], y + 2 * k);
-                    put(ks + s * C::kKBytes + box * C::kBoxBytes, r, c, y);
-                }
+                // [128 rows][128 bytes] -> two boxes of 64 channels. Lanes 4..7 of eight take the next row's
+                // other box: neither loads nor swizzled stores of a quarter warp meet in a bank.
+                const int in = ct % 16, box = (in / 4 + in / 8) & 1, r0 = 2 * (ct / 16) + ((in / 4) & 1), c = in % 4;
+#pragma unroll 1
+                for (int r = r0; r < BN; r += 64)
+                    convert4(raw + r * D + box * 64 + c * 16, 16 * D, ks + s * C::kKBytes + box * C::kBoxBytes, r, 16, c, BN);
                 done(&bars->k_full[s]);
                 return true;
             },
@@ -477,19 +466,11 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(Cfg<FP8>::kThreads, 
                     return false;
                 // [64 rows][256 bytes] -> four boxes of 64 columns, with the same lane order per box pair.
                 const int hidden = tail && u == tail_half ? (tail_row & 63) : 64;
-#pragma unroll 4
-                for (int i = ct; i < 64 * 16; i += 128) {
-                    const int in = i % 16, bp = (i / 16) & 1, box = 2 * bp + ((in / 4 + in / 8) & 1);
-                    const int r = 2 * (i / 32) + ((in / 4) & 1), c = in % 4;
-                    uint32_t y[8] = {0u, 0u, 0u, 0u, 0u, 0u, 0u, 0u};
-                    if (r < hidden) {
-                        const uint4 x = *reinterpret_cast<const uint4*>(raw + r * DV + box * 64 + c * 16);
-                        const uint32_t w[4] = {x.x, x.y, x.z, x.w};
-#pragma unroll
-                        for (int k = 0; k < 4; ++k) e4m3x4_to_f16(w[k], y + 2 * k);
-                    }
-                    put(vs + su * C::kVHBytes + box * 64 * 128, r, c, y);
-                }
+                const int in = ct % 16, box = 2 * ((ct / 16) & 1) + ((in / 4 + in / 8) & 1);
+                const int r0 = 2 * (ct / 32) + ((in / 4) & 1), c = in % 4;
+#pragma unroll 1
+                for (int r = r0; r < 64; r += 32)
+                    convert4(raw + r * DV + box * 64 + c * 16, 8 * DV, vs + su * C::kVHBytes + box * 64 * 128, r, 8, c, hidden);
                 done(&bars->v_full[su]);
                 return true;
             });

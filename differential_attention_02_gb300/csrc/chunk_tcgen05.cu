@@ -25,18 +25,17 @@
 // would still reach the output through P V, the V rows of the last page behind the
 // last visible key are cleared in shared memory before that product.
 //
-// fp8 cache: tensor-core operands of one product have one type and the query is
-// bf16, so e4m3 tiles are brought into shared memory raw and converted by a fourth
-// warpgroup into the tiles that the MMAs read: K to bf16 (the query's type), V to
-// fp16, both exactly. P is then fp16 as well, eight times finer than bf16. The K
-// scales go into the maps' score scales, V's into the epilogue.
+// fp8 cache: e4m3 tiles are brought into shared memory raw and a fourth warpgroup
+// converts them into the fp16 tiles that the MMAs read; the softmax warps convert the
+// query rows once (chunk_fp8.cuh). The K scales go into the maps' score scales, V's into
+// the epilogue.
 //
 // Entries that finish their tile store the output; the others leave per row and map
 // the unnormalised accumulator, running maximum and sum (columns in quartets, rows
 // innermost, so that a warp's 32 rows store 512 contiguous bytes).
-#include <cuda_fp8.h>
 #include <math.h>
 
+#include "chunk_fp8.cuh"
 #include "common.cuh"
 #include "kernels.h"
 
@@ -64,7 +63,7 @@ struct Cfg {
     static constexpr int kOffQ1 = 0, kOffQ2 = kQBytes, kOffStages = 2 * kQBytes;
     static constexpr int kOffRaw = kOffStages + kStages * kStageBytes;
     static constexpr int kOffBar = kOffRaw + kRawStages * kRawBytes;
-    static constexpr int kBarBytes = 256;
+    static constexpr int kBarBytes = 320;
     static constexpr size_t kSmem = 1024 + (size_t)kOffBar + kBarBytes;
     static_assert(kSmem <= 232448, "shared memory budget");
     static constexpr uint32_t kTmemCols = 512, kColS = 0, kColO = 2 * BN;
@@ -72,9 +71,10 @@ struct Cfg {
 };
 
 struct Bars {
-    uint64_t q_full;
-    uint64_t kv_full[3], kv_empty[3];
-    uint64_t raw_full[2], raw_empty[2];
+    uint64_t q_full, q_ready;  // landed; fp8: converted by the softmax warps
+    uint64_t kv_full[3], kv_empty[3];            // operand tiles (fp8: K1 and K2 only)
+    uint64_t v_full[2], v_empty[2];              // fp8: V tiles
+    uint64_t raw_full[2][2], raw_empty[2][2];    // fp8: e4m3 tiles, [stage][K, V]
     uint64_t s_full[2], p_half[2], p_full[2], o_done[2];
     uint64_t tail_full, tail_done;  // V of a last key tile that gets rows cleared: landed, cleared
     uint64_t drain;
@@ -82,10 +82,11 @@ struct Bars {
     int abort;
     ChunkEntry e;
 };
-static_assert(sizeof(Bars) <= 256, "barrier block fits its reserve");
+static_assert(sizeof(Bars) <= Cfg<true>::kBarBytes, "barrier block fits its reserve");
 
+template <bool FP8>
 __device__ __forceinline__ void issue_qk(uint32_t s_tmem, uint64_t q_desc, uint64_t k_desc) {
-    constexpr uint32_t idesc = idesc_bf16_f32(BM, BN, 0, 0);
+    constexpr uint32_t idesc = idesc_kind_f16(BM, BN, 0, 0, FP8);
 #pragma unroll
     for (int kk = 0; kk < D / 16; ++kk)
         umma_ss(s_tmem, q_desc + (uint64_t)(kk * 2), k_desc + (uint64_t)(kk * 2), idesc, kk > 0 ? 1u : 0u);
@@ -99,23 +100,6 @@ __device__ __forceinline__ void issue_pv_half(uint32_t o_tmem, uint32_t p_tmem, 
     for (int k = 0; k < BN / 32; ++k) {
         const int kk = half * (BN / 32) + k;
         umma_ts(o_tmem, p_tmem + kk * 8, v_desc + (uint64_t)(kk * 128), idesc, (acc || kk > 0) ? 1u : 0u);
-    }
-}
-
-// Four e4m3 values of a word as two 16-bit pairs, exactly.
-__device__ __forceinline__ void e4m3x4_to_f16(uint32_t w, uint32_t* out) {
-    const __half2_raw lo = __nv_cvt_fp8x2_to_halfraw2((__nv_fp8x2_storage_t)(w & 0xffffu), __NV_E4M3);
-    const __half2_raw hi = __nv_cvt_fp8x2_to_halfraw2((__nv_fp8x2_storage_t)(w >> 16), __NV_E4M3);
-    out[0] = (uint32_t)lo.x | ((uint32_t)lo.y << 16);
-    out[1] = (uint32_t)hi.x | ((uint32_t)hi.y << 16);
-}
-__device__ __forceinline__ void e4m3x4_to_bf16(uint32_t w, uint32_t* out) {
-    uint32_t h[2];
-    e4m3x4_to_f16(w, h);
-#pragma unroll
-    for (int i = 0; i < 2; ++i) {
-        const float2 f = __half22float2(*reinterpret_cast<const __half2*>(&h[i]));
-        out[i] = pack_bf16x2(f.x, f.y);
     }
 }
 
@@ -136,13 +120,19 @@ __global__ void __launch_bounds__(Cfg<FP8>::kThreads, 1) chunk_kernel(const __gr
             mbar_init(&bars->kv_empty[s], 1);
         }
         for (int s = 0; s < C::kRawStages; ++s) {
-            mbar_init(&bars->raw_full[s], 1);
-            mbar_init(&bars->raw_empty[s], 4);
+            mbar_init(&bars->v_full[s], 4);
+            mbar_init(&bars->v_empty[s], 1);
+            for (int u = 0; u < 2; ++u) {
+                mbar_init(&bars->raw_full[s][u], 1);
+                mbar_init(&bars->raw_empty[s][u], 4);
+            }
         }
         for (int g = 0; g < 2; ++g) {
             mbar_init(&bars->s_full[g], 1);
-            mbar_init(&bars->p_half[g], 4);  // one arrival per softmax warp
-            mbar_init(&bars->p_full[g], 4);
+            if (!FP8) {
+                mbar_init(&bars->p_half[g], 4);  // one arrival per softmax warp
+                mbar_init(&bars->p_full[g], 4);
+            }
             mbar_init(&bars->o_done[g], 1);
         }
         mbar_init(&bars->tail_full, 1);
@@ -157,7 +147,21 @@ __global__ void __launch_bounds__(Cfg<FP8>::kThreads, 1) chunk_kernel(const __gr
     const int ei = (int)(blockIdx.x);
     if (ei >= plan.upto[3]) return;  // every thread of the CTA
     // The entry lives in shared memory, so that the softmax loop keeps its registers for scores.
-    if (threadIdx.x == 0) bars->e = p.entries[chunk_entry(plan.upto, p.max_entries, ei)];
+    if (threadIdx.x == 0) {
+        bars->e = p.entries[chunk_entry(plan.upto, p.max_entries, ei)];
+        if constexpr (FP8) {
+            // One arrival per softmax warp that has rows of the entry: with few tokens the others stay out
+            // and leave the sub-partitions to the conversion (153 -> 144 us for 10 rows a tile; with a bf16
+            // cache, where nothing competes with them, it gained nothing).
+            const uint32_t warps = (uint32_t)min(4, (bars->e.tile.ntok * p.group + 31) / 32);
+            for (int g = 0; g < 2; ++g) {
+                mbar_init(&bars->p_half[g], warps);
+                mbar_init(&bars->p_full[g], warps);
+            }
+            mbar_init(&bars->q_ready, 2 * warps);
+            fence_mbarrier_init();
+        }
+    }
     if (warp == kWarpMma) {
         tmem_alloc(&bars->tmem_base, C::kTmemCols);
         tmem_relinquish();
@@ -201,38 +205,47 @@ __global__ void __launch_bounds__(Cfg<FP8>::kThreads, 1) chunk_kernel(const __gr
                 };
                 int next0 = page_at(2 * e.kt0), next1 = page_at(2 * e.kt0 + 1);
                 constexpr int kRing = FP8 ? C::kRawStages : C::kStages;
-                uint64_t* full = FP8 ? bars->raw_full : bars->kv_full;
-                uint64_t* empty = FP8 ? bars->raw_empty : bars->kv_empty;
-                int j = 0;
+                int j = 0, v = 0;  // tiles of K (bf16: K and V) and of V loaded
                 for (; j < nkv; ++j) {
                     const int s = j % kRing;
+                    const uint32_t free_ph = ((j / kRing) & 1) ^ 1;
                     const int pg[2] = {next0, next1};
                     if (j + 1 < nkv) {
                         next0 = page_at(2 * (e.kt0 + j + 1));
                         next1 = page_at(2 * (e.kt0 + j + 1) + 1);
                     }
-                    if (!mbar_wait(&empty[s], ((j / kRing) & 1) ^ 1, abort_flag, p.err, 0x31)) break;
                     if constexpr (FP8) {
                         uint8_t* st = smem + C::kOffRaw + s * C::kRawBytes;
-                        mbar_arrive_expect_tx(&full[s], C::kRawBytes);
+                        if (!mbar_wait(&bars->raw_empty[s][0], free_ph, abort_flag, p.err, 0x31)) break;
+                        mbar_arrive_expect_tx(&bars->raw_full[s][0], 2 * BN * D);
 #pragma unroll
                         for (int h = 0; h < 2; ++h) {
-                            tma_load_4d(st + h * 64 * D, &p.tm_k1, &full[s], 0, 0, hk, pg[h]);
-                            tma_load_4d(st + BN * D + h * 64 * D, &p.tm_k2, &full[s], 0, 0, hk, pg[h]);
-                            tma_load_4d(st + 2 * BN * D + h * 64 * DV, &p.tm_v, &full[s], 0, 0, hk, pg[h]);
+                            tma_load_4d(st + h * 64 * D, &p.tm_k1, &bars->raw_full[s][0], 0, 0, hk, pg[h]);
+                            tma_load_4d(st + BN * D + h * 64 * D, &p.tm_k2, &bars->raw_full[s][0], 0, 0, hk, pg[h]);
                         }
+                        if (!mbar_wait(&bars->raw_empty[s][1], free_ph, abort_flag, p.err, 0x31)) {
+                            ++j;  // this tile's K is on its way
+                            break;
+                        }
+                        mbar_arrive_expect_tx(&bars->raw_full[s][1], BN * DV);
+#pragma unroll
+                        for (int h = 0; h < 2; ++h)
+                            tma_load_4d(st + 2 * BN * D + h * 64 * DV, &p.tm_v, &bars->raw_full[s][1], 0, 0, hk, pg[h]);
+                        v = j + 1;
                     } else {
+                        if (!mbar_wait(&bars->kv_empty[s], free_ph, abort_flag, p.err, 0x31)) break;
                         uint8_t* st = stages + s * C::kStageBytes;
                         // A last tile that gets V rows cleared has a barrier of its own for V: the
                         // clearing warp follows no other phase of the ring.
                         const bool own = tail && j == last;
-                        uint64_t* vfull = own ? &bars->tail_full : &full[s];
-                        mbar_arrive_expect_tx(&full[s], own ? 2 * C::kKBytes : C::kStageBytes);
+                        uint64_t* full = &bars->kv_full[s];
+                        uint64_t* vfull = own ? &bars->tail_full : full;
+                        mbar_arrive_expect_tx(full, own ? 2 * C::kKBytes : C::kStageBytes);
                         if (own) mbar_arrive_expect_tx(vfull, C::kVBytes);
 #pragma unroll
                         for (int h = 0; h < 2; ++h) {
-                            tma_load_4d(st + h * 64 * 128, &p.tm_k1, &full[s], 0, 0, hk, pg[h]);
-                            tma_load_4d(st + C::kKBytes + h * 64 * 128, &p.tm_k2, &full[s], 0, 0, hk, pg[h]);
+                            tma_load_4d(st + h * 64 * 128, &p.tm_k1, full, 0, 0, hk, pg[h]);
+                            tma_load_4d(st + C::kKBytes + h * 64 * 128, &p.tm_k2, full, 0, 0, hk, pg[h]);
                         }
 #pragma unroll
                         for (int h = 0; h < 2; ++h)
@@ -244,9 +257,16 @@ __global__ void __launch_bounds__(Cfg<FP8>::kThreads, 1) chunk_kernel(const __gr
                 }
                 // Drain: no copy may still be landing in shared memory when the CTA exits.
                 mbar_wait(&bars->q_full, 0, nullptr, p.err, 0x32);
-                for (int u = max(0, j - kRing); u < j; ++u)
-                    mbar_wait(&full[u % kRing], (u / kRing) & 1, nullptr, p.err, 0x33);
-                if (!FP8 && tail && j == nkv) mbar_wait(&bars->tail_full, 0, nullptr, p.err, 0x33);
+                if constexpr (FP8) {
+                    for (int u = max(0, j - kRing); u < j; ++u)
+                        mbar_wait(&bars->raw_full[u % kRing][0], (u / kRing) & 1, nullptr, p.err, 0x33);
+                    for (int u = max(0, v - kRing); u < v; ++u)
+                        mbar_wait(&bars->raw_full[u % kRing][1], (u / kRing) & 1, nullptr, p.err, 0x33);
+                } else {
+                    for (int u = max(0, j - kRing); u < j; ++u)
+                        mbar_wait(&bars->kv_full[u % kRing], (u / kRing) & 1, nullptr, p.err, 0x33);
+                    if (tail && j == nkv) mbar_wait(&bars->tail_full, 0, nullptr, p.err, 0x33);
+                }
             }
         } else if (warp == kWarpMma) {
             // ------------------------------------------------------------ MMA issuer
@@ -256,15 +276,16 @@ __global__ void __launch_bounds__(Cfg<FP8>::kThreads, 1) chunk_kernel(const __gr
             const uint64_t dk0 = sdesc_sw128(smem_u32(stages), 16, 1024);
             const uint64_t dv0 = sdesc_sw128(smem_u32(stages) + 2 * C::kKBytes, BN * 128, 1024);
             constexpr uint64_t kStageStep = C::kStageBytes >> 4, kK2Step = C::kKBytes >> 4;
-            bool ok = nkv > 0 && mbar_wait_warp(&bars->q_full, 0, abort_flag, p.err, 0x34) &&
+            bool ok = nkv > 0 && mbar_wait_warp(FP8 ? &bars->q_ready : &bars->q_full, 0, abort_flag, p.err, 0x34) &&
                       mbar_wait_warp(&bars->kv_full[0], 0, abort_flag, p.err, 0x35);
             if (ok) {
                 tc_fence_after();
                 if (elect_one()) {
-                    issue_qk(tS[0], dq[0], dk0);
+                    issue_qk<FP8>(tS[0], dq[0], dk0);
                     umma_commit(&bars->s_full[0]);
-                    issue_qk(tS[1], dq[1], dk0 + kK2Step);
+                    issue_qk<FP8>(tS[1], dq[1], dk0 + kK2Step);
                     umma_commit(&bars->s_full[1]);
+                    if (FP8) umma_commit(&bars->kv_empty[0]);
                 }
                 __syncwarp();
             }
@@ -273,6 +294,10 @@ __global__ void __launch_bounds__(Cfg<FP8>::kThreads, 1) chunk_kernel(const __gr
                 const uint64_t dv = dv0 + s * kStageStep, dk1 = dk0 + s1 * kStageStep;
                 const bool more = j + 1 < nkv;
                 if (!FP8 && j == last && tail && !mbar_wait_warp(&bars->tail_done, 0, abort_flag, p.err, 0x3a)) break;
+                if (FP8 && !mbar_wait_warp(&bars->v_full[s], (uint32_t)(j / C::kStages) & 1, abort_flag, p.err, 0x3a)) break;
+                // S_m(j+1) follows PV_m(j). With an fp8 cache the next K tiles may still be in conversion: then
+                // S_0(j+1) waits behind PV_1(j) rather than PV_1(j) behind it.
+                bool s0_late = false;
                 for (int m = 0; m < 2; ++m) {
                     if (!mbar_wait_warp(&bars->p_half[m], j & 1, abort_flag, p.err, 0x36 + m)) {
                         ok = false;
@@ -281,8 +306,9 @@ __global__ void __launch_bounds__(Cfg<FP8>::kThreads, 1) chunk_kernel(const __gr
                     tc_fence_after();
                     if (elect_one()) issue_pv_half<FP8>(tO[m], tS[m], dv, 0, j > 0 ? 1u : 0u);
                     __syncwarp();
-                    if (m == 0 && more &&
-                        !mbar_wait_warp(&bars->kv_full[s1], ((j + 1) / C::kStages) & 1, abort_flag, p.err, 0x38)) {
+                    const uint32_t ph1 = (uint32_t)((j + 1) / C::kStages) & 1;
+                    bool next = more;
+                    if (!FP8 && m == 0 && more && !mbar_wait_warp(&bars->kv_full[s1], ph1, abort_flag, p.err, 0x38)) {
                         ok = false;
                         break;
                     }
@@ -290,17 +316,38 @@ __global__ void __launch_bounds__(Cfg<FP8>::kThreads, 1) chunk_kernel(const __gr
                         ok = false;
                         break;
                     }
+                    if (FP8 && m == 0 && more) {
+                        next = __all_sync(0xffffffffu, mbar_try_wait(&bars->kv_full[s1], ph1));
+                        s0_late = !next;
+                    }
                     tc_fence_after();
                     if (elect_one()) {
                         issue_pv_half<FP8>(tO[m], tS[m], dv, 1, 1u);
                         umma_commit(&bars->o_done[m]);
-                        if (m == 1) umma_commit(&bars->kv_empty[s]);
-                        if (more) {
-                            issue_qk(tS[m], dq[m], dk1 + m * kK2Step);
+                        if (m == 1) umma_commit(FP8 ? &bars->v_empty[s] : &bars->kv_empty[s]);
+                        if (next && !(FP8 && m == 1)) {
+                            issue_qk<FP8>(tS[m], dq[m], dk1 + m * kK2Step);
                             umma_commit(&bars->s_full[m]);
                         }
                     }
                     __syncwarp();
+                    if (FP8 && m == 1 && more) {
+                        if (!mbar_wait_warp(&bars->kv_full[s1], ph1, abort_flag, p.err, 0x38)) {
+                            ok = false;
+                            break;
+                        }
+                        tc_fence_after();
+                        if (elect_one()) {
+                            if (s0_late) {
+                                issue_qk<FP8>(tS[0], dq[0], dk1);
+                                umma_commit(&bars->s_full[0]);
+                            }
+                            issue_qk<FP8>(tS[1], dq[1], dk1 + kK2Step);
+                            umma_commit(&bars->s_full[1]);
+                            umma_commit(&bars->kv_empty[s1]);
+                        }
+                        __syncwarp();
+                    }
                 }
             }
             // Every MMA issued (also before an abort) must finish before TMEM is freed.
@@ -323,50 +370,45 @@ __global__ void __launch_bounds__(Cfg<FP8>::kThreads, 1) chunk_kernel(const __gr
                 if (lane == 0) mbar_arrive(&bars->tail_done);
             }
         } else if (FP8 && warp >= kWarpConvert) {
-            // ------------------------------------------------------------ e4m3 -> bf16 (K), fp16 (V)
+            // ------------------------------------------------------------ e4m3 -> fp16
             const int cw = warp - kWarpConvert, ct = cw * 32 + lane;
             for (int j = 0; j < nkv; ++j) {
-                const int rs = j % (FP8 ? C::kRawStages : 1), s = j % C::kStages;
-                if (!mbar_wait_warp(&bars->raw_full[rs], (j / 2) & 1, abort_flag, p.err, 0x48)) break;
-                if (!mbar_wait_warp(&bars->kv_empty[s], ((j / C::kStages) & 1) ^ 1, abort_flag, p.err, 0x49)) break;
-                const uint8_t* raw = smem + C::kOffRaw + rs * C::kRawBytes;
+                static_assert(!FP8 || (C::kRawStages == 2 && C::kStages == 2), "one stage index");
+                const int s = j % 2;
+                const uint32_t ph = (uint32_t)(j / 2) & 1;
+                if (!mbar_wait_warp(&bars->raw_full[s][0], ph, abort_flag, p.err, 0x48)) break;
+                if (!mbar_wait_warp(&bars->kv_empty[s], ph ^ 1, abort_flag, p.err, 0x49)) break;
+                const uint8_t* raw = smem + C::kOffRaw + s * C::kRawBytes;
                 uint8_t* st = stages + s * C::kStageBytes;
-                // K1 and K2: 16-byte chunk c of row r; a warp takes 8 rows x 4 chunks.
-#pragma unroll 4
-                for (int i = ct; i < 2 * BN * 4; i += 128) {
-                    const int m = i / (BN * 4), r = (i / 4) % BN, c = i % 4;
-                    const uint4 x = *reinterpret_cast<const uint4*>(raw + m * BN * D + r * D + c * 16);
-                    const uint32_t w[4] = {x.x, x.y, x.z, x.w};
-                    uint32_t y[8];
-#pragma unroll
-                    for (int k = 0; k < 4; ++k) e4m3x4_to_bf16(w[k], y + 2 * k);
-                    uint8_t* dst = st + m * C::kKBytes;
-                    *reinterpret_cast<uint4*>(dst + sw128_offset(r, 2 * c)) = make_uint4(y[0], y[1], y[2], y[3]);
-                    *reinterpret_cast<uint4*>(dst + sw128_offset(r, 2 * c + 1)) = make_uint4(y[4], y[5], y[6], y[7]);
-                }
-                // V: lanes 4..7 of eight take the next row's other box, so that neither the loads nor
-                // the swizzled stores of a quarter warp meet in a bank.
-                const int hidden = j == last ? tail_row : BN;
-#pragma unroll 4
-                for (int i = ct; i < BN * 8; i += 128) {
-                    const int pair = i / 16, in = i % 16;  // two rows of 8 chunks
-                    const int box = (in / 4 + in / 8) & 1, r = 2 * pair + ((in / 4) & 1), c = in % 4;
-                    uint32_t y[8] = {0u, 0u, 0u, 0u, 0u, 0u, 0u, 0u};
-                    if (r < hidden) {
-                        const uint4 x = *reinterpret_cast<const uint4*>(raw + 2 * BN * D + r * DV + box * 64 + c * 16);
-                        const uint32_t w[4] = {x.x, x.y, x.z, x.w};
-#pragma unroll
-                        for (int k = 0; k < 4; ++k) e4m3x4_to_f16(w[k], y + 2 * k);
-                    }
-                    uint8_t* dst = st + 2 * C::kKBytes + box * C::kBoxBytes;
-                    *reinterpret_cast<uint4*>(dst + sw128_offset(r, 2 * c)) = make_uint4(y[0], y[1], y[2], y[3]);
-                    *reinterpret_cast<uint4*>(dst + sw128_offset(r, 2 * c + 1)) = make_uint4(y[4], y[5], y[6], y[7]);
-                }
+                // K1, K2 and V in batches of four 16-byte chunks a thread, each batch loaded before the first
+                // chunk is stored (the compiler must assume that they overlap), in loops that stay small:
+                // three roles share an SM sub-partition's instruction cache. K and V have barriers of their
+                // own, so that the next scores do not wait for V nor its conversion for the last products.
+                // K: a warp takes 8 rows x 4 chunks.
+#pragma unroll 1
+                for (int m = 0; m < 2; ++m)
+                    convert4(raw + m * BN * D + ct * 16, 128 * 16, st + m * C::kKBytes, ct / 4, 32, ct % 4, BN);
                 fence_proxy_async_shared();
                 __syncwarp();
                 if (lane == 0) {
                     mbar_arrive(&bars->kv_full[s]);
-                    mbar_arrive(&bars->raw_empty[rs]);
+                    mbar_arrive(&bars->raw_empty[s][0]);
+                }
+                if (!mbar_wait_warp(&bars->raw_full[s][1], ph, abort_flag, p.err, 0x4a)) break;
+                if (!mbar_wait_warp(&bars->v_empty[s], ph ^ 1, abort_flag, p.err, 0x4b)) break;
+                // V: lanes 4..7 of eight take the next row's other box, so that neither the loads nor
+                // the swizzled stores of a quarter warp meet in a bank.
+                const int hidden = j == last ? tail_row : BN;
+                const int in = ct % 16, box = (in / 4 + in / 8) & 1, r0 = 2 * (ct / 16) + ((in / 4) & 1), c = in % 4;
+#pragma unroll 1
+                for (int r = r0; r < BN; r += 64)
+                    convert4(raw + 2 * BN * D + r * DV + box * 64 + c * 16, 16 * DV, st + 2 * C::kKBytes + box * C::kBoxBytes,
+                             r, 16, c, hidden);
+                fence_proxy_async_shared();
+                __syncwarp();
+                if (lane == 0) {
+                    mbar_arrive(&bars->v_full[s]);
+                    mbar_arrive(&bars->raw_empty[s][1]);
                 }
             }
         }
@@ -385,13 +427,22 @@ __global__ void __launch_bounds__(Cfg<FP8>::kThreads, 1) chunk_kernel(const __gr
         const uint32_t tS = lane_base + C::kColS + g * BN;
         const uint32_t tO = lane_base + C::kColO + g * DV;
         // (A bf16 cache has one score scale for both maps: a kernel constant in the loop's FMAs.)
-        const float sl2 = !FP8 || g == 0 ? p.scale1_log2 : p.scale2_log2;
+        float sl2 = !FP8 || g == 0 ? p.scale1_log2 : p.scale2_log2;
         const int pos0 = e.tile.pos0, kb0 = e.kt0 * BN;
         const int lim = r < e.tile.ntok * p.group ? pos0 + r / p.group + 1 : 0;  // keys that this row sees
+        // fp8: a warp none of whose rows belongs to the entry skips the key tiles. Its rows' weights are
+        // whatever the scores' columns hold, and nothing reads their sums.
+        const int n_mine = FP8 && lg * 32 >= e.tile.ntok * p.group ? 0 : nkv;
         float m_used = kChunkNoMax, l = 0.f;
         bool ok = true;
+        if (FP8 && n_mine > 0) {
+            ok = mbar_wait_warp(&bars->q_full, 0, abort_flag, p.err, 0x46);
+            if (ok) sl2 *= q_row_to_f16<D>(g == 0 ? q1s : q2s, r);
+            __syncwarp();
+            if (lane == 0) mbar_arrive(&bars->q_ready);
+        }
 
-        for (int j = 0; j < nkv; ++j) {
+        for (int j = 0; ok && j < n_mine; ++j) {
             if (!mbar_wait_warp(&bars->s_full[g], j & 1, abort_flag, p.err, 0x40 + g)) {
                 ok = false;
                 break;
@@ -464,7 +515,7 @@ __global__ void __launch_bounds__(Cfg<FP8>::kThreads, 1) chunk_kernel(const __gr
         }
 
         // ------------------------------------------------------------ epilogue
-        if (ok && nkv > 0) {
+        if (ok && n_mine > 0) {
             ok = mbar_wait_warp(&bars->o_done[0], (nkv - 1) & 1, abort_flag, p.err, 0x44) &&
                  mbar_wait_warp(&bars->o_done[1], (nkv - 1) & 1, abort_flag, p.err, 0x45);
         }
