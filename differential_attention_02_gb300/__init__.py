@@ -10,6 +10,7 @@ from __future__ import annotations
 
 import ctypes
 import os
+import struct
 
 import torch
 
@@ -129,8 +130,7 @@ def load_library(path: str = LIB_PATH) -> ctypes.CDLL:
     lib.diffattn_rope_freqs.restype = i32
     lib.diffattn_rope_freqs.argtypes = [i32, f64, i32, f64, i32, f64, f64, vp, fp]
     lib.diffattn_rope.restype = i32
-    lib.diffattn_rope.argtypes = [ctypes.POINTER(Tensor4)] * 2 + [ctypes.POINTER(i32), i32, vp, i32, i32, i32, rp, i32, i32,
-                                                                  i32, vp]
+    lib.diffattn_rope.argtypes = [ctypes.c_char_p] * 3 + [i32, vp, i32, i32, i32, rp, i32, i32, i32, vp]
     append = [Tensor4] * 3 + [i32] + [Tensor4] * 3 + [vp, i32, i32, vp, vp, rp] + [i32] * 5
     lib.diffattn_kv_append_chunk_paged.restype = i32
     lib.diffattn_kv_append_chunk_paged.argtypes = append + [vp]
@@ -550,33 +550,33 @@ def diffattn_rope(tensors, rope: RopePlan, positions=None, backward: bool = Fals
         raise ValueError("all tensors must be on one CUDA device")
     if positions is not None:
         _int32(positions, dev, (B, N), "positions")
-    src, dst, heads, fresh = [], [], [], out is None
+    fresh = out is None
     if fresh:
         out = [torch.empty_like(t, dtype=out_dtype) for t in tensors]
     odt = out[0].dtype
     if len(out) != n or (out_dtype is not None and out_dtype != odt):
         raise ValueError("out must match the operands and out_dtype")
-    rows = (B, N, d)
+    src, dst, heads = [], [], []
     for t, o in zip(tensors, out):
         b, h, m, w = shape = t.shape
-        s, r = t.stride(), o.stride()
-        if (b, m, w) != rows or t.dtype != dtype or s[3] != 1 or t.device != dev:
+        s0, s1, s2, s3 = t.stride()
+        r0, r1, r2, r3 = o.stride()
+        if b != B or m != N or w != d or s3 != 1 or t.dtype != dtype or t.device != dev:
             raise ValueError("operands must share device, dtype, batch, rows and width, the last dimension contiguous")
-        if not fresh and (o.shape != shape or o.dtype != odt or r[3] != 1 or o.device != dev):
+        if not fresh and (o.shape != shape or o.dtype != odt or r3 != 1 or o.device != dev):
             raise ValueError("out must match the operands' shapes and share one dtype and the device")
         heads.append(h)
-        src.append(Tensor4(t.data_ptr(), s[0], s[1], s[2]))
-        dst.append(Tensor4(o.data_ptr(), r[0], r[1], r[2]))
-    arr = _TENSORS[n]
+        src += (t.data_ptr(), s0, s1, s2)
+        dst += (o.data_ptr(), r0, r1, r2)
+    # the diffattn_tensor and head arrays as packed bytes
     _check((_lib or load_library()).diffattn_rope(
-        arr(*src), arr(*dst), _INTS[n](*heads), n, None if positions is None else positions.data_ptr(), B, N, d, rope._c,
-        1 if backward else 0, _dtype_code(dtype), _dtype_code(odt), _raw_stream(dev.index)), "diffattn_rope")
+        _PACK4[n](*src), _PACK4[n](*dst), _PACKI[n](*heads), n, None if positions is None else positions.data_ptr(), B, N, d,
+        rope._c, 1 if backward else 0, _dtype_code(dtype), _dtype_code(odt), _raw_stream(dev.index)), "diffattn_rope")
     return tuple(out)
 
 
-_TENSORS = [Tensor4 * n for n in range(5)]
-_INTS = [ctypes.c_int * n for n in range(5)]
-
+_PACK4 = [struct.Struct(f"={4 * n}q").pack for n in range(5)]
+_PACKI = [struct.Struct(f"={n}i").pack for n in range(5)]
 
 def _t3(t: torch.Tensor, T: int, H: int, width: int) -> Tensor4:
     """[T, H, width] rows with a contiguous last dimension -> diffattn_tensor (stride_b unused)."""

@@ -113,7 +113,7 @@ __device__ __forceinline__ void turn(float* a, float* b, const float* c, const f
 // grid.x: blocks of 256 / (d / 8) tokens; grid.y: ranges of the (operand, head) rows
 // of a token, so that a few tokens still fill the GPU while many share their sines.
 template <typename TI, typename TO>
-__global__ void __launch_bounds__(256) rope_kernel(const __grid_constant__ RopeParams p) {
+__global__ void __launch_bounds__(256, sizeof(TI) == 2 ? 4 : 2) rope_kernel(const __grid_constant__ RopeParams p) {
     const int chunks = p.d / 8, per_block = 256 / chunks;
     const int j = threadIdx.x % chunks;
     const int64_t t = (int64_t)blockIdx.x * per_block + threadIdx.x / chunks;
@@ -235,10 +235,24 @@ __global__ void __launch_bounds__(256) append_chunk_kernel(const __grid_constant
             }
             if (!found) {
                 found = true;
-                const int b = warp_count_le(p.q_start, p.B + 1, t, lane) - 1;
-                if (b < 0 || b >= p.B) return;  // a row behind the last sequence
-                const int64_t n = (int64_t)p.q_start[b + 1] - p.q_start[b];
-                const int64_t at = (int64_t)p.seq_lens[b] - n + (t - p.q_start[b]);
+                int b, first, next, len;
+                if (p.B <= 32) {  // starts and lengths of all sequences in one step
+                    const int end = lane < p.B ? p.q_start[lane + 1] : INT32_MAX;
+                    const int lens = lane < p.B ? p.seq_lens[lane] : 0;
+                    const int start0 = p.q_start[0];
+                    b = __popc(__ballot_sync(0xffffffffu, end <= t));
+                    next = __shfl_sync(0xffffffffu, end, b & 31);
+                    first = b == 0 ? start0 : __shfl_sync(0xffffffffu, end, (b - 1) & 31);
+                    len = __shfl_sync(0xffffffffu, lens, b & 31);
+                    if (t < first || b >= p.B) return;  // a row before the first sequence or behind the last
+                } else {
+                    b = warp_count_le(p.q_start, p.B + 1, t, lane) - 1;
+                    if (b < 0 || b >= p.B) return;
+                    first = p.q_start[b];
+                    next = p.q_start[b + 1];
+                    len = p.seq_lens[b];
+                }
+                const int64_t at = (int64_t)len - ((int64_t)next - first) + (t - first);
                 if (at < 0 || at / 64 >= p.max_pages) return;
                 page = p.block_table[(int64_t)b * p.max_pages + at / 64];
                 if (page < 0 || page >= p.num_pages) return;
@@ -277,9 +291,10 @@ cudaError_t launch_rope(const RopeParams& p, cudaStream_t stream) {
     if (e != cudaSuccess) return e;
     const int per_block = 256 / (p.d / 8);
     const int64_t blocks = ((int64_t)p.B * p.N + per_block - 1) / per_block;
-    // Eight blocks of 256 threads per SM, as long as a thread keeps a whole batch of rows.
-    int64_t split = ((int64_t)sms * 8 + blocks - 1) / blocks;
-    const int64_t most = (p.rows + kRowsBatch - 1) / kRowsBatch;
+    // One resident round of blocks (four per SM) where a token's rows allow it: a thread then keeps
+    // its sines for more rows and nothing runs on in a second round.
+    int64_t split = (int64_t)sms * 4 / blocks;
+    const int64_t most = (p.rows + 1) / 2;
     split = split < most ? split : most;
     const dim3 grid((unsigned)blocks, (unsigned)(split > 1 ? split : 1));
     if (p.in_dtype == 0) return launch_rope_t<float>(p, grid, stream);
@@ -291,9 +306,10 @@ cudaError_t launch_append_chunk(AppendChunkParams p, cudaStream_t stream) {
     int sms = 0;
     cudaError_t e = device_sm_count(&sms);
     if (e != cudaSuccess) return e;
-    // Up to 32 warps per SM share the heads of few tokens, a head each at the least.
-    int64_t split = ((int64_t)sms * 32 + p.T - 1) / p.T;
-    p.head_splits = (int)(split < p.H_kv ? split : p.H_kv);
+    // The warps that are resident at once (24 per SM) share the heads of few tokens, a head each at the
+    // least: more would start in a second round and look their token up again.
+    const int64_t split = (int64_t)sms * 24 / p.T;
+    p.head_splits = (int)(split < 1 ? 1 : split < p.H_kv ? split : p.H_kv);
     const int64_t blocks = ((int64_t)p.T * p.head_splits + 7) / 8;
     if (p.in_f16) {
         if (p.fp8) append_chunk_kernel<__half, true><<<(unsigned)blocks, 256, 0, stream>>>(p);

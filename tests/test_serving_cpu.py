@@ -63,8 +63,8 @@ def test_rope_refusals(lib):
         rot = rot or da.Rotation(0x30000, 64, 0, 1.0)
         h = (ctypes.c_int * 4)(*(list(heads) + [0] * (4 - len(heads))))
         arr = da.Tensor4 * 4
-        return lib.diffattn_rope(None if null.get("no_in") else arr(*t), None if null.get("no_out") else arr(*o),
-                                 None if null.get("no_heads") else h, count, vp(pos), B, N, d,
+        return lib.diffattn_rope(None if null.get("no_in") else bytes(arr(*t)), None if null.get("no_out") else bytes(arr(*o)),
+                                 None if null.get("no_heads") else bytes(h), count, vp(pos), B, N, d,
                                  None if null.get("no_rot") else ctypes.byref(rot), 0, ind, outd, None)
     assert call(B=0) == da.OK and call(N=0) == da.OK and call(heads=(0, 0)) == da.OK
     for kw in (dict(B=-1), dict(N=-1), dict(d=60), dict(d=264), dict(d=0), dict(count=0), dict(count=5), dict(heads=(-1, 2)),
