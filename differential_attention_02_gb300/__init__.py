@@ -729,7 +729,7 @@ def interleave_gate_up(w_gate, w_up):
 
 def layer_fwd(x, w_q, w_k, w_v, w_o, w_gu, w_down, n_heads: int, lam: float, lam_init: float,
               eps: float = 1e-5, norm1_weight=None, norm2_weight=None, head_weight=None, ws=None, stream=None,
-              w_qkv=None):
+              w_qkv=None, rope: RopePlan | None = None, positions=None):
     """One DIFF Transformer layer: Y = MultiHead(RMSNorm(X)) + X, X' = SwiGLU(RMSNorm(Y)) + Y.
 
     x: [B, N, d_model] bf16 or fp32; module weights as in module_fwd (w_qkv, if given, is
@@ -737,12 +737,14 @@ def layer_fwd(x, w_q, w_k, w_v, w_o, w_gu, w_down, n_heads: int, lam: float, lam
     gate and up weights interleaved by interleave_gate_up; w_down: [d_ff, d_model]; every weight
     bf16, or every weight fp16, and the GEMM operands take that type; norm weights fp32 [d_model],
     head_weight fp32 [Dv] (the per-head RMSNorm's gain). d_model a multiple of 256, d_ff of 128.
-    Returns X' [B, N, d_model] fp32 (the residual stream is kept in fp32).
+    rope and positions as in module_fwd. Returns X' [B, N, d_model] fp32 (the residual stream is
+    kept in fp32).
 
-    Six launches: RMSNorm of X; the QKV projection; the fused attention; W_O with the residual
-    add in its epilogue, which also writes Y (times norm2's gain) as the next operand and the row
-    sums of Y^2; gate/up with SwiGLU in its epilogue, scaled by 1/RMS(Y) per row
-    (RMSNorm(Y) W = (Y W) / r); W_down with the second residual add.
+    Six launches, seven with rope: RMSNorm of X; the QKV projection (and the rotation of its Q and
+    K columns in place); the fused attention; W_O with the residual add in its epilogue, which also
+    writes Y (times norm2's gain) as the next operand and the row sums of Y^2; gate/up with SwiGLU
+    in its epilogue, scaled by 1/RMS(Y) per row (RMSNorm(Y) W = (Y W) / r); W_down with the second
+    residual add.
 
     Range: the 16-bit operand copy of Y (times norm2's gain) is taken before the
     normalisation, so fp16 weights need |Y * g| <= 65504; bf16 weights have fp32's range."""
@@ -750,12 +752,19 @@ def layer_fwd(x, w_q, w_k, w_v, w_o, w_gu, w_down, n_heads: int, lam: float, lam
     M = B * N
     op = (w_qkv if w_qkv is not None else w_q).dtype
     _, n1 = add_rmsnorm(x, weight=norm1_weight, eps=eps, n_dtype=op, stream=stream)
-    att = _module_attention(n1, w_q, w_k, w_v, n_heads, lam, lam_init, eps, head_weight, ws, stream, op, w_qkv)
-    y, y16, sq = gemm_residual(att, w_o, x.reshape(M, dm), c16_dtype=op, c16_gain=norm2_weight, want_row_sq=True,
-                               ws=ws, stream=stream)
+    att = _module_attention(n1, w_q, w_k, w_v, n_heads, lam, lam_init, eps, head_weight, ws, stream, op, w_qkv,
+                            rope=rope, positions=positions)
+    return _layer_tail(att, x.reshape(M, dm), w_o, w_gu, w_down, eps, norm2_weight, ws, stream).view(B, N, dm)
+
+
+def _layer_tail(att, x, w_o, w_gu, w_down, eps, norm2_weight, ws, stream):
+    """The layer behind its attention: W_O and the residual add, the feed-forward and its add. [M, d_model]."""
+    dm, op = x.shape[1], att.dtype
+    y, y16, sq = gemm_residual(att, w_o, x, c16_dtype=op, c16_gain=norm2_weight, want_row_sq=True, ws=ws,
+                               stream=stream)
     h = gemm_swiglu(y16, w_gu, row_sq=sq, sq_count=dm, eps=eps, out_dtype=op, ws=ws, stream=stream)
     out, _, _ = gemm_residual(h, w_down, y, ws=ws, stream=stream)
-    return out.view(B, N, dm)
+    return out
 
 
 def gemm_residual(a, w, r, c16_dtype=None, c16_gain=None, want_row_sq=False, out=None, ws=None, stream=None):
@@ -829,10 +838,12 @@ gemm_bf16 = gemm
 
 def module_fwd(x, w_q, w_k, w_v, w_o, n_heads: int, lam: float, lam_init: float, eps: float = 1e-5,
                norm_weight=None, ws=None, stream=None, out_dtype=torch.bfloat16, qkv_dtype=torch.float16,
-               w_qkv=None):
+               w_qkv=None, rope: RopePlan | None = None, positions=None):
     """Multi-head differential attention module: the projection GEMMs (one against
     w_qkv = torch.cat([w_q, w_k, w_v], 1) when it is given, else three), the fused
-    attention reading Q/K/V in place through strided views, and the W_O GEMM.
+    attention reading Q/K/V in place through strided views, and the W_O GEMM. With
+    `rope`, Q1, Q2, K1 and K2 of every head are rotated in place in between (row n at
+    position n, or at positions[b, n], int32).
 
     x [B,N,d_model]; w_q, w_k [d_model, h*2d]; w_v [d_model, h*Dv]; w_o [h*Dv, d_model],
     all bf16 or all fp16. Head i uses Q[..., 2di:2di+d] as Q1 and Q[..., 2di+d:2d(i+1)] as Q2
@@ -849,15 +860,15 @@ def module_fwd(x, w_q, w_k, w_v, w_o, n_heads: int, lam: float, lam_init: float,
     (8 significant bits instead of 11) for callers who want bf16 throughout.
     """
     att = _module_attention(x, w_q, w_k, w_v, n_heads, lam, lam_init, eps, norm_weight, ws, stream, x.dtype, w_qkv,
-                            qkv_dtype)
+                            qkv_dtype, rope, positions)
     B, N, dm = x.shape
     y = gemm(att, w_o, out_dtype=out_dtype, ws=ws, stream=stream)
     return y.view(B, N, dm)
 
 
 def _module_attention(x, w_q, w_k, w_v, n_heads, lam, lam_init, eps, norm_weight, ws, stream, att_dtype, w_qkv=None,
-                      qkv_dtype=torch.float16):
-    """The projections and the fused attention of module_fwd: returns concat(heads) [B*N, h*Dv]
+                      qkv_dtype=torch.float16, rope=None, positions=None):
+    """The projections, the rotation and the fused attention of module_fwd: returns concat(heads) [B*N, h*Dv]
     of att_dtype, the operand W_O multiplies."""
     if qkv_dtype not in (torch.float16, torch.bfloat16):
         raise ValueError("qkv_dtype must be torch.float16 or torch.bfloat16")
@@ -885,9 +896,95 @@ def _module_attention(x, w_q, w_k, w_v, n_heads, lam, lam_init, eps, norm_weight
     q4 = q.unflatten(0, (B, N)).unflatten(2, (h, 2 * d)).permute(0, 2, 1, 3)
     k4 = k.unflatten(0, (B, N)).unflatten(2, (h, 2 * d)).permute(0, 2, 1, 3)
     v4 = v.unflatten(0, (B, N)).unflatten(2, (h, Dv)).permute(0, 2, 1, 3)
-    att = diffattn_fwd(q4[..., :d], q4[..., d:], k4[..., :d], k4[..., d:], v4, lam, lam_init, eps, norm_weight,
-                       out_dtype=att_dtype, ws=ws, stream=stream)
+    qk = (q4[..., :d], q4[..., d:], k4[..., :d], k4[..., d:])
+    if rope is not None:
+        diffattn_rope(qk, rope, positions, out=qk, stream=stream)
+    elif positions is not None:
+        raise ValueError("positions are those of rope")
+    att = diffattn_fwd(*qk, v4, lam, lam_init, eps, norm_weight, out_dtype=att_dtype, ws=ws, stream=stream)
     return att.view(B * N, h * Dv)
+
+
+def module_serve(x, w_qkv, w_o, n_heads: int, pages, block_table, q_start, seq_lens, lam: float, lam_init: float, L: int,
+                 kv_group: int = 1, rope: RopePlan | None = None, positions=None, scales=None, eps: float = 1e-5,
+                 norm_weight=None, out_dtype=torch.bfloat16, ws=None, stream=None) -> torch.Tensor:
+    """The module over a paged cache: the new tokens x [T, d_model] of many sequences (prompts, chunks of
+    prompts and single tokens in one batch; sequence b's rows are q_start[b] .. q_start[b + 1] - 1 and become
+    the last of its seq_lens[b] tokens) are projected, their K and V appended, their attention taken over
+    the whole cached sequences, and multiplied by w_o. Returns [T, d_model] of out_dtype.
+
+    w_qkv [d_model, h*2d + h_kv*2d + h_kv*Dv] = torch.cat([w_q, w_k, w_v], 1) with the heads laid out as in
+    module_fwd, h_kv = n_heads / kv_group; w_o [h*Dv, d_model]; x and the weights all bf16 or all fp16.
+    pages = (k1_pages, k2_pages, v_pages), block_table, scales (fp8 pages) and L as in diffattn_chunk_paged. Q, K
+    and V are bf16, the type that the paged attention reads. With rope, Q rotates at `positions` (int32 [T], the
+    token's place in its sequence: seq_lens[b] - q_start[b + 1] + row) and K as it is appended, at the
+    same place by construction. Rows of no sequence: their attention is zero.
+
+    Four launches of its own beside the two GEMMs: rotation of Q, append, plan and attention (a fifth joins
+    sequences that were split). Calls on different streams share no workspace unless `ws` is given; it then
+    needs chunk_workspace_bytes."""
+    ctx = _elsewhere(x.device, stream)
+    if ctx is not None:
+        with ctx:
+            return module_serve(x, w_qkv, w_o, n_heads, pages, block_table, q_start, seq_lens, lam, lam_init, L, kv_group,
+                                rope, positions, scales, eps, norm_weight, out_dtype, ws)
+    att, ws = _serve_attention(x, w_qkv, n_heads, pages, block_table, q_start, seq_lens, lam, lam_init, L, kv_group, rope,
+                               positions, scales, eps, norm_weight, x.dtype, ws)
+    if att.shape[0] == 0:
+        return torch.empty((0, w_o.shape[1]), dtype=out_dtype, device=x.device)
+    return gemm(att, w_o, out_dtype=out_dtype, ws=ws)
+
+
+def layer_serve(x, w_qkv, w_o, w_gu, w_down, n_heads: int, pages, block_table, q_start, seq_lens, lam: float,
+                lam_init: float, L: int, kv_group: int = 1, rope: RopePlan | None = None, positions=None, scales=None,
+                eps: float = 1e-5, norm1_weight=None, norm2_weight=None, head_weight=None, ws=None,
+                stream=None) -> torch.Tensor:
+    """layer_fwd over a paged cache: x [T, d_model] bf16 or fp32, the new tokens of many sequences, and the
+    cache's arguments as in module_serve; weights and norms as in layer_fwd. Returns X' [T, d_model] fp32."""
+    ctx = _elsewhere(x.device, stream)
+    if ctx is not None:
+        with ctx:
+            return layer_serve(x, w_qkv, w_o, w_gu, w_down, n_heads, pages, block_table, q_start, seq_lens, lam, lam_init,
+                               L, kv_group, rope, positions, scales, eps, norm1_weight, norm2_weight, head_weight, ws)
+    if x.dim() != 2 or x.dtype not in (torch.bfloat16, torch.float32) or not x.is_contiguous():
+        raise ValueError("x must be a contiguous [T, d_model] bf16 or fp32 tensor")
+    _, n1 = add_rmsnorm(x, weight=norm1_weight, eps=eps, n_dtype=w_qkv.dtype)
+    att, ws = _serve_attention(n1, w_qkv, n_heads, pages, block_table, q_start, seq_lens, lam, lam_init, L, kv_group, rope,
+                               positions, scales, eps, head_weight, w_qkv.dtype, ws)
+    if att.shape[0] == 0:
+        return torch.empty(x.shape, dtype=torch.float32, device=x.device)
+    return _layer_tail(att, x, w_o, w_gu, w_down, eps, norm2_weight, ws, None)
+
+
+def _serve_attention(x, w_qkv, n_heads, pages, block_table, q_start, seq_lens, lam, lam_init, L, kv_group, rope,
+                     positions, scales, eps, norm_weight, att_dtype, ws):
+    """The projection, rotation, append and attention of module_serve on the current stream: concat(heads)
+    [T, h*Dv] of att_dtype, and the workspace."""
+    T, h, dev = x.shape[0], n_heads, x.device
+    if x.dim() != 2 or kv_group < 1 or h % kv_group:
+        raise ValueError("x must be [T, d_model], and kv_group must divide the heads")
+    hk, d, Dv = h // kv_group, pages[0].shape[-1], pages[2].shape[-1]
+    if w_qkv.shape[1] != 2 * d * (h + hk) + Dv * hk:
+        raise ValueError("w_qkv must be torch.cat([w_q, w_k, w_v], 1) with the cache's heads and widths")
+    if (rope is None) != (positions is None):
+        raise ValueError("rope goes with the rows' positions")
+    if positions is not None:
+        _int32(positions, dev, (T,), "positions")
+    _on_device(dev, w_qkv, *pages, block_table, q_start, seq_lens)
+    if ws is None:
+        ws = _serving_workspace(max(256, chunk_workspace_bytes(T, seq_lens.shape[0], h, kv_group, L, d, Dv)), dev)
+    # rows of no sequence are written by no kernel, and W_O reads them
+    att = torch.zeros((T, h, Dv), dtype=att_dtype, device=dev)
+    if T:
+        qkv = gemm(x, w_qkv, out_dtype=torch.bfloat16, ws=ws)
+        q, k, v = (t.unflatten(1, (n, -1)) for t, n in zip(qkv.split((2 * d * h, 2 * d * hk, Dv * hk), 1), (h, hk, hk)))
+        if rope is not None:
+            q4 = tuple(t.transpose(0, 1)[None] for t in (q[..., :d], q[..., d:]))
+            diffattn_rope(q4, rope, positions[None], out=q4)
+        diffattn_kv_append_chunk_paged(k[..., :d], k[..., d:], v, *pages, block_table, q_start, seq_lens, rope, scales)
+        diffattn_chunk_paged(q[..., :d], q[..., d:], *pages, block_table, q_start, seq_lens, lam, lam_init, L, kv_group, eps,
+                             norm_weight, out=att, ws=ws, scales=scales)
+    return att.view(T, h * Dv), ws
 
 
 _host_buffers = {}

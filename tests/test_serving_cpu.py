@@ -167,3 +167,15 @@ def test_python_wrappers_refuse_before_device_work(lib):
         da.diffattn_rope([torch.zeros(1, 2, 3, 64, dtype=bf)], plan)
     with pytest.raises(ValueError, match="CUDA"):
         da.diffattn_kv_append_chunk_paged(q[:, :2], q[:, :2], torch.zeros(3, 2, 128, dtype=bf), k, k, v, table, start, lens)
+
+
+def test_serving_models_refuse_before_device_work(lib):
+    """The served module and layer check shapes on the host; tensors on the CPU never reach a kernel."""
+    x, w, wo = torch.zeros(3, 64), torch.zeros(64, 512), torch.zeros(128, 64)
+    pages = [torch.zeros(2, 1, 64, n, dtype=torch.bfloat16) for n in (64, 64, 128)]
+    i32 = lambda *v: torch.tensor(v, dtype=torch.int32)  # noqa: E731
+    args = (pages, i32(0).view(1, 1), i32(0, 3), i32(3), 0.5, 0.5, 3)
+    with pytest.raises(ValueError, match="CUDA"):
+        da.module_serve(x, w, wo, 1, *args)
+    with pytest.raises(ValueError, match="CUDA"):
+        da.layer_serve(x, w, wo, w, wo, 1, *args)
