@@ -58,6 +58,24 @@ bool encode_4d(CUtensorMap* m, const diffattn_tensor& t, int width, int rows, in
                CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
 }
 
+// Map over 8-bit pages [B, H, 64, width] whose boxes are a head's whole page, in shared memory as in
+// memory. Where its rows follow one another, the 64 rows are taken as rows of 1024 bytes.
+bool encode_raw_pages(CUtensorMap* m, const diffattn_tensor& t, int width, int H, int B) {
+    if (t.stride_n != width)
+        return encode_4d(m, t, width, 64, H, B, width, 64, CU_TENSOR_MAP_SWIZZLE_NONE, CU_TENSOR_MAP_DATA_TYPE_UINT8);
+    auto enc = tensor_map_encoder();
+    if (!enc) return false;
+    const int64_t page = 64 * (int64_t)width, sh = H > 1 ? t.stride_h : page, sb = B > 1 ? t.stride_b : H * sh;
+    const cuuint32_t rows = (cuuint32_t)(page / 1024);
+    cuuint64_t dims[4] = {256, rows, (cuuint64_t)H, (cuuint64_t)B};
+    cuuint64_t strides[3] = {1024, (cuuint64_t)sh, (cuuint64_t)sb};
+    cuuint32_t box[4] = {256, rows, 1, 1};
+    cuuint32_t es[4] = {1, 1, 1, 1};
+    return enc(m, CU_TENSOR_MAP_DATA_TYPE_UINT32, 4, const_cast<void*>(t.ptr), dims, strides, box, es,
+               CU_TENSOR_MAP_INTERLEAVE_NONE, CU_TENSOR_MAP_SWIZZLE_NONE, CU_TENSOR_MAP_L2_PROMOTION_L2_256B,
+               CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
+}
+
 // 3-D map over a contiguous output [B, N, W] (W = H * Dv elements per token),
 // boxes of 128 bytes x `box_rows` rows, 128-byte swizzle (for TMA stores).
 bool encode_out_3d(CUtensorMap* m, void* ptr, int W, int N, int B, int elem_bytes, int box_rows) {
@@ -958,32 +976,50 @@ namespace {
 // Bounds of the plan's lists and the workspace regions of the chunk attention. They follow from
 // the sizes alone (chunk_plan.cu gives the argument), whatever the lengths on the device.
 struct ChunkLayout {
-    int tm, rows, ctas, max_tiles, max_entries, max_slots, max_merges;
-    size_t tiles, entries, merges, stats, o, total;
+    int tm, ctas, n;  // n: lists
+    struct List {
+        int which, rows, q_rows, max_tiles, max_entries, max_slots, max_merges;
+        size_t plan, tiles, entries, merges, stats, o;
+    } list[2];
+    size_t total;
 };
-bool chunk_layout(int B, int H, int kv_group, int T, int L, int d, int Dv, ChunkLayout* l) {
+// `fp8`: tiles of few rows may go to a kernel of their own (chunk_few_tcgen05.cu). All of them are such
+// if the whole call has few rows; both kernels run where a sequence has up to eight times as many on
+// average (a longer chunk's rows dominate: an empty list costs its launch, 3 us).
+bool chunk_layout(int B, int H, int kv_group, int T, int L, int d, int Dv, bool fp8, ChunkLayout* l) {
     const int64_t H_kv = H / kv_group;
     const int n_sm = device_sm_count();
     const int sms = n_sm > 0 ? n_sm : 152;
     l->ctas = d == 64 ? sms : sms / 2;  // one CTA per SM; a pair per work item for the wide heads
     l->tm = kChunkRows / kv_group;
-    l->rows = std::min(l->tm, T) * kv_group;
-    const int64_t tiles = (int64_t)T / l->tm + std::min(B, T);
     // Cutting needs an item of at least two key tiles.
     const int64_t extra = L > kChunkKeys ? l->ctas : 0;
-    const int64_t entries = tiles * H_kv + extra;
-    if (entries * 2 > INT32_MAX) return false;
-    l->max_tiles = (int)tiles;
-    l->max_entries = (int)entries;
-    l->max_slots = (int)(2 * extra);
-    l->max_merges = (int)extra;
-    l->tiles = round256(kControlBytes + sizeof(ChunkPlan));
-    l->entries = l->tiles + round256(tiles * sizeof(ChunkTile));
-    l->merges = l->entries + round256(2 * entries * sizeof(ChunkEntry));
-    l->stats = l->merges + round256(extra * sizeof(ChunkMerge));
-    const size_t states = (size_t)l->max_slots * 2 * l->rows;
-    l->o = l->stats + round256(states * 2 * sizeof(float));
-    l->total = l->o + round256(states * Dv * sizeof(float));
+    const int64_t rows = (int64_t)T * kv_group, sequences = std::min(B, T);
+    const bool few = fp8 && d == 64 && kv_group <= kFewRows && rows <= 8 * kFewRows * sequences;
+    l->n = few && rows > kFewRows ? 2 : 1;
+    size_t at = kControlBytes;
+    for (int i = 0; i < l->n; ++i) {
+        ChunkLayout::List& x = l->list[i];
+        x.which = l->n == 1 ? (few ? kTilesFew : kTilesAll) : i == 0 ? kTilesMany : kTilesFew;
+        x.q_rows = (x.which == kTilesFew ? kFewRows / kv_group : l->tm) * kv_group;
+        x.rows = (int)std::min<int64_t>(x.q_rows, rows);
+        const int64_t tiles = x.which == kTilesFew ? sequences : (int64_t)T / l->tm + sequences;
+        const int64_t entries = tiles * H_kv + extra;
+        if (entries * 2 > INT32_MAX) return false;
+        x.max_tiles = (int)tiles;
+        x.max_entries = (int)entries;
+        x.max_slots = (int)(2 * extra);
+        x.max_merges = (int)extra;
+        x.plan = at;
+        x.tiles = x.plan + round256(sizeof(ChunkPlan));
+        x.entries = x.tiles + round256(tiles * sizeof(ChunkTile));
+        x.merges = x.entries + round256(2 * entries * sizeof(ChunkEntry));
+        x.stats = x.merges + round256(extra * sizeof(ChunkMerge));
+        const size_t states = (size_t)x.max_slots * 2 * x.rows;
+        x.o = x.stats + round256(states * 2 * sizeof(float));
+        at = x.o + round256(states * Dv * sizeof(float));
+    }
+    l->total = at;
     return true;
 }
 
@@ -1025,19 +1061,30 @@ diffattn_status chunk_paged(bool fp8, const float* scales, diffattn_tensor q1, d
     if (norm_weight != nullptr && !aligned16(norm_weight)) return DIFFATTN_ERR_INVALID_ARG;
     if (!((d == 64 && Dv == 128) || (d == 128 && Dv == 256)) || kv_group > kChunkRows) return DIFFATTN_ERR_UNSUPPORTED;
     ChunkLayout l;
-    if (!chunk_layout(B, H, kv_group, T, L, d, Dv, &l)) return DIFFATTN_ERR_UNSUPPORTED;
+    if (!chunk_layout(B, H, kv_group, T, L, d, Dv, fp8, &l)) return DIFFATTN_ERR_UNSUPPORTED;
     if (workspace == nullptr || workspace_bytes < l.total || (reinterpret_cast<uintptr_t>(workspace) & 255u))
         return DIFFATTN_ERR_WORKSPACE;
     const int H_kv = H / kv_group;
-    ChunkParams p{};
-    bool ok = encode_chunk_q(&p.tm_q1, q1, d, H_kv, kv_group, T, l.tm) &&
-              encode_chunk_q(&p.tm_q2, q2, d, H_kv, kv_group, T, l.tm);
+    ChunkLists lists{};
+    ChunkParams& p = lists.p[0];
+    bool ok = true;
+    for (int i = 0; i < l.n; ++i)
+        ok = ok && encode_chunk_q(&lists.p[i].tm_q1, q1, d, H_kv, kv_group, T, l.list[i].q_rows / kv_group) &&
+             encode_chunk_q(&lists.p[i].tm_q2, q2, d, H_kv, kv_group, T, l.list[i].q_rows / kv_group);
     if (fp8) {  // raw rows, converted in the kernel
-        const CUtensorMapDataType u8 = CU_TENSOR_MAP_DATA_TYPE_UINT8;
-        const CUtensorMapSwizzle none = CU_TENSOR_MAP_SWIZZLE_NONE;
-        ok = ok && encode_4d(&p.tm_k1, k1_pages, d, 64, H_kv, num_pages, d, 64, none, u8) &&
-             encode_4d(&p.tm_k2, k2_pages, d, 64, H_kv, num_pages, d, 64, none, u8) &&
-             encode_4d(&p.tm_v, v_pages, Dv, 64, H_kv, num_pages, Dv, 64, none, u8);
+        for (int i = 0; i < l.n; ++i) {
+            ChunkParams& a = lists.p[i];
+            ok = ok && encode_raw_pages(&a.tm_v, v_pages, Dv, H_kv, num_pages);
+            if (l.list[i].which == kTilesFew) {
+                const CUtensorMapSwizzle sw = CU_TENSOR_MAP_SWIZZLE_64B;
+                const CUtensorMapDataType u8 = CU_TENSOR_MAP_DATA_TYPE_UINT8;
+                ok = ok && encode_4d(&a.tm_k1, k1_pages, d, 64, H_kv, num_pages, d, 64, sw, u8) &&
+                     encode_4d(&a.tm_k2, k2_pages, d, 64, H_kv, num_pages, d, 64, sw, u8);
+            } else {
+                ok = ok && encode_raw_pages(&a.tm_k1, k1_pages, d, H_kv, num_pages) &&
+                     encode_raw_pages(&a.tm_k2, k2_pages, d, H_kv, num_pages);
+            }
+        }
     } else {
         const CUtensorMapSwizzle sw = CU_TENSOR_MAP_SWIZZLE_128B;
         ok = ok && encode_4d(&p.tm_k1, k1_pages, d, 64, H_kv, num_pages, 64, 64, sw) &&
@@ -1061,21 +1108,39 @@ diffattn_status chunk_paged(bool fp8, const float* scales, diffattn_tensor q1, d
     p.scale1_log2 = (float)(fp8 ? sl2 * scales[0] * 256.0 : sl2);
     p.scale2_log2 = (float)(fp8 ? sl2 * scales[1] * 256.0 : sl2);
     p.v_scale = fp8 ? (float)(scales[2] * 256.0) : 1.f;
-    uint8_t* ws = static_cast<uint8_t*>(workspace);
-    p.err = err_word(workspace);
-    p.plan = reinterpret_cast<ChunkPlan*>(ws + kControlBytes);
-    p.tiles = reinterpret_cast<ChunkTile*>(ws + l.tiles);
-    p.entries = reinterpret_cast<ChunkEntry*>(ws + l.entries);
-    p.merges = reinterpret_cast<ChunkMerge*>(ws + l.merges);
-    p.part_stats = reinterpret_cast<float*>(ws + l.stats);
-    p.part_o = reinterpret_cast<float*>(ws + l.o);
-    p.max_tiles = l.max_tiles; p.max_entries = l.max_entries; p.max_slots = l.max_slots; p.max_merges = l.max_merges;
-    p.rows = l.rows;
     p.ctas = l.ctas;
+    p.err = err_word(workspace);
+    if (l.n == 2) {  // the second list's parameters: everything but its boxes of Q and K and its lists
+        const ChunkParams few = lists.p[1];
+        lists.p[1] = p;
+        lists.p[1].tm_q1 = few.tm_q1; lists.p[1].tm_q2 = few.tm_q2;
+        lists.p[1].tm_k1 = few.tm_k1; lists.p[1].tm_k2 = few.tm_k2;
+    }
+    if (l.list[l.n - 1].which == kTilesFew) {  // its operands are the stored values
+        ChunkParams& few = lists.p[l.n - 1];
+        few.scale1_log2 *= 1.f / 256; few.scale2_log2 *= 1.f / 256; few.v_scale *= 1.f / 256;
+    }
+    uint8_t* ws = static_cast<uint8_t*>(workspace);
+    for (int i = 0; i < l.n; ++i) {
+        const ChunkLayout::List& x = l.list[i];
+        ChunkParams& a = lists.p[i];
+        a.plan = reinterpret_cast<ChunkPlan*>(ws + x.plan);
+        a.tiles = reinterpret_cast<ChunkTile*>(ws + x.tiles);
+        a.entries = reinterpret_cast<ChunkEntry*>(ws + x.entries);
+        a.merges = reinterpret_cast<ChunkMerge*>(ws + x.merges);
+        a.part_stats = reinterpret_cast<float*>(ws + x.stats);
+        a.part_o = reinterpret_cast<float*>(ws + x.o);
+        a.max_tiles = x.max_tiles; a.max_entries = x.max_entries; a.max_slots = x.max_slots; a.max_merges = x.max_merges;
+        a.rows = x.rows; a.q_rows = x.q_rows;
+        a.which = x.which;
+    }
     cudaStream_t st = static_cast<cudaStream_t>(stream);
-    cudaError_t e = launch_chunk_plan(p, st);
-    if (e == cudaSuccess) e = d == 64 ? launch_chunk_64(p, st) : launch_chunk_pair(p, st);
-    if (e == cudaSuccess && p.max_merges > 0) e = launch_chunk_merge(p, st);
+    cudaError_t e = launch_chunk_plan(lists, l.n, st);
+    for (int i = 0; i < l.n && e == cudaSuccess; ++i) {
+        const ChunkParams& a = lists.p[i];
+        e = a.which == kTilesFew ? launch_chunk_few(a, st) : d == 64 ? launch_chunk_64(a, st) : launch_chunk_pair(a, st);
+    }
+    if (e == cudaSuccess && p.max_merges > 0) e = launch_chunk_merge(lists, l.n, st);
     return cuda_status(e);
 }
 }  // namespace
@@ -1088,9 +1153,11 @@ diffattn_status diffattn_chunk_workspace_size(int T, int B, int H, int kv_group,
     if (T == 0 || B == 0 || H == 0) return DIFFATTN_OK;
     if (H % kv_group != 0) return DIFFATTN_ERR_INVALID_ARG;
     if (kv_group > kChunkRows) return DIFFATTN_ERR_UNSUPPORTED;
-    ChunkLayout l;
-    if (!chunk_layout(B, H, kv_group, T, L, d, Dv, &l)) return DIFFATTN_ERR_UNSUPPORTED;
-    *bytes = l.total;
+    ChunkLayout l;  // the larger of the two caches' needs
+    for (const bool fp8 : {false, true}) {
+        if (!chunk_layout(B, H, kv_group, T, L, d, Dv, fp8, &l)) return DIFFATTN_ERR_UNSUPPORTED;
+        *bytes = std::max(*bytes, l.total);
+    }
     return DIFFATTN_OK;
 }
 

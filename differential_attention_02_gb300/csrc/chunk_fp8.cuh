@@ -20,6 +20,8 @@
 // colliding; a bf16 cache's tile moves 192 KB in 2,500.
 #pragma once
 
+#include <cuda_fp8.h>
+
 #include "common.cuh"
 
 namespace da {
@@ -54,24 +56,38 @@ __device__ __forceinline__ float q_row_to_f16(uint8_t* boxes, int r) {
     return __uint_as_float((uint32_t)(127 - shift) << 23);
 }
 
-// Sixteen e4m3 values (raw chunk c of row r) as fp16 values times 2^-8, exactly, into their two
-// chunks of a swizzled box.
-__device__ __forceinline__ void put_e4m3x16(uint8_t* box, int r, int c, uint4 x) {
+// Sixteen e4m3 values as fp16 values in pairs, exactly: times 2^-8 by integers, or as they are by
+// the conversion instruction (CVT), a third of the instructions but slower ones.
+template <bool CVT>
+__device__ __forceinline__ void e4m3x16_to_f16(uint4 x, uint32_t* y) {
     const uint32_t w[4] = {x.x, x.y, x.z, x.w};
-    uint32_t y[8];
 #pragma unroll
     for (int i = 0; i < 4; ++i)
 #pragma unroll
         for (int h = 0; h < 2; ++h) {
-            const uint32_t b = __byte_perm(w[i], 0, h ? 0x4342 : 0x4140);  // a byte in the low half of each 16 bits
-            y[2 * i + h] = (b + (b & 0x00800080u)) << 7;                   // the sign bit, doubled, moves one further
+            if constexpr (CVT) {
+                const __half2_raw q =
+                    __nv_cvt_fp8x2_to_halfraw2((__nv_fp8x2_storage_t)(h ? w[i] >> 16 : w[i] & 0xffffu), __NV_E4M3);
+                y[2 * i + h] = (uint32_t)q.x | ((uint32_t)q.y << 16);
+            } else {
+                const uint32_t b = __byte_perm(w[i], 0, h ? 0x4342 : 0x4140);  // a byte in the low half of each 16 bits
+                y[2 * i + h] = (b + (b & 0x00800080u)) << 7;  // the sign bit, doubled, moves one further
+            }
         }
+}
+
+// Raw chunk c of row r into its two chunks of a swizzled fp16 box.
+template <bool CVT>
+__device__ __forceinline__ void put_e4m3x16(uint8_t* box, int r, int c, uint4 x) {
+    uint32_t y[8];
+    e4m3x16_to_f16<CVT>(x, y);
     *reinterpret_cast<uint4*>(box + sw128_offset(r, 2 * c)) = make_uint4(y[0], y[1], y[2], y[3]);
     *reinterpret_cast<uint4*>(box + sw128_offset(r, 2 * c + 1)) = make_uint4(y[4], y[5], y[6], y[7]);
 }
 
 // Four raw chunks, `step` bytes and `rows` rows apart, all loaded before the first is stored; rows
 // from `hidden` on become zeros.
+template <bool CVT = false>
 __device__ __forceinline__ void convert4(const uint8_t* raw, int step, uint8_t* box, int r, int rows, int c, int hidden) {
     uint4 x[4];
 #pragma unroll
@@ -79,7 +95,7 @@ __device__ __forceinline__ void convert4(const uint8_t* raw, int step, uint8_t* 
 #pragma unroll
     for (int u = 0; u < 4; ++u) {
         if (r + u * rows >= hidden) x[u] = make_uint4(0, 0, 0, 0);
-        put_e4m3x16(box, r + u * rows, c, x[u]);
+        put_e4m3x16<CVT>(box, r + u * rows, c, x[u]);
     }
 }
 

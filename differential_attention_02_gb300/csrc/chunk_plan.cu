@@ -60,7 +60,8 @@ __device__ __forceinline__ int block_scan(int v, int* warp_sums, int* total) {
     return __shfl_sync(0xffffffffu, y - w, warp) + x - v;
 }
 
-__global__ void __launch_bounds__(kPlanThreads) chunk_plan_kernel(const __grid_constant__ ChunkParams p) {
+__global__ void __launch_bounds__(kPlanThreads) chunk_plan_kernel(const __grid_constant__ ChunkLists lists) {
+    const ChunkParams& p = lists.p[blockIdx.x];
     __shared__ int warp_sums[kPlanWarps];
     __shared__ float est[kMaxParts];
     __shared__ int keys_s[kTilesInSmem];
@@ -85,13 +86,19 @@ __global__ void __launch_bounds__(kPlanThreads) chunk_plan_kernel(const __grid_c
             n = min(max(next, first), p.T) - first;
             len = min(max(m, 0), p.L);
         }
-        const int nt = (n + p.tm - 1) / p.tm;
+        // Only a sequence's last tile may have few rows.
+        int nt = (n + p.tm - 1) / p.tm, end = nt;
+        if (p.which != kTilesAll && nt > 0) {
+            const bool few = (n - (nt - 1) * p.tm) * p.group <= kFewRows;
+            if (p.which == kTilesMany) nt = end -= few;
+            else nt = few;
+        }
         int sum;
         const int at = n_tiles + block_scan(nt, warp_sums, &sum);
         unsigned long long keys = 0;
         int most = 0;
         for (int i = 0; i < nt && at + i < p.max_tiles; ++i) {
-            const int k = nt - 1 - i;
+            const int k = end - 1 - i;
             const ChunkTile t{b, first + k * p.tm, min(p.tm, n - k * p.tm), len - n + k * p.tm};
             p.tiles[at + i] = t;
             const int q = tile_keys(t);
@@ -225,7 +232,8 @@ __global__ void __launch_bounds__(kPlanThreads) chunk_plan_kernel(const __grid_c
 constexpr int kMergeRows = 32;
 
 template <int DV>
-__global__ void __launch_bounds__(DV * 2) chunk_merge_kernel(const __grid_constant__ ChunkParams p) {
+__global__ void __launch_bounds__(DV * 2) chunk_merge_kernel(const __grid_constant__ ChunkLists lists) {
+    const ChunkParams& p = lists.p[blockIdx.y];
     constexpr int CG = DV / 4, WARPS = CG / 4;
     __shared__ float red[WARPS][kMergeRows];
     pdl_trigger();
@@ -311,18 +319,23 @@ __global__ void __launch_bounds__(DV * 2) chunk_merge_kernel(const __grid_consta
 
 }  // namespace
 
-cudaError_t launch_chunk_plan(const ChunkParams& p, cudaStream_t stream) {
-    return launch_pdl(chunk_plan_kernel, dim3(1), dim3(kPlanThreads), 0, stream, p);
+cudaError_t launch_chunk_plan(const ChunkLists& lists, int n, cudaStream_t stream) {
+    return launch_pdl(chunk_plan_kernel, dim3(n), dim3(kPlanThreads), 0, stream, lists);
 }
 
-cudaError_t launch_chunk_merge(const ChunkParams& p, cudaStream_t stream) {
+cudaError_t launch_chunk_merge(const ChunkLists& lists, int n, cudaStream_t stream) {
     int sms = 0;
     const cudaError_t e = device_sm_count(&sms);
     if (e != cudaSuccess) return e;
-    const int64_t most = (int64_t)p.max_merges * ((p.rows + kMergeRows - 1) / kMergeRows);
-    const dim3 grid((unsigned)(most < 4 * sms ? most : 4 * sms));  // one resident round at most
-    return p.Dv == 128 ? launch_pdl(chunk_merge_kernel<128>, grid, dim3(256), 0, stream, p)
-                       : launch_pdl(chunk_merge_kernel<256>, grid, dim3(512), 0, stream, p);
+    int64_t most = 0;
+    for (int i = 0; i < n; ++i) {
+        const ChunkParams& p = lists.p[i];
+        const int64_t blocks = (int64_t)p.max_merges * ((p.rows + kMergeRows - 1) / kMergeRows);
+        if (blocks > most) most = blocks;
+    }
+    const dim3 grid((unsigned)(most < 4 * sms ? most : 4 * sms), n);  // one resident round at most
+    return lists.p[0].Dv == 128 ? launch_pdl(chunk_merge_kernel<128>, grid, dim3(256), 0, stream, lists)
+                                : launch_pdl(chunk_merge_kernel<256>, grid, dim3(512), 0, stream, lists);
 }
 
 }  // namespace da

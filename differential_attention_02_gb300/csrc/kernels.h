@@ -176,6 +176,13 @@ struct ChunkParams {
     float* part_stats;  // [slot][2][rows][2]: running max (log2 units) and sum of each map
     float* part_o;      // [slot][2][Dv / 4][rows][4]
     int max_tiles, max_entries, max_slots, max_merges, rows, ctas;  // ctas: entries that run at once
+    int which;   // tiles of the list: every one, those of more than kFewRows rows, or the others
+    int q_rows;  // rows of a Q box (chunk_few_tcgen05.cu; 128 or what whole groups leave of it elsewhere)
+};
+enum { kTilesAll = 0, kTilesMany = 1, kTilesFew = 2 };
+// A call's lists, one or two: a kernel takes its own list's parameters.
+struct ChunkLists {
+    ChunkParams p[2];
 };
 // Entry i of the plan, longest class first: each list holds one class from its front and one from
 // its back.
@@ -187,8 +194,10 @@ __host__ __device__ __forceinline__ int64_t chunk_entry(const int* upto, int max
 }
 constexpr int kChunkRows = 128, kChunkKeys = 128;
 constexpr float kChunkNoMax = -1e30f;  // running maximum (log2 units) of a row that has seen no key
-cudaError_t launch_chunk_plan(const ChunkParams& p, cudaStream_t stream);
-cudaError_t launch_chunk_merge(const ChunkParams& p, cudaStream_t stream);
+constexpr int kFewRows = 16;
+cudaError_t launch_chunk_plan(const ChunkLists& lists, int n, cudaStream_t stream);
+cudaError_t launch_chunk_merge(const ChunkLists& lists, int n, cudaStream_t stream);
+cudaError_t launch_chunk_few(const ChunkParams& p, cudaStream_t stream);    // d = 64, Dv = 128, fp8, few rows a tile
 cudaError_t launch_chunk_64(const ChunkParams& p, cudaStream_t stream);     // d = 64, Dv = 128
 cudaError_t launch_chunk_pair(const ChunkParams& p, cudaStream_t stream);   // d = 128, Dv = 256
 
