@@ -1,19 +1,27 @@
 // Differential attention of few new tokens over an fp8 paged cache, d = 64 and Dv = 128:
-// the entries of chunk_tcgen05.cu's plan whose tile has at most 32 rows (tokens x query
+// the entries of the plan (chunk_plan.cu) whose tile has at most 16 rows (tokens x query
 // heads of a KV head), as a batch of decoding or verifying sequences has.
 //
-// There a 128-row tile spends its time on rows that do not exist: the products read each
-// K/V tile once per map as their second operand, and 128 threads per map take the
+// In chunk_tcgen05.cu a 128-row tile spends its time on rows that do not exist: the products
+// read each K/V tile once per map as their second operand, and 128 threads per map take the
 // exponentials of rows that nobody needs. Here the keys are the rows instead,
-//   S_m^T = K_m Q_m^T  [128 keys x rows],   O^T += V^T [P_1^T | P_2^T]  [Dv x 2 rows],
+//   S_m^T = K_m Q_m^T  [128 keys x 16],   O^T += V^T [P_1^T | P_2^T]  [Dv x 32],
 // so each tile is read once, V for both maps together, and the softmax has one thread per
-// key with as many exponentials as there are rows. A row's maximum then lies across the
-// threads; it is moved as lazily as there (a scale of 2^8 of stale maximum costs fp16
-// nothing), so in most tiles the threads only vote that none has to move.
+// key and map with 16 exponentials. A row's maximum then lies across the threads; it is
+// moved as lazily as there (a stale maximum of up to 2^8 costs fp16 nothing), so for most
+// tiles the warps only vote that none has to move, and take the exponentials meanwhile.
 //
-// The conversion of the e4m3 tiles to fp16 remains (chunk_fp8.cuh says why): eight warps
-// do it, four on K and four on V. Queries, sums, scales, masks, hidden V rows and the
-// partial states are those of chunk_tcgen05.cu.
+// K goes from the raw tile into tensor memory (the products' first operand), V into shared
+// memory as fp16 (chunk_fp8.cuh), by four warps each. Queries, sums, scales, masks,
+// hidden V rows and the partial states are those of chunk_tcgen05.cu.
+//
+// Measured on 16 sequences x 5 drafted tokens over 8192 keys, 16 query and 8 KV heads (10 rows a
+// tile; the bytes take 40 us): 113 us in 128-row tiles; here 104 with the conversion's
+// result joined by hand, 84 now. What bounds it is the issue of instructions: 1,500 a key tile on
+// each of the SM's schedulers (conversion and softmax half each), at 0.65 a cycle; the
+// exponentials of 32 rows (94 us), two streams of tiles with accumulators of their own (98 us),
+// loops over the rows with more code than the instruction cache takes (129 us) were slower.
+// A start takes 10 us, most of it instructions fetched for the first time.
 //
 // 20 warps: 0..3 softmax of map 1 and output, 4..7 softmax of map 2, 8 TMA producer, 9 MMA
 // issuer, 12..15 convert K, 16..19 convert V.
@@ -26,7 +34,7 @@
 namespace da {
 namespace {
 
-constexpr int BN = kChunkKeys, D = 64, DV = 128, R = kFewRows;
+constexpr int BN = kChunkKeys, D = 64, DV = 128, R = kFewRows;  // a multiple of 16, a lane per row
 constexpr int kWarpProducer = 8, kWarpMma = 9, kWarpK = 12, kWarpV = 16, kThreads = 640;
 constexpr float kRescaleThreshold = 8.0f;  // log2 units
 
@@ -243,7 +251,7 @@ __global__ void __launch_bounds__(kThreads, 1) chunk_few_kernel(const __grid_con
                 const int hidden = j == last ? tail_row : BN;
 #pragma unroll 1
                 for (int r = r0; r < BN; r += 64)
-                    convert4<true>(raw + r * DV + box * 64 + c * 16, 16 * DV, v + box * kBoxBytes, r, 16, c, hidden);
+                    convert4(raw + r * DV + box * 64 + c * 16, 16 * DV, v + box * kBoxBytes, r, 16, c, hidden);
                 fence_proxy_async_shared();
                 __syncwarp();
                 if (lane == 0) {
@@ -268,7 +276,7 @@ __global__ void __launch_bounds__(kThreads, 1) chunk_few_kernel(const __grid_con
                     uint32_t y[32];
 #pragma unroll
                     for (int c = 0; c < 4; ++c)
-                        e4m3x16_to_f16<true>(*reinterpret_cast<const uint4*>(raw + m * BN * D + ((c ^ ((r >> 1) & 3)) << 4)), y + 8 * c);
+                        e4m3x16_to_f16(*reinterpret_cast<const uint4*>(raw + m * BN * D + ((c ^ ((r >> 1) & 3)) << 4)), y + 8 * c);
                     tmem_st32(tK + s * D + m * (D / 2), y);
                 }
                 tmem_st_wait();

@@ -4,23 +4,17 @@
 // So K and V are brought into shared memory raw and rewritten as fp16 by a warpgroup,
 // and P is fp16, eight times finer than bf16.
 //
-// As fp16 the bits s eeee mmm of an e4m3 value, the magnitude moved to bits 7 .. 13 and
-// the sign to bit 15, are the value times 2^-8, subnormals included (their exponent bias
-// differs by 8), so a pair takes four integer instructions and no arithmetic; the factor
-// 2^8 goes into the score scales and V's. (NaN codes come out as +-480: cached values are
-// finite.)
+// The conversion is the instruction cvt.rn.f16x2.e4m3x2 on the halves of a word. Through the
+// intrinsic, whose result comes in two halves that have to be joined again, it was slower than four
+// integer instructions a pair; written out it is faster: 2 x 1024 tokens at the end of 8192, 16 query and
+// 8 KV heads 262 -> 246 us, d = 128 (2 x 1024 of 4096, 8 heads) 184 -> 166 us, 16 x 5 drafted tokens over
+// 8192 keys 104 -> 84 us.
 //
-// What the path cost on the way, 16 sequences x 5 drafted tokens over 8192 keys, 16
-// query and 8 KV heads: K to bf16 beside a bf16 query 217 us, K to fp16 by the
-// conversion instruction 205, by integers 197, eight chunks of a thread loaded before the
-// first is stored 164, the same in loops small enough for the instruction cache 153, warps
-// without rows kept out 144. What bounds it now is shared memory: a key tile is written
-// raw (32 KB), read (32 KB), written as fp16 (64 KB) and read by the products (128 KB),
-// 2,000 of its 3,800 cycles at the full rate, with the products and the conversion
-// colliding; a bf16 cache's tile moves 192 KB in 2,500.
+// What else the path cost on the way, on those drafted tokens in 128-row tiles: K to bf16 beside a
+// bf16 query 217 us, K to fp16 197, eight chunks of a thread loaded before the first is stored 164,
+// the same in loops small enough for the instruction cache 153, warps without rows kept out 144.
+// (Tiles of few rows now have a kernel of their own, chunk_few_tcgen05.cu.)
 #pragma once
-
-#include <cuda_fp8.h>
 
 #include "common.cuh"
 
@@ -56,38 +50,29 @@ __device__ __forceinline__ float q_row_to_f16(uint8_t* boxes, int r) {
     return __uint_as_float((uint32_t)(127 - shift) << 23);
 }
 
-// Sixteen e4m3 values as fp16 values in pairs, exactly: times 2^-8 by integers, or as they are by
-// the conversion instruction (CVT), a third of the instructions but slower ones.
-template <bool CVT>
+// Sixteen e4m3 values as fp16 values in pairs, exactly.
 __device__ __forceinline__ void e4m3x16_to_f16(uint4 x, uint32_t* y) {
     const uint32_t w[4] = {x.x, x.y, x.z, x.w};
 #pragma unroll
     for (int i = 0; i < 4; ++i)
-#pragma unroll
-        for (int h = 0; h < 2; ++h) {
-            if constexpr (CVT) {
-                const __half2_raw q =
-                    __nv_cvt_fp8x2_to_halfraw2((__nv_fp8x2_storage_t)(h ? w[i] >> 16 : w[i] & 0xffffu), __NV_E4M3);
-                y[2 * i + h] = (uint32_t)q.x | ((uint32_t)q.y << 16);
-            } else {
-                const uint32_t b = __byte_perm(w[i], 0, h ? 0x4342 : 0x4140);  // a byte in the low half of each 16 bits
-                y[2 * i + h] = (b + (b & 0x00800080u)) << 7;  // the sign bit, doubled, moves one further
-            }
-        }
+        asm("{\n\t.reg .b16 lo, hi;\n\t"
+            "mov.b32 {lo, hi}, %2;\n\t"
+            "cvt.rn.f16x2.e4m3x2 %0, lo;\n\t"
+            "cvt.rn.f16x2.e4m3x2 %1, hi;\n\t}"
+            : "=r"(y[2 * i]), "=r"(y[2 * i + 1])
+            : "r"(w[i]));
 }
 
 // Raw chunk c of row r into its two chunks of a swizzled fp16 box.
-template <bool CVT>
 __device__ __forceinline__ void put_e4m3x16(uint8_t* box, int r, int c, uint4 x) {
     uint32_t y[8];
-    e4m3x16_to_f16<CVT>(x, y);
+    e4m3x16_to_f16(x, y);
     *reinterpret_cast<uint4*>(box + sw128_offset(r, 2 * c)) = make_uint4(y[0], y[1], y[2], y[3]);
     *reinterpret_cast<uint4*>(box + sw128_offset(r, 2 * c + 1)) = make_uint4(y[4], y[5], y[6], y[7]);
 }
 
 // Four raw chunks, `step` bytes and `rows` rows apart, all loaded before the first is stored; rows
 // from `hidden` on become zeros.
-template <bool CVT = false>
 __device__ __forceinline__ void convert4(const uint8_t* raw, int step, uint8_t* box, int r, int rows, int c, int hidden) {
     uint4 x[4];
 #pragma unroll
@@ -95,7 +80,7 @@ __device__ __forceinline__ void convert4(const uint8_t* raw, int step, uint8_t* 
 #pragma unroll
     for (int u = 0; u < 4; ++u) {
         if (r + u * rows >= hidden) x[u] = make_uint4(0, 0, 0, 0);
-        put_e4m3x16<CVT>(box, r + u * rows, c, x[u]);
+        put_e4m3x16(box, r + u * rows, c, x[u]);
     }
 }
 
