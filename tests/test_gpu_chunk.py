@@ -176,6 +176,47 @@ def test_one_token_rows_agree_with_the_decode(fp8):
     assert_bf16_parity(got, dec.double().cpu().numpy(), "decode")
 
 
+@pytest.mark.parametrize("group,n_new", [(2, [1, 8, 9, 1, 1, 1, 0, 2, 1, 1, 1, 40]), (1, [16, 17, 1, 0, 15, 1]), (16, [1, 1, 0, 1]),
+                                         (5, [3, 4, 1, 2, 1, 1, 3, 1])])
+def test_few_rows_beside_many(group, n_new):
+    """fp8 batches whose sequences have at most 16 rows on average: tiles of up to 16 rows and longer ones
+    run in kernels of their own; whole, split, and with NaN behind the lengths."""
+    lens = [n + 37 * b * b + 5 for b, n in enumerate(n_new)]
+    edge = 0 if group == 16 else 1  # rows of no sequence before and behind; they count into the average
+    c = Case(n_new, lens, 2 * group, group, 64, True, seed=group, pad=2 * edge, first=edge)
+    assert c.T * group <= 16 * len(n_new)
+    out = torch.full((c.T, 2 * group, 128), 7.0, device="cuda")
+    got = c.run(out=out)
+    c.check(got, f"few beside many, group {group}")
+    assert bool((got[:c.starts[0]] == 7.0).all()) and bool((got[c.starts[-1]:] == 7.0).all())
+    dirty = c.run(pools=ref.poison(c.pools, c.table, c.lens))
+    rows = slice(c.starts[0], c.starts[-1])
+    assert torch.equal(got[rows], dirty[rows])
+
+
+@pytest.mark.parametrize("order", ["rising", "falling", "sink"])
+@pytest.mark.parametrize("n", [2, 20])
+@pytest.mark.parametrize("fp8", [False, True])
+@pytest.mark.parametrize("d", [64, 128])
+def test_moving_maxima(d, fp8, n, order):
+    """Scores that rise key by key (the running maximum moves in every tile), that fall, and one early key
+    far above a long tail whose small weights add up to as much (2^-10 of it each, 1030 keys). A shift of
+    a row's scores multiplies its exponential's argument error only by fp32's 2^-24 x 60: 4e-6 of a weight."""
+    c = Case([n], [1100], 2, 1, d, fp8, seed=40)
+    u = torch.randn(d, generator=torch.Generator().manual_seed(1))
+    u = u / u.norm()
+    x = torch.arange(1100, dtype=torch.float32) / 1100
+    want = {"rising": 30 * x, "falling": 30 * (1 - x), "sink": torch.where(torch.arange(1100) == 3, 6.93, 0.0)}[order]
+    for q in c.q:  # scores: q k / sqrt d, with q = 4 sqrt d u plus a little noise
+        q.copy_((4 * d ** 0.5 * u + 0.02 * torch.randn(q.shape, generator=torch.Generator().manual_seed(2))).to(BF))
+    for p, s in zip(c.pools[:2], c.scales or (1.0, 1.0)):
+        for i in range(18):
+            k = min(64, 1100 - 64 * i)
+            rows = (want[64 * i:64 * i + k, None] / 4 * u) / s
+            p[int(c.table[0, i]), :, :k] = rows.clamp(-448, 448).to(p.dtype)
+    c.check(c.run(), f"{order} d{d} fp8={fp8}")
+
+
 def test_score_range():
     """Queries scaled so that the softmax is nearly flat and nearly one-hot."""
     for scale in (1e-4, 30.0):
