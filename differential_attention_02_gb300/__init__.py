@@ -11,6 +11,7 @@ from __future__ import annotations
 import ctypes
 import os
 import struct
+import threading
 
 import torch
 
@@ -488,15 +489,18 @@ def rope_plan(rotary_dim: int, base: float = 10000.0, interleaved: bool = False,
 # The checks below run on every serving step, where a call's host time can exceed its kernels':
 # plain loops, one attribute access each, and the raw stream handle.
 _raw_stream = torch._C._cuda_getCurrentRawStream
+_current_device = torch._C._cuda_getDevice
+_thread_id = threading.get_ident
+_INT32 = torch.int32
 
 
 def _elsewhere(dev, stream):
     """None when `dev` is the current device and no other stream is asked for; else a context that makes
     both current, so that buffers are allocated on the stream that uses them."""
+    if stream is None and dev.index is not None and dev.index == _current_device():  # (a CPU device has no index)
+        return None
     if dev.type != "cuda":
         raise ValueError("all tensors must be on one CUDA device")
-    if stream is None and dev.index == torch.cuda.current_device():
-        return None
     return torch.cuda.stream(stream if stream is not None else torch.cuda.current_stream(dev))
 
 
@@ -507,18 +511,26 @@ def _on_device(dev, *tensors):
 
 
 def _int32(t, dev, shape, what):
-    if t.dtype != torch.int32 or t.shape != shape or t.device != dev or not t.is_contiguous():
+    if t.dtype != _INT32 or t.shape != shape or t.device != dev or not t.is_contiguous():
         raise ValueError(f"{what} must be a contiguous int32 tensor of shape {list(shape)} on the operands' device")
 
 
 _serving_ws: dict = {}
 
 
+def _kept_workspace(dev):
+    """The kept workspace of this thread and the current stream, if there is one and it may be used."""
+    if torch.cuda.is_current_stream_capturing():
+        return None
+    return _serving_ws.get((dev.index, _raw_stream(dev.index), _thread_id()))
+
+
 def _serving_workspace(nbytes: int, dev) -> torch.Tensor:
-    """Workspace of the current stream: kept per stream, so that calls on two streams share none. During
-    a graph capture a new one from the graph's own memory, so that two graphs share none either."""
+    """Workspace of this thread and the current stream, kept: calls on two streams share none, nor do two
+    threads, whose launches may interleave on one stream. During a graph capture a new one from the graph's
+    own memory, so that two graphs share none either."""
     capturing = torch.cuda.is_current_stream_capturing()
-    key = (dev.index, _raw_stream(dev.index))
+    key = (dev.index, _raw_stream(dev.index), _thread_id())
     buf = None if capturing else _serving_ws.get(key)
     if buf is None or buf.numel() < nbytes:
         buf = torch.empty(nbytes + 256, dtype=torch.uint8, device=dev)
@@ -578,12 +590,13 @@ def diffattn_rope(tensors, rope: RopePlan, positions=None, backward: bool = Fals
 _PACK4 = [struct.Struct(f"={4 * n}q").pack for n in range(5)]
 _PACKI = [struct.Struct(f"={n}i").pack for n in range(5)]
 
+
 def _t3(t: torch.Tensor, T: int, H: int, width: int) -> Tensor4:
     """[T, H, width] rows with a contiguous last dimension -> diffattn_tensor (stride_b unused)."""
-    s = t.stride()
-    if t.shape != (T, H, width) or s[2] != 1:
+    sn, sh, s1 = t.stride()
+    if t.shape != (T, H, width) or s1 != 1:
         raise ValueError(f"ragged rows must be [{T}, {H}, {width}] with a contiguous last dimension")
-    return Tensor4(t.data_ptr(), 0, s[1], s[0])
+    return Tensor4(t.data_ptr(), 0, sh, sn)
 
 
 def _paged_args(dev, k1, k2, v, H_kv, d, block_table, q_start, seq_lens, scales):
@@ -654,7 +667,8 @@ def diffattn_chunk_paged(q1, q2, k1_pages, k2_pages, v_pages, block_table, q_sta
     them. q1, q2: [T, H, d] bf16 rows, sequence b's q_start[b] .. q_start[b + 1] - 1, the last of its
     seq_lens[b] tokens; each sees its sequence up to itself. Pages, block_table, kv_group and scales as for
     diffattn_decode_paged; L = the largest length. Returns [T, H, Dv]; rows of no sequence are left as
-    they are. Calls on different streams use workspaces of their own unless `ws` is given."""
+    they are. Calls on different streams and threads use workspaces of their own unless `ws` is given (whose
+    error word read_error then reads)."""
     dev = q1.device
     ctx = _elsewhere(dev, stream)
     if ctx is not None:
@@ -678,15 +692,21 @@ def diffattn_chunk_paged(q1, q2, k1_pages, k2_pages, v_pages, block_table, q_sta
         out = torch.empty((T, H, Dv), dtype=out_dtype, device=dev)
     elif out.shape != (T, H, Dv) or not out.is_contiguous() or out.device != dev:
         raise ValueError("out must be a contiguous [T, H, Dv] tensor on the operands' device")
-    if ws is None:
-        ws = _serving_workspace(chunk_workspace_bytes(T, B, H, kv_group, L, d, Dv), dev)
     lib = _lib or load_library()
     args = (_t3(q1, T, H, d), _t3(q2, T, H, d), *paged, L, out.data_ptr(), w, T, B, H, kv_group, d, Dv, lam, lam_init, eps)
-    tail = (_dtype_code(out.dtype), ws.data_ptr(), ws.numel(), _raw_stream(dev.index))
+    name, call = (("diffattn_chunk_paged_fp8", lib.diffattn_chunk_paged_fp8) if fp8 else
+                  ("diffattn_chunk_paged", lib.diffattn_chunk_paged))
     if fp8:
-        _check(lib.diffattn_chunk_paged_fp8(*args, *scales, *tail), "diffattn_chunk_paged_fp8")
-    else:
-        _check(lib.diffattn_chunk_paged(*args, *tail), "diffattn_chunk_paged")
+        args += tuple(scales)
+    code, kept = _dtype_code(out.dtype), ws
+    if ws is None:  # the kept workspace, unless the call says that it is too small
+        kept = _kept_workspace(dev)
+        status = ERR_WORKSPACE if kept is None else call(*args, code, kept.data_ptr(), kept.numel(), _raw_stream(dev.index))
+        if status != ERR_WORKSPACE:
+            _check(status, name)
+            return out
+        kept = _serving_workspace(chunk_workspace_bytes(T, B, H, kv_group, L, d, Dv), dev)
+    _check(call(*args, code, kept.data_ptr(), kept.numel(), _raw_stream(dev.index)), name)
     return out
 
 
@@ -921,8 +941,8 @@ def module_serve(x, w_qkv, w_o, n_heads: int, pages, block_table, q_start, seq_l
     same place by construction. Rows of no sequence: their attention is zero.
 
     Four launches of its own beside the two GEMMs: rotation of Q, append, plan and attention (a fifth joins
-    sequences that were split). Calls on different streams share no workspace unless `ws` is given; it then
-    needs chunk_workspace_bytes."""
+    sequences that were split). Calls on different streams and threads share no workspace unless `ws` is
+    given; it then needs chunk_workspace_bytes."""
     ctx = _elsewhere(x.device, stream)
     if ctx is not None:
         with ctx:
@@ -971,8 +991,11 @@ def _serve_attention(x, w_qkv, n_heads, pages, block_table, q_start, seq_lens, l
     if positions is not None:
         _int32(positions, dev, (T,), "positions")
     _on_device(dev, w_qkv, *pages, block_table, q_start, seq_lens)
+    need = max(256, chunk_workspace_bytes(T, seq_lens.shape[0], h, kv_group, L, d, Dv))
     if ws is None:
-        ws = _serving_workspace(max(256, chunk_workspace_bytes(T, seq_lens.shape[0], h, kv_group, L, d, Dv)), dev)
+        ws = _serving_workspace(need, dev)
+    elif ws.numel() < need:
+        raise ValueError(f"ws must have {need} bytes (chunk_workspace_bytes)")
     # rows of no sequence are written by no kernel, and W_O reads them
     att = torch.zeros((T, h, Dv), dtype=att_dtype, device=dev)
     if T:

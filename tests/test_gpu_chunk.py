@@ -357,3 +357,26 @@ def test_shape_refusals():
             f()
     with pytest.raises(da.DiffAttnError):
         call(L=65)  # past the table
+
+
+def test_two_threads_on_one_stream():
+    """Calls of two threads may interleave their launches on one stream: each has a workspace of its own."""
+    import threading
+    cases = [Case([2, 90], [4000, 1500], 4, 1, 64, seed=50), Case([3, 1, 7], [2000, 3000, 900], 4, 1, 64, True, seed=51)]
+    want = [c.run() for c in cases]
+    bad = []
+
+    def work(c, want):
+        dev = [x.cuda() for x in c.q], [p.cuda() for p in c.pools]
+        rest = c.table.cuda(), _i32(c.starts), _i32(c.lens)
+        for _ in range(40):
+            got = da.diffattn_chunk_paged(*dev[0], *dev[1], *rest, LAM, LI, L=c.L, scales=c.scales)
+            torch.cuda.current_stream().synchronize()
+            if not torch.equal(got, want):
+                bad.append(c)
+    threads = [threading.Thread(target=work, args=a) for a in zip(cases, want)]
+    for t in threads:
+        t.start()
+    for t in threads:
+        t.join()
+    assert not bad
