@@ -127,7 +127,7 @@ struct AppendChunkParams {
     int64_t page_stride[3], head_stride[3], row_stride[3];  // elements
     const int32_t *block_table, *q_start, *seq_lens;       // [B][max_pages], [B + 1], [B]
     int max_pages, num_pages, T, B, H_kv, d, Dv, in_f16, fp8;
-    float scale[3];                                        // cache value = stored value * scale
+    float scale[3], inv[3];                                // cache value = stored value * scale; 1 / scale, set by the launcher
     RopeTable table;                                       // rotation of K1 and K2 (rotary 0: none)
     int head_splits;                                       // warps per token, set by the launcher
 };

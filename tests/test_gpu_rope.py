@@ -328,3 +328,27 @@ def test_unsorted_starts_stay_inside():
     dev = [p.cuda() for p in pools]
     da.diffattn_kv_append_chunk_paged(*new, *dev, table.cuda(), _i32([7, -3, 100, 2]), _i32([64, 5, 64]))
     torch.cuda.synchronize()
+
+
+@pytest.mark.parametrize("scale", [0.0113, 1.0, 3.0, 2.0 ** -61, 2.0 ** 61, 1e-38, 3e38, 1e-30])
+def test_append_fp8_quantizes_as_the_single_token_append(scale):
+    """e4m3(x / scale) of the correctly rounded quotient, bit for bit: values next to the borders between
+    codes (the midpoints times the scale and their neighbours), every magnitude, infinities and NaN."""
+    mid = torch.arange(0, 0x7E, dtype=torch.int32).to(torch.uint8).view(torch.float8_e4m3fn).float()
+    mid = (mid[:-1] + mid[1:]) / 2 * scale
+    g = torch.Generator().manual_seed(9)
+    x = torch.cat([mid, -mid, torch.randn(2000, generator=g) * 100 * min(scale, 1e30),
+                   torch.randn(1000, generator=g) * 1e-39, torch.tensor([float("inf"), float("-inf"), 0.0, -0.0, 3e38])])
+    x = torch.cat([x.to(torch.bfloat16)] + [(x.to(torch.bfloat16).view(torch.int16) + i).view(torch.bfloat16) for i in (-1, 1)])
+    x = x[~x.isnan()]
+    T = -(-x.numel() // 256)
+    x = torch.cat([x, torch.zeros(T * 256 - x.numel(), dtype=x.dtype)]).view(T, 1, 256).cuda()
+    new = [x[..., :64], x[..., 64:128], x[..., 128:]]
+    make = lambda: [torch.zeros(-(-T // 64), 1, 64, w, dtype=torch.uint8, device="cuda") for w in (64, 64, 128)]  # noqa: E731
+    a, b = make(), make()
+    table = torch.arange(-(-T // 64), dtype=torch.int32, device="cuda")[None]
+    da.diffattn_kv_append_chunk_paged(*new, *a, table, _i32([0, T]), _i32([T]), scales=(scale,) * 3)
+    for t in range(T):
+        da.diffattn_kv_append_paged(*(n[t:t + 1].contiguous() for n in new), *b, table, _i32([t + 1]), scales=(scale,) * 3)
+    for p, q in zip(a, b):
+        assert torch.equal(p, q)
