@@ -994,8 +994,6 @@ bool chunk_layout(int B, int H, int kv_group, int T, int L, int d, int Dv, bool 
     const int sms = n_sm > 0 ? n_sm : 152;
     l->ctas = d == 64 ? sms : sms / 2;  // one CTA per SM; a pair per work item for the wide heads
     l->tm = kChunkRows / kv_group;
-    // Cutting needs an item of at least two key tiles.
-    const int64_t extra = L > kChunkKeys ? l->ctas : 0;
     const int64_t rows = (int64_t)T * kv_group, sequences = std::min(B, T);
     const bool few = fp8 && d == 64 && kv_group <= kFewRows && rows <= kFewRows * sequences;
     l->n = few && rows > kFewRows ? 2 : 1;
@@ -1006,6 +1004,10 @@ bool chunk_layout(int B, int H, int kv_group, int T, int L, int d, int Dv, bool 
         x.q_rows = (x.which == kTilesFew ? kFewRows / kv_group : l->tm) * kv_group;
         x.rows = (int)std::min<int64_t>(x.q_rows, rows);
         const int64_t tiles = x.which == kTilesFew ? sequences : (int64_t)T / l->tm + sequences;
+        // Entries that cutting may add: three rounds of CTAs (one, two, three: 500 tokens at the end of 65,000 keys
+        // 348, 348, 326 us; 32 ragged decoding sequences 102, 86, 86). Of two lists, whose CTAs without an entry
+        // cost 1 us a round, one and two. Cutting needs an item of at least two key tiles.
+        const int64_t extra = L > kChunkKeys ? (l->n == 1 ? 3 : 1 + i) * (int64_t)l->ctas : 0;
         const int64_t entries = tiles * H_kv + extra;
         if (entries * 2 > INT32_MAX) return false;
         x.max_tiles = (int)tiles;

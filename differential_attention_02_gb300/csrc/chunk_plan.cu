@@ -10,14 +10,15 @@
 // prompts' chunks have a thousand items, and splitting them only costs partial states.
 // Of the lengths that cut the longest item into 1 .. 64 parts, the one with the shortest
 // estimated makespan is taken, at a fixed cost per entry (start and epilogue: about 4 us
-// against 1.3 us a key tile) and a further one per partial state. With W key tiles in all
-// and C entries at a time, a length k >= W / C adds at most C entries and leaves at most
-// 2 C of them partial (an item of n > k key tiles has ceil(n / k) <= 2 n / k parts), which
-// sizes the lists and the workspace on the host. Shorter ones would not pay: cutting the
-// whole row of items at every multiple of W / C, which balances any batch within an
-// entry, was measured against the whole items of larger batches and was no faster (four
-// prompts' chunks 592 against 586 us, a mixed batch 110 against 104 us), since every cut
-// costs a partial state of 128 KB and its merge.
+// against 1.3 us a key tile; 5 against 0.8 in tiles of few rows) and a further one per partial
+// state. With W key tiles in all and room for E more entries (three rounds of CTAs, api.cu),
+// a length k >= W / E adds at most E entries and leaves at most 2 E of them partial (an
+// item of n > k key tiles has ceil(n / k) <= 2 n / k parts), which sizes the lists and
+// the workspace on the host. Batches of two rounds of items and more stay whole: a mixed
+// batch of 428 items took 106 us cut and 102 whole, and cutting the whole row of items
+// at every multiple of W / C, which balances any batch within an entry, was no faster either
+// (four prompts' chunks 592 against 586 us, the mixed batch 110 against 104), since
+// every cut costs a partial state of 128 KB and its merge.
 #include <math.h>
 
 #include "common.cuh"
@@ -29,7 +30,7 @@ namespace {
 constexpr int kPlanThreads = 512, kPlanWarps = kPlanThreads / 32;
 constexpr int kMaxParts = 64;
 constexpr int kTilesInSmem = 2048;  // longer lists are read back from the workspace
-constexpr float kEntryCost = 3.f;
+constexpr float kEntryCost = 3.f, kFewEntryCost = 6.f;  // key tiles' times
 
 __device__ __forceinline__ int tile_keys(const ChunkTile& t) {  // key tiles that the tile's last token sees
     const int keys = t.pos0 + t.ntok;
@@ -123,8 +124,9 @@ __global__ void __launch_bounds__(kPlanThreads) chunk_plan_kernel(const __grid_c
     int k = longest, entries = n_items;
     const bool may_split = p.max_slots > 0 && W > 0 && n_items < 2 * p.ctas;
     if (may_split) {
-        const int least = (int)((W + p.ctas - 1) / p.ctas);  // at most `longest`, or nothing is split
-        const float split_cost = kEntryCost + 5.f * (float)p.rows / kChunkRows, ctas = (float)p.ctas;
+        const int least = (int)((W + p.max_merges - 1) / p.max_merges);  // where it is above `longest`, nothing is split
+        const float entry_cost = p.which == kTilesFew ? kFewEntryCost : kEntryCost;
+        const float split_cost = entry_cost + 5.f * (float)p.rows / kChunkRows, ctas = (float)p.ctas;
         for (int s = 1 + warp; s <= kMaxParts; s += kPlanWarps) {
             const int ks = (longest + s - 1) / s;
             float e = INFINITY;
@@ -139,8 +141,8 @@ __global__ void __launch_bounds__(kPlanThreads) chunk_plan_kernel(const __grid_c
                 all = __reduce_add_sync(0xffffffffu, items) * p.H_kv;
                 const float all_items = (float)all;
                 const float all_split = (float)__reduce_add_sync(0xffffffffu, split) * (float)p.H_kv;
-                const float cost = (float)ks + (s > 1 ? split_cost : kEntryCost);
-                const float sum = (float)W + kEntryCost * all_items + (split_cost - kEntryCost) * all_split;
+                const float cost = (float)ks + (s > 1 ? split_cost : entry_cost);
+                const float sum = (float)W + entry_cost * all_items + (split_cost - entry_cost) * all_split;
                 e = fminf(ceilf(all_items / ctas) * cost, sum / ctas + 0.5f * cost);
             }
             if (lane == 0) {
