@@ -1003,11 +1003,15 @@ bool chunk_layout(int B, int H, int kv_group, int T, int L, int d, int Dv, bool 
         x.which = l->n == 1 ? (few ? kTilesFew : kTilesAll) : i == 0 ? kTilesMany : kTilesFew;
         x.q_rows = (x.which == kTilesFew ? kFewRows / kv_group : l->tm) * kv_group;
         x.rows = (int)std::min<int64_t>(x.q_rows, rows);
-        const int64_t tiles = x.which == kTilesFew ? sequences : (int64_t)T / l->tm + sequences;
+        // Full tiles and each sequence's last one, which in the longer tiles' list has more than kFewRows rows.
+        const int64_t last = x.which == kTilesMany ? std::min(sequences, rows / (kFewRows + 1)) : sequences;
+        const int64_t tiles = x.which == kTilesFew ? sequences : (int64_t)T / l->tm + last;
         // Entries that cutting may add: three rounds of CTAs (one, two, three: 500 tokens at the end of 65,000 keys
-        // 348, 348, 326 us; 32 ragged decoding sequences 102, 86, 86). Of two lists, whose CTAs without an entry
-        // cost 1 us a round, one and two. Cutting needs an item of at least two key tiles.
-        const int64_t extra = L > kChunkKeys ? (l->n == 1 ? 3 : 1 + i) * (int64_t)l->ctas : 0;
+        // 348, 348, 326 us; 32 ragged decoding sequences 102, 86, 86). Of two lists two rounds for the few-row
+        // tiles; for the longer ones, of which there may be none, what is left of a round: CTAs without an entry
+        // cost 2 us a round. Cutting needs an item of at least two key tiles.
+        const int64_t ctas = l->ctas;
+        const int64_t extra = L <= kChunkKeys ? 0 : l->n == 1 ? 3 * ctas : i == 1 ? 2 * ctas : ctas - tiles * H_kv % ctas;
         const int64_t entries = tiles * H_kv + extra;
         if (entries * 2 > INT32_MAX) return false;
         x.max_tiles = (int)tiles;
