@@ -380,3 +380,21 @@ def test_two_threads_on_one_stream():
     for t in threads:
         t.join()
     assert not bad
+
+
+@pytest.mark.parametrize("fp8", [False, True])
+@pytest.mark.parametrize("d", [64, 128])
+def test_batches_of_next_to_nothing(d, fp8):
+    """No sequence has a new token; one of a thousand has; a cache of a single token."""
+    c = Case([3, 2], [100, 200], 4, 2, d, fp8, seed=60)
+    out = torch.full((5, 4, 2 * d), 7.0, device="cuda")
+    c.run(starts=[2, 2, 2], out=out)
+    assert bool((out == 7.0).all())  # rows of no sequence
+    n = [0] * 1000
+    n[613] = 2
+    lens = [1 + b % 60 for b in range(1000)]
+    lens[613] = 333
+    c = Case(n, lens, 2, 1, d, fp8, seed=61)
+    c.check(c.run(), "one of a thousand")
+    c = Case([1], [1], 2, 1, d, fp8, seed=62)
+    c.check(c.run(L=1), "a cache of one token")
