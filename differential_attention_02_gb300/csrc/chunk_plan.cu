@@ -10,8 +10,8 @@
 // prompts' chunks have a thousand items, and splitting them only costs partial states.
 // Of the lengths that cut the longest item into 1 .. 64 parts, the one with the shortest
 // estimated makespan is taken, at a fixed cost per entry (start and epilogue: about 4 us
-// against 1.3 us a key tile; 5 against 0.8 in tiles of few rows) and a further one per partial
-// state. With W key tiles in all and room for E more entries (three rounds of CTAs, api.cu),
+// against 1.3 us a key tile; 5 against 0.8 in tiles of few rows), a further one per partial
+// state, and the merge's own time. With W key tiles in all and room for E more entries (three rounds of CTAs, api.cu),
 // a length k >= W / E adds at most E entries and leaves at most 2 E of them partial (an
 // item of n > k key tiles has ceil(n / k) <= 2 n / k parts), which sizes the lists and
 // the workspace on the host. Batches of two rounds of items and more stay whole: a mixed
@@ -30,7 +30,7 @@ namespace {
 constexpr int kPlanThreads = 512, kPlanWarps = kPlanThreads / 32;
 constexpr int kMaxParts = 64;
 constexpr int kTilesInSmem = 2048;  // longer lists are read back from the workspace
-constexpr float kEntryCost = 3.f, kFewEntryCost = 6.f;  // key tiles' times
+constexpr float kEntryCost = 3.f, kFewEntryCost = 6.f, kMergeCost = 3.f, kMergeStep = 0.45f;  // key tiles' times
 
 __device__ __forceinline__ int tile_keys(const ChunkTile& t) {  // key tiles that the tile's last token sees
     const int keys = t.pos0 + t.ntok;
@@ -127,6 +127,8 @@ __global__ void __launch_bounds__(kPlanThreads) chunk_plan_kernel(const __grid_c
         const int least = (int)((W + p.max_merges - 1) / p.max_merges);  // where it is above `longest`, nothing is split
         const float entry_cost = p.which == kTilesFew ? kFewEntryCost : kEntryCost;
         const float split_cost = entry_cost + 5.f * (float)p.rows / kChunkRows, ctas = (float)p.ctas;
+        int width = 32;  // lanes that the merge gives to a row's parts: 32 / width (below)
+        while (width / 2 >= p.rows) width /= 2;
         for (int s = 1 + warp; s <= kMaxParts; s += kPlanWarps) {
             const int ks = (longest + s - 1) / s;
             float e = INFINITY;
@@ -143,7 +145,11 @@ __global__ void __launch_bounds__(kPlanThreads) chunk_plan_kernel(const __grid_c
                 const float all_split = (float)__reduce_add_sync(0xffffffffu, split) * (float)p.H_kv;
                 const float cost = (float)ks + (s > 1 ? split_cost : entry_cost);
                 const float sum = (float)W + entry_cost * all_items + (split_cost - entry_cost) * all_split;
-                e = fminf(ceilf(all_items / ctas) * cost, sum / ctas + 0.5f * cost);
+                // Whole items differ in length and the short ones fill in behind the long ones; parts are alike
+                // (with one factor 160 ragged decoding items were cut, 84 us against 77 whole, and 64 of d = 128, 109
+                // against 92; without the merge's steps one item of 98 key tiles got 49 parts, 53 us against 33).
+                e = fminf(ceilf(all_items / ctas) * cost, sum / ctas + (s > 1 ? 0.75f : 0.5f) * cost) +
+                    (s > 1 ? kMergeCost + kMergeStep * (float)((s * width + 31) / 32) : 0.f);
             }
             if (lane == 0) {
                 est[s - 1] = e;
