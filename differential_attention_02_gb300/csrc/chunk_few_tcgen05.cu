@@ -118,9 +118,12 @@ __global__ void __launch_bounds__(kThreads, 1) chunk_few_kernel(const __grid_con
     }
     pdl_trigger();
     pdl_wait();  // the plan, Q and the newest cache rows come from earlier kernels
+    const int ei = (int)blockIdx.x;
+    ChunkEntry guess{};
+    if (threadIdx.x == 0) guess = p.entries[ei];  // the right one in the longest class: one latency instead of two
     const ChunkPlan plan = *p.plan;
-    if ((int)blockIdx.x >= plan.upto[3]) return;  // every thread of the CTA
-    if (threadIdx.x == 0) bars->e = p.entries[chunk_entry(plan.upto, p.max_entries, (int)blockIdx.x)];
+    if (ei >= plan.upto[3]) return;  // every thread of the CTA
+    if (threadIdx.x == 0) bars->e = ei < plan.upto[0] ? guess : p.entries[chunk_entry(plan.upto, p.max_entries, ei)];
     if (warp == kWarpMma) {
         tmem_alloc(&bars->tmem_base, kTmemCols);
         tmem_relinquish();

@@ -142,10 +142,11 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(Cfg<FP8>::kThreads, 
     cluster_sync_start();
     pdl_trigger();
     pdl_wait();  // the plan, Q and the newest cache rows come from earlier kernels
-    const ChunkPlan plan = *p.plan;
     const int ei = (int)(blockIdx.x >> 1);
+    ChunkEntry e = p.entries[ei];  // the right one in the longest class: one latency instead of two
+    const ChunkPlan plan = *p.plan;
     if (ei >= plan.upto[3]) return;  // every thread of both CTAs
-    const ChunkEntry e = p.entries[chunk_entry(plan.upto, p.max_entries, ei)];
+    if (ei >= plan.upto[0]) e = p.entries[chunk_entry(plan.upto, p.max_entries, ei)];
     const int hk = e.hk;
     if (warp == 1) {
         tmem_alloc(&bars->tmem_base, C::kTmemCols);
@@ -517,7 +518,9 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(Cfg<FP8>::kThreads, 
         // The exchange buffers live in the K/V rings: both CTAs must be past their last MMA.
         ok = pair_sync(&bars->xsync, peer, 0, abort_flag, p.err, 0x63) && ok;
         ok = __all_sync(0xffffffffu, ok);
-        if (epi && ok) {
+        // A warp without rows has nothing to exchange or store (272 items of 1 or 2 rows: 61 -> 51 us).
+        const bool mine = epi && lg * 32 < rows;
+        if (mine && ok) {
             // The half of this map's row the peer finishes -> the peer's buffer.
             const uint32_t peer_x = mapa_shared(smem_u32(xbuf + r * C::kXStride), peer);
 #pragma unroll 1
@@ -535,7 +538,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(Cfg<FP8>::kThreads, 
         ok = __all_sync(0xffffffffu, ok);
         const float* xrow = xbuf + r * C::kXStride;
         float ss = 0.f;
-        if (epi && ok) {
+        if (mine && ok) {
 #pragma unroll 1
             for (int c = 0; c < H2 / 32; ++c) {
                 uint32_t o[32];
@@ -555,7 +558,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(Cfg<FP8>::kThreads, 
         ok = __all_sync(0xffffffffu, ok && !*abort_flag);
         uint8_t* stage = smem + C::kOffOut;
         const bool out16 = p.out_bf16 || p.out_f16;
-        if (epi && ok) {
+        if (mine && ok) {
             const float tot = ss + ssbuf[r];
             const float rsc = tot == 0.f ? 0.f : (1.0f - p.lambda_init) / sqrtf(tot / (float)DV + p.eps);
             const bool f16 = p.out_f16 != 0;

@@ -143,12 +143,14 @@ __global__ void __launch_bounds__(Cfg<FP8>::kThreads, 1) chunk_kernel(const __gr
     }
     pdl_trigger();
     pdl_wait();  // the plan, Q and the newest cache rows come from earlier kernels
-    const ChunkPlan plan = *p.plan;
     const int ei = (int)(blockIdx.x);
+    ChunkEntry guess{};
+    if (threadIdx.x == 0) guess = p.entries[ei];  // the right one in the longest class: one latency instead of two
+    const ChunkPlan plan = *p.plan;
     if (ei >= plan.upto[3]) return;  // every thread of the CTA
     // The entry lives in shared memory, so that the softmax loop keeps its registers for scores.
     if (threadIdx.x == 0) {
-        bars->e = p.entries[chunk_entry(plan.upto, p.max_entries, ei)];
+        bars->e = ei < plan.upto[0] ? guess : p.entries[chunk_entry(plan.upto, p.max_entries, ei)];
         if constexpr (FP8) {
             // One arrival per softmax warp that has rows of the entry: with few tokens the others stay out
             // and leave the sub-partitions to the conversion (153 -> 144 us for 10 rows a tile; with a bf16
@@ -550,7 +552,8 @@ __global__ void __launch_bounds__(Cfg<FP8>::kThreads, 1) chunk_kernel(const __gr
             constexpr int kHalf = DV / 2;  // columns handled by this group
             float oh[kHalf];
             float ss = 0.f;
-            if (ok) {
+            const bool mine = lg * 32 < rows;  // a warp without rows has nothing to add up or store
+            if (ok && mine) {
 #pragma unroll
                 for (int c = 0; c < kHalf / 32; ++c) {
                     uint32_t o1[32], o2[32];
@@ -573,7 +576,7 @@ __global__ void __launch_bounds__(Cfg<FP8>::kThreads, 1) chunk_kernel(const __gr
             // the row range of the next sequence.
             uint8_t* stage = stages;
             const bool out16 = p.out_bf16 || p.out_f16;
-            if (ok) {
+            if (ok && mine) {
                 const float tot = epi[2 * BM + r] + epi[3 * BM + r];
                 const float rsc = tot == 0.f ? 0.f : (1.0f - p.lambda_init) / sqrtf(tot / (float)DV + p.eps);
                 const float* w = p.norm_w ? p.norm_w + g * kHalf : nullptr;
