@@ -50,6 +50,13 @@ __device__ __forceinline__ float q_row_to_f16(uint8_t* boxes, int r) {
     return __uint_as_float((uint32_t)(127 - shift) << 23);
 }
 
+// The score scale of a query row (log2 units): its map's times the row's 2^-shift, kept above zero. Masked
+// scores are -inf, and -inf times a scale that underflowed to 0 would be NaN. A row whose scale is raised
+// here has raw scores below 2^32 (2^16 x 448 x 128 channels), so scores below 2^-94: 0 either way.
+__device__ __forceinline__ float row_score_scale(float map_scale, float down) {
+    return fmaxf(map_scale * down, 0x1p-126f);
+}
+
 // Sixteen e4m3 values as fp16 values in pairs, exactly.
 __device__ __forceinline__ void e4m3x16_to_f16(uint4 x, uint32_t* y) {
     const uint32_t w[4] = {x.x, x.y, x.z, x.w};

@@ -322,7 +322,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(Cfg<FP8>::kThreads, 
         float sl2 = rank ? p.scale2_log2 : p.scale1_log2;
         if (FP8 && nkv > 0) {
             ok = mbar_wait_warp(&bars->q_full, 0, abort_flag, p.err, 0x69);
-            if (ok) sl2 *= q_row_to_f16<D>(qs, r);
+            if (ok) sl2 = row_score_scale(sl2, q_row_to_f16<D>(qs, r));
             __syncwarp();
             if (lane == 0) mbar_arrive(&bars->q_ready);
         }

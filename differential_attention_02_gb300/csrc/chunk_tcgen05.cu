@@ -439,7 +439,7 @@ __global__ void __launch_bounds__(Cfg<FP8>::kThreads, 1) chunk_kernel(const __gr
         bool ok = true;
         if (FP8 && n_mine > 0) {
             ok = mbar_wait_warp(&bars->q_full, 0, abort_flag, p.err, 0x46);
-            if (ok) sl2 *= q_row_to_f16<D>(g == 0 ? q1s : q2s, r);
+            if (ok) sl2 = row_score_scale(sl2, q_row_to_f16<D>(g == 0 ? q1s : q2s, r));
             __syncwarp();
             if (lane == 0) mbar_arrive(&bars->q_ready);
         }
