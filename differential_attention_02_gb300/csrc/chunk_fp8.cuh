@@ -24,7 +24,8 @@ namespace da {
 // place in its swizzled boxes, by the thread that owns the row; returns 2^-shift. The row's
 // largest exponent goes to 2^15, so nothing overflows, and what falls below fp16's normal
 // range is smaller than the row's maximum by 2^-29 and more: less than the fp32 sums of the
-// scores keep. (Rows below 2^-85 keep a factor of 2^100: their scores are 0 either way.)
+// scores keep. (Rows below 2^-111 keep a factor of 2^126, the last whose inverse is a normal
+// number; their values still come to 2^-7 and more, well inside fp16's normal range.)
 template <int D>
 __device__ __forceinline__ float q_row_to_f16(uint8_t* boxes, int r) {
     uint32_t m = 0;  // largest magnitude of a packed pair's halves
@@ -35,7 +36,7 @@ __device__ __forceinline__ float q_row_to_f16(uint8_t* boxes, int r) {
 #pragma unroll
         for (int i = 0; i < 4; ++i) m = max(m, max(w[i] & 0x7fffu, (w[i] >> 16) & 0x7fffu));
     }
-    const int shift = min(142 - (int)(m >> 7), 100);
+    const int shift = min(142 - (int)(m >> 7), 126);
     const float up = __uint_as_float((uint32_t)(127 + shift) << 23);
 #pragma unroll
     for (int c = 0; c < D / 8; ++c) {

@@ -10,7 +10,7 @@ import serving_reference as ref
 from test_gpu_chunk import Case
 
 pytestmark = pytest.mark.gpu
-BF = torch.bfloat16
+F8, BF = torch.float8_e4m3fn, torch.bfloat16
 
 # New tokens and lengths of batches that go to the kernel for tiles of few rows, to it and the 128-row
 # one in one call, to the 128-row one alone, and to the CTA pair's (d = 128).
@@ -45,3 +45,15 @@ def test_scores_that_vanish(kind, size, k_scale):
     c.q = [(x.float() * size).to(BF) for x in c.q]
     c.scales = (k_scale, k_scale, ref.SCALES[2])
     c.check(c.run(), f"{kind} rows of {size}, K scale {k_scale}")
+
+
+@kinds
+def test_tiny_queries_and_a_large_scale(kind):
+    """Query rows at the lower end of bf16's range against a K scale that brings their scores back to unit
+    size: the rows' power of two has to cover the whole range."""
+    c = _case(kind, seed=2)
+    c.q = [(x.float() * 2.0 ** -122).to(BF) for x in c.q]
+    g = torch.Generator().manual_seed(3)
+    c.pools[:2] = [(torch.randn(p.shape, generator=g) * 16).to(F8) for p in c.pools[:2]]
+    c.scales = (2.0 ** 118, 2.0 ** 118, ref.SCALES[2])
+    c.check(c.run(), kind)
