@@ -41,7 +41,7 @@ namespace {
 
 constexpr int BN = kChunkKeys, D = 64, DV = 128, R = kFewRows;  // a multiple of 16, a lane per row
 constexpr int kWarpProducer = 8, kWarpMma = 9, kWarpProducerV = 10, kWarpPv = 11, kWarpK = 12, kWarpV = 16, kThreads = 640;
-constexpr float kRescaleThreshold = 8.0f;  // log2 units
+constexpr float kRescaleThreshold = 8.0f + kWeightShift;  // log2 units over the maximum as it is held (chunk_fp8.cuh)
 
 // Register split (see fwd_tcgen05.cu): 2 x 144 + 3 x 64 = 5 x 96, what the block is launched with.
 constexpr int kRegsLaunch = 96, kRegsSoftmax = 144, kRegsOther = 64;
@@ -405,7 +405,7 @@ __global__ void __launch_bounds__(kThreads, 1) chunk_few_kernel(const __grid_con
                 if (t < R) {
                     const float m0 = mx[t];
                     const float m1 = fmaxf(fmaxf(fmaxf(bars->most[m][0][t], bars->most[m][1][t]),
-                                                 fmaxf(bars->most[m][2][t], bars->most[m][3][t])), m0);
+                                                 fmaxf(bars->most[m][2][t], bars->most[m][3][t])) - kWeightShift, m0);
                     mx[t] = m1;
                     bars->alpha[m][t] = fast_exp2(m0 - m1);
                 }

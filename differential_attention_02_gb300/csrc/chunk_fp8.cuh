@@ -2,7 +2,8 @@
 // tensor-core product have one type; every e4m3 value is an fp16 value, and a bf16 query
 // row becomes one of fp16 times a power of two, which goes into the row's score scale.
 // So K and V are brought into shared memory raw and rewritten as fp16 by a warpgroup,
-// and P is fp16, eight times finer than bf16.
+// and P is fp16, eight times finer than bf16 down to 2^-21 of a row's largest
+// weight (kWeightShift).
 //
 // The conversion is the instruction cvt.rn.f16x2.e4m3x2 on the halves of a word. Through the
 // intrinsic, whose result comes in two halves that have to be joined again, it was slower than four
@@ -19,6 +20,15 @@
 #include "common.cuh"
 
 namespace da {
+
+// The weights beside an fp16 V are fp16 too, whose values end at 2^-24 (weights below 2^-25 become 0 in
+// the product), while the fp32 sum of the weights keeps them. So the running maximum is held lower by this many
+// powers of two: a row's largest weight is 2^7, up to 2^15 where the maximum lags by its threshold of 2^8, both
+// within fp16's 65504, and a weight is off by at most 2^-32 of the row's largest. Sums, accumulators and partial
+// states all carry the factor, and it leaves with the division by the sum. It costs nothing (a constant in the
+// maximum's multiplication). A tail of 8191 keys 15, 17 and 18 nats below one key whose V row is zero, relative RMS
+// of the output: up to 9e-3, 5e-2 and 1.4e-1 without it, 3e-4, 5e-4 and 1.2e-3 with it.
+constexpr float kWeightShift = 7.f;  // log2 units
 
 // fp8 cache: a query row of D bf16 values as fp16 values of the same row times 2^shift, in
 // place in its swizzled boxes, by the thread that owns the row; returns 2^-shift. The row's

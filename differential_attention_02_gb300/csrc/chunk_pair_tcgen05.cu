@@ -362,7 +362,8 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(Cfg<FP8>::kThreads, 
                 mx3 = fmax3(mx3, __uint_as_float(sr[i + 6]), __uint_as_float(sr[i + 7]));
             }
             // kChunkNoMax: see chunk_tcgen05.cu (rows that have seen no key).
-            const float m_new = fmax3(fmaxf(mx0, mx1), mx2, mx3) * sl2;
+            const float top = fmax3(fmaxf(mx0, mx1), mx2, mx3);
+            const float m_new = FP8 ? fmaf(top, sl2, -kWeightShift) : top * sl2;
             float alpha = 1.f;
             bool rescale = false;
             if (m_new > m_used + kRescaleThreshold) {

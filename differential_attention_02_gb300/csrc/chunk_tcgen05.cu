@@ -471,7 +471,8 @@ __global__ void __launch_bounds__(Cfg<FP8>::kThreads, 1) chunk_kernel(const __gr
             // The maximum starts at the finite floor kChunkNoMax: a row that has seen no key keeps it,
             // so that its weights are exp2(-inf) = 0, and its first real maximum rescales the empty
             // sums by exp2(floor - max) = 0.
-            const float m_new = fmax3(fmaxf(mx0, mx1), mx2, mx3) * sl2;
+            const float top = fmax3(fmaxf(mx0, mx1), mx2, mx3);
+            const float m_new = FP8 ? fmaf(top, sl2, -kWeightShift) : top * sl2;
             float alpha = 1.f;
             bool rescale = false;
             if (m_new > m_used + kRescaleThreshold) {

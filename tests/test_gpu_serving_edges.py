@@ -2,11 +2,14 @@
 scales at the ends of what the call takes, small weights behind a large one, and each of its three
 kernels (few rows, 128-row tiles, the CTA pair's) with the options that the bf16 tests cover."""
 
+import math
+
 import pytest
 import torch
 
 import differential_attention_02_gb300 as da
 import serving_reference as ref
+from parity import errors
 from test_gpu_chunk import Case
 
 pytestmark = pytest.mark.gpu
@@ -57,3 +60,29 @@ def test_tiny_queries_and_a_large_scale(kind):
     c.pools[:2] = [(torch.randn(p.shape, generator=g) * 16).to(F8) for p in c.pools[:2]]
     c.scales = (2.0 ** 118, 2.0 ** 118, ref.SCALES[2])
     c.check(c.run(), kind)
+
+
+@pytest.mark.parametrize("at", [3, 5000])
+@pytest.mark.parametrize("nats", [15.0, 17.0, 26 * math.log(2)])
+@pytest.mark.parametrize("d,n", [(64, 2), (64, 20), (128, 2), (128, 20)])
+def test_tail_behind_a_sink(d, n, nats, at):
+    """One key far above a tail of 8191 whose scores are standard normal, its V row zero: the output is the
+    tail's alone. A weight of the product is off by at most 2^-32 of the row's largest (half a step of
+    fp16's smallest values, 2^-25, where the largest stands at 2^7 or more), so by 2^-32 / sqrt 3 RMS, and the
+    tail's weights are e^(1 - nats) RMS (E[e^2z] = e^2), 0.2 nats less where the sink's e4m3 row is
+    rounded up. The values are independent of both, so the output's relative RMS error is the weights'.
+    Beside it, in quadrature, the path's own bound."""
+    c = Case([n], [8192], 2, 1, d, True, seed=70)
+    g = torch.Generator().manual_seed(4)
+    u = torch.randn(d, generator=g)
+    u = u / u.norm()
+    for q in c.q:
+        q.copy_((4 * d ** 0.5 * u + 0.02 * torch.randn(q.shape, generator=g)).to(BF))
+    for p, s in zip(c.pools[:2], c.scales):
+        p.copy_((torch.randn(p.shape, generator=g) * 0.25 / s).clamp(-448, 448).to(F8))
+        p[int(c.table[0, at // 64]), :, at % 64] = (nats / 4 * u / s).clamp(-448, 448).to(F8)
+    c.pools[2].view(torch.uint8)[int(c.table[0, at // 64]), :, at % 64] = 0
+    _, rms = errors(c.run(), c.want().numpy())
+    tol = math.hypot(3e-3, 2.0 ** -32 / math.sqrt(3) / math.exp(1 - nats - 0.2))
+    print(f"d{d} n{n} {nats:.1f} nats: {rms:.2e} of {tol:.2e}")
+    assert rms <= tol, f"rel-RMS {rms:.3e} against {tol:.3e}"
