@@ -490,7 +490,6 @@ def rope_plan(rotary_dim: int, base: float = 10000.0, interleaved: bool = False,
 # plain loops, one attribute access each, and the raw stream handle.
 _raw_stream = torch._C._cuda_getCurrentRawStream
 _current_device = torch._C._cuda_getDevice
-_thread_id = threading.get_ident
 _INT32 = torch.int32
 
 
@@ -515,14 +514,39 @@ def _int32(t, dev, shape, what):
         raise ValueError(f"{what} must be a contiguous int32 tensor of shape {list(shape)} on the operands' device")
 
 
-_serving_ws: dict = {}
+class _Kept(threading.local):
+    """A thread's workspaces by (device, stream), oldest first: they go with the thread."""
+
+    def __init__(self):
+        self.buffers = {}
+
+
+_kept = _Kept()
+_KEPT_STREAMS = 4  # per thread: at full tiles a workspace has up to 120 MB
+
+
+def kept_workspace(device=None, stream=None):
+    """The workspace that diffattn_chunk_paged, module_serve and layer_serve keep for this thread and the
+    stream (default: the current one) when they are given none, or None: read_error(kept_workspace())
+    tells whether a wait of their kernels ran out. A thread keeps four, those of the streams that it took up
+    last. Calls captured into a graph have workspaces of the graph's own; give them `ws` to read its error
+    word."""
+    dev = torch.device("cuda", torch.cuda.current_device()) if device is None else torch.device(device)
+    index = torch.cuda.current_device() if dev.index is None else dev.index
+    return _kept.buffers.get((index, _raw_stream(index) if stream is None else stream.cuda_stream))
+
+
+def release_workspaces() -> None:
+    """Drops this thread's kept workspaces; calls in flight may still use them (their memory is reused in
+    the order of their streams)."""
+    _kept.buffers.clear()
 
 
 def _kept_workspace(dev):
     """The kept workspace of this thread and the current stream, if there is one and it may be used."""
     if torch.cuda.is_current_stream_capturing():
         return None
-    return _serving_ws.get((dev.index, _raw_stream(dev.index), _thread_id()))
+    return _kept.buffers.get((dev.index, _raw_stream(dev.index)))
 
 
 def _serving_workspace(nbytes: int, dev) -> torch.Tensor:
@@ -530,14 +554,16 @@ def _serving_workspace(nbytes: int, dev) -> torch.Tensor:
     threads, whose launches may interleave on one stream. During a graph capture a new one from the graph's
     own memory, so that two graphs share none either."""
     capturing = torch.cuda.is_current_stream_capturing()
-    key = (dev.index, _raw_stream(dev.index), _thread_id())
-    buf = None if capturing else _serving_ws.get(key)
+    key = (dev.index, _raw_stream(dev.index))
+    buf = None if capturing else _kept.buffers.get(key)
     if buf is None or buf.numel() < nbytes:
         buf = torch.empty(nbytes + 256, dtype=torch.uint8, device=dev)
         buf = buf[(-buf.data_ptr()) % 256:]
         buf[:256].zero_()  # the control block: the rest needs no initialisation
         if not capturing:
-            _serving_ws[key] = buf
+            if key not in _kept.buffers and len(_kept.buffers) >= _KEPT_STREAMS:
+                del _kept.buffers[next(iter(_kept.buffers))]
+            _kept.buffers[key] = buf
     return buf
 
 
@@ -667,8 +693,8 @@ def diffattn_chunk_paged(q1, q2, k1_pages, k2_pages, v_pages, block_table, q_sta
     them. q1, q2: [T, H, d] bf16 rows, sequence b's q_start[b] .. q_start[b + 1] - 1, the last of its
     seq_lens[b] tokens; each sees its sequence up to itself. Pages, block_table, kv_group and scales as for
     diffattn_decode_paged; L = the largest length. Returns [T, H, Dv]; rows of no sequence are left as
-    they are. Calls on different streams and threads use workspaces of their own unless `ws` is given (whose
-    error word read_error then reads)."""
+    they are. Calls on different streams and threads use workspaces of their own unless `ws` is given;
+    read_error(kept_workspace()) or read_error(ws) reads the error word."""
     dev = q1.device
     ctx = _elsewhere(dev, stream)
     if ctx is not None:

@@ -2,6 +2,7 @@
 scales at the ends of what the call takes, small weights behind a large one, and each of its three
 kernels (few rows, 128-row tiles, the CTA pair's) with the options that the bf16 tests cover."""
 
+import ctypes
 import math
 
 import pytest
@@ -10,7 +11,7 @@ import torch
 import differential_attention_02_gb300 as da
 import serving_reference as ref
 from parity import errors
-from test_gpu_chunk import Case
+from test_gpu_chunk import LAM, LI, Case
 
 pytestmark = pytest.mark.gpu
 F8, BF = torch.float8_e4m3fn, torch.bfloat16
@@ -86,3 +87,23 @@ def test_tail_behind_a_sink(d, n, nats, at):
     tol = math.hypot(3e-3, 2.0 ** -32 / math.sqrt(3) / math.exp(1 - nats - 0.2))
     print(f"d{d} n{n} {nats:.1f} nats: {rms:.2e} of {tol:.2e}")
     assert rms <= tol, f"rel-RMS {rms:.3e} against {tol:.3e}"
+
+
+def test_error_word_of_a_kept_workspace():
+    """A wait that runs out (the library's own test of it: a barrier that nothing completes, 1 s) in the
+    workspace that a call without `ws` kept; the next call is right and leaves no error."""
+    da.release_workspaces()
+    c = _case("both", seed=6)
+    dev = [x.cuda() for x in c.q] + [p.cuda() for p in c.pools]
+    rest = (c.table.cuda(), _i32(c.starts), _i32(c.lens), LAM, LI)
+
+    def call():
+        return da.diffattn_chunk_paged(*dev, *rest, L=c.L, kv_group=2, scales=c.scales)
+    assert da.kept_workspace() is None
+    want = call()
+    ws = da.kept_workspace()
+    assert da.read_error(ws) == 0
+    stream = torch.cuda.current_stream().cuda_stream
+    assert da.load_library().diffattn_selftest_timeout(ctypes.c_void_p(ws.data_ptr()), ws.numel(), ctypes.c_void_p(stream)) == da.OK
+    assert da.read_error(da.kept_workspace()) == (0x7F << 8) | 1
+    assert torch.equal(call(), want) and da.kept_workspace() is ws and da.read_error(ws) == 0
