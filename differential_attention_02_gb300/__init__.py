@@ -629,6 +629,8 @@ def _paged_args(dev, k1, k2, v, H_kv, d, block_table, q_start, seq_lens, scales)
     """The pages as diffattn_tensors, the table's sizes, whether the cache is fp8, and the sequences."""
     dt, shape = k1.dtype, k1.shape
     fp8 = scales is not None
+    if fp8 and len(scales) != 3:
+        raise ValueError("scales must be (k1_scale, k2_scale, v_scale)")
     if fp8 != (dt == torch.float8_e4m3fn or dt == torch.uint8) or _is_fp8(k2) != fp8 or _is_fp8(v) != fp8:
         raise ValueError("fp8 pages (all three) go with scales, bf16 pages without")
     if not fp8 and not (dt == k2.dtype == v.dtype == torch.bfloat16):
@@ -673,7 +675,7 @@ def diffattn_kv_append_chunk_paged(k1_new, k2_new, v_new, k1_pages, k2_pages, v_
     args = (_t3(k1_new, T, Hk, d), _t3(k2_new, T, Hk, d), _t3(v_new, T, Hk, Dv), _dtype_code(dtype), *paged,
             None if rope is None else rope._c, T, B, Hk, d, Dv)
     if fp8:
-        _check(lib.diffattn_kv_append_chunk_paged_fp8(*args, *scales, _raw_stream(dev.index)),
+        _check(lib.diffattn_kv_append_chunk_paged_fp8(*args, *map(float, scales), _raw_stream(dev.index)),
                "diffattn_kv_append_chunk_paged_fp8")
     else:
         _check(lib.diffattn_kv_append_chunk_paged(*args, _raw_stream(dev.index)), "diffattn_kv_append_chunk_paged")
@@ -681,7 +683,7 @@ def diffattn_kv_append_chunk_paged(k1_new, k2_new, v_new, k1_pages, k2_pages, v_
 
 def chunk_workspace_bytes(T, B, H, kv_group, L, d, Dv) -> int:
     n = ctypes.c_size_t()
-    _check((_lib or load_library()).diffattn_chunk_workspace_size(T, B, H, kv_group, L, d, Dv, ctypes.byref(n)),
+    _check((_lib or load_library()).diffattn_chunk_workspace_size(T, B, H, int(kv_group), int(L), d, Dv, ctypes.byref(n)),
            "diffattn_chunk_workspace_size")
     return n.value
 
@@ -703,6 +705,7 @@ def diffattn_chunk_paged(q1, q2, k1_pages, k2_pages, v_pages, block_table, q_sta
                                         kv_group, eps, norm_weight, out_dtype, out, ws, None, scales)
     T, H, d = q1.shape
     Dv = v_pages.shape[-1]
+    L, kv_group = int(L), int(kv_group)
     if q1.dtype != torch.bfloat16 or q2.dtype != torch.bfloat16 or q2.device != dev:
         raise ValueError("q1 and q2 must be [T, H, d] bf16 tensors on one device")
     if kv_group < 1 or H % kv_group:
@@ -719,11 +722,12 @@ def diffattn_chunk_paged(q1, q2, k1_pages, k2_pages, v_pages, block_table, q_sta
     elif out.shape != (T, H, Dv) or not out.is_contiguous() or out.device != dev:
         raise ValueError("out must be a contiguous [T, H, Dv] tensor on the operands' device")
     lib = _lib or load_library()
-    args = (_t3(q1, T, H, d), _t3(q2, T, H, d), *paged, L, out.data_ptr(), w, T, B, H, kv_group, d, Dv, lam, lam_init, eps)
+    args = (_t3(q1, T, H, d), _t3(q2, T, H, d), *paged, L, out.data_ptr(), w, T, B, H, kv_group, d, Dv, float(lam),
+            float(lam_init), float(eps))
     name, call = (("diffattn_chunk_paged_fp8", lib.diffattn_chunk_paged_fp8) if fp8 else
                   ("diffattn_chunk_paged", lib.diffattn_chunk_paged))
     if fp8:
-        args += tuple(scales)
+        args += tuple(map(float, scales))
     code, kept = _dtype_code(out.dtype), ws
     if ws is None:  # the kept workspace, unless the call says that it is too small
         kept = _kept_workspace(dev)
@@ -1006,7 +1010,8 @@ def _serve_attention(x, w_qkv, n_heads, pages, block_table, q_start, seq_lens, l
                      positions, scales, eps, norm_weight, att_dtype, ws):
     """The projection, rotation, append and attention of module_serve on the current stream: concat(heads)
     [T, h*Dv] of att_dtype, and the workspace."""
-    T, h, dev = x.shape[0], n_heads, x.device
+    T, h, dev = x.shape[0], int(n_heads), x.device
+    L, kv_group = int(L), int(kv_group)
     if x.dim() != 2 or kv_group < 1 or h % kv_group:
         raise ValueError("x must be [T, d_model], and kv_group must divide the heads")
     hk, d, Dv = h // kv_group, pages[0].shape[-1], pages[2].shape[-1]

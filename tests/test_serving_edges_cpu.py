@@ -5,6 +5,7 @@ import gc
 import threading
 import weakref
 
+import numpy as np
 import pytest
 import torch
 
@@ -74,3 +75,46 @@ def test_kept_workspace_is_reachable(host):
     assert da.kept_workspace(stream=type("Stream", (), {"cuda_stream": 7})()) is a
     da.release_workspaces()
     assert da.kept_workspace(stream=type("Stream", (), {"cuda_stream": 7})()) is None
+
+
+class Recorder:
+    """Stands in for the library: every call returns OK and leaves its arguments, as ctypes converts them."""
+
+    def __init__(self, real):
+        self.calls = {}
+        for name in ("diffattn_chunk_paged", "diffattn_chunk_paged_fp8", "diffattn_kv_append_chunk_paged",
+                     "diffattn_kv_append_chunk_paged_fp8"):
+            types = getattr(real, name).argtypes
+
+            def call(*args, name=name, types=types):
+                assert len(args) == len(types)
+                for a, t in zip(args, types):
+                    t.from_param(a)  # raises what the call would
+                self.calls[name] = args
+                return da.OK
+            setattr(self, name, call)
+
+
+@pytest.mark.parametrize("kind", [np.float32, np.float64, lambda x: torch.tensor(x, dtype=torch.float64), float])
+def test_scalars_of_every_kind(host, monkeypatch, kind):
+    """lam, lam_init, eps and the scales as Python, NumPy or 0-dim torch numbers, L and kv_group as NumPy or torch
+    integers, as the one-token calls take them."""
+    lib = Recorder(da.load_library())
+    monkeypatch.setattr(da, "_lib", lib)
+    monkeypatch.setattr(da, "_elsewhere", lambda dev, stream: None)
+    f8, i32 = torch.float8_e4m3fn, torch.int32
+    host.dev = torch.device("cpu")
+    q = torch.zeros(3, 4, 64, dtype=torch.bfloat16)
+    k, v = torch.zeros(2, 2, 64, 64, dtype=torch.uint8).view(f8), torch.zeros(2, 2, 64, 128, dtype=torch.uint8).view(f8)
+    rest = (torch.zeros(1, 2, dtype=i32), torch.zeros(2, dtype=i32), torch.zeros(1, dtype=i32))
+    scales = tuple(kind(s) for s in (0.5, 0.25, 2.0))
+    da.diffattn_kv_append_chunk_paged(q[:, :2], q[:, :2], torch.zeros(3, 2, 128, dtype=torch.bfloat16), k, k, v, *rest, scales=scales)
+    assert lib.calls["diffattn_kv_append_chunk_paged_fp8"][-4:-1] == (0.5, 0.25, 2.0)
+    ints = (int, np.int64, lambda x: torch.tensor(x))
+    for to_int in ints:
+        da.diffattn_chunk_paged(q, q, k, k, v, *rest, kind(0.75), kind(0.5), to_int(100), to_int(2), kind(0.125), scales=scales,
+                                ws=torch.zeros(64, dtype=torch.uint8))
+        args = lib.calls["diffattn_chunk_paged_fp8"]
+        assert args[16:22] == (2, 64, 128, 0.75, 0.5, 0.125) and args[22:25] == (0.5, 0.25, 2.0) and args[10] == 100
+    with pytest.raises(ValueError, match="scales"):
+        da.diffattn_chunk_paged(q, q, k, k, v, *rest, 0.5, 0.5, 100, 2, scales=scales[:2])
