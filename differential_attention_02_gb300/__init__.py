@@ -514,6 +514,16 @@ def _int32(t, dev, shape, what):
         raise ValueError(f"{what} must be a contiguous int32 tensor of shape {list(shape)} on the operands' device")
 
 
+def _gain(t, dev, n, what):
+    if t is not None and (t.dtype != torch.float32 or t.shape != (n,) or t.device != dev or not t.is_contiguous()):
+        raise ValueError(f"{what} must be a contiguous fp32 tensor of shape [{n}] on the operands' device")
+
+
+def _workspace_arg(ws, dev):
+    if ws.device != dev or not ws.is_contiguous():
+        raise ValueError("ws must be a contiguous buffer on the operands' device")
+
+
 class _Kept(threading.local):
     """A thread's workspaces by (device, stream), oldest first: they go with the thread."""
 
@@ -713,10 +723,10 @@ def diffattn_chunk_paged(q1, q2, k1_pages, k2_pages, v_pages, block_table, q_sta
     paged, fp8, B = _paged_args(dev, k1_pages, k2_pages, v_pages, H // kv_group, d, block_table, q_start, seq_lens, scales)
     w = None
     if norm_weight is not None:
-        if (norm_weight.dtype != torch.float32 or norm_weight.shape != (Dv,) or not norm_weight.is_contiguous()
-                or norm_weight.device != dev):
-            raise ValueError("norm_weight must be a contiguous fp32 [Dv] tensor on the operands' device")
+        _gain(norm_weight, dev, Dv, "norm_weight")
         w = norm_weight.data_ptr()
+    if ws is not None:
+        _workspace_arg(ws, dev)
     if out is None:
         out = torch.empty((T, H, Dv), dtype=out_dtype, device=dev)
     elif out.shape != (T, H, Dv) or not out.is_contiguous() or out.device != dev:
@@ -978,6 +988,7 @@ def module_serve(x, w_qkv, w_o, n_heads: int, pages, block_table, q_start, seq_l
         with ctx:
             return module_serve(x, w_qkv, w_o, n_heads, pages, block_table, q_start, seq_lens, lam, lam_init, L, kv_group,
                                 rope, positions, scales, eps, norm_weight, out_dtype, ws)
+    _on_device(x.device, w_o)
     att, ws = _serve_attention(x, w_qkv, n_heads, pages, block_table, q_start, seq_lens, lam, lam_init, L, kv_group, rope,
                                positions, scales, eps, norm_weight, x.dtype, ws)
     if att.shape[0] == 0:
@@ -998,6 +1009,9 @@ def layer_serve(x, w_qkv, w_o, w_gu, w_down, n_heads: int, pages, block_table, q
                                L, kv_group, rope, positions, scales, eps, norm1_weight, norm2_weight, head_weight, ws)
     if x.dim() != 2 or x.dtype not in (torch.bfloat16, torch.float32) or not x.is_contiguous():
         raise ValueError("x must be a contiguous [T, d_model] bf16 or fp32 tensor")
+    _on_device(x.device, w_qkv, w_o, w_gu, w_down)
+    _gain(norm1_weight, x.device, x.shape[1], "norm1_weight")
+    _gain(norm2_weight, x.device, x.shape[1], "norm2_weight")
     _, n1 = add_rmsnorm(x, weight=norm1_weight, eps=eps, n_dtype=w_qkv.dtype)
     att, ws = _serve_attention(n1, w_qkv, n_heads, pages, block_table, q_start, seq_lens, lam, lam_init, L, kv_group, rope,
                                positions, scales, eps, head_weight, w_qkv.dtype, ws)
@@ -1025,8 +1039,10 @@ def _serve_attention(x, w_qkv, n_heads, pages, block_table, q_start, seq_lens, l
     need = max(256, chunk_workspace_bytes(T, seq_lens.shape[0], h, kv_group, L, d, Dv))
     if ws is None:
         ws = _serving_workspace(need, dev)
-    elif ws.numel() < need:
-        raise ValueError(f"ws must have {need} bytes (chunk_workspace_bytes)")
+    else:
+        _workspace_arg(ws, dev)
+        if ws.numel() < need:
+            raise ValueError(f"ws must have {need} bytes (chunk_workspace_bytes)")
     # rows of no sequence are written by no kernel, and W_O reads them
     att = torch.zeros((T, h, Dv), dtype=att_dtype, device=dev)
     if T:

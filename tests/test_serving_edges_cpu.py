@@ -118,3 +118,57 @@ def test_scalars_of_every_kind(host, monkeypatch, kind):
         assert args[16:22] == (2, 64, 128, 0.75, 0.5, 0.125) and args[22:25] == (0.5, 0.25, 2.0) and args[10] == 100
     with pytest.raises(ValueError, match="scales"):
         da.diffattn_chunk_paged(q, q, k, k, v, *rest, 0.5, 0.5, 100, 2, scales=scales[:2])
+
+
+def _chunk_args(dev="cpu"):
+    q = torch.zeros(3, 4, 64, dtype=torch.bfloat16)
+    k, v = (torch.zeros(2, 2, 64, n, dtype=torch.bfloat16) for n in (64, 128))
+    i32 = lambda *s: torch.zeros(*s, dtype=torch.int32)  # noqa: E731
+    return q, q, k, k, v, i32(1, 2), i32(2), i32(1), 0.5, 0.5, 100, 2
+
+
+ELSEWHERE = torch.device("meta")  # another device than the operands', without memory
+
+
+def test_workspaces_of_another_device_are_refused(host, monkeypatch):
+    """A kernel would write to whatever address they have."""
+    lib = Recorder(da.load_library())
+    monkeypatch.setattr(da, "_lib", lib)
+    monkeypatch.setattr(da, "_elsewhere", lambda dev, stream: None)
+    da.diffattn_chunk_paged(*_chunk_args(), ws=torch.zeros(1 << 20, dtype=torch.uint8))
+    lib.calls.clear()
+    for ws in (torch.empty(1 << 20, dtype=torch.uint8, device=ELSEWHERE), torch.zeros(1, dtype=torch.uint8).expand(1 << 20),
+               torch.zeros(1 << 20, dtype=torch.uint8)[::2]):
+        with pytest.raises(ValueError, match="ws"):
+            da.diffattn_chunk_paged(*_chunk_args(), ws=ws)
+    assert not lib.calls
+
+
+def test_served_models_refuse_operands_of_another_device(monkeypatch):
+    """Workspace, weights and gains, before any launch: the projections take no look at their devices."""
+    monkeypatch.setattr(da, "_elsewhere", lambda dev, stream: None)
+    launched = []
+    for name in ("gemm", "gemm_residual", "gemm_swiglu", "add_rmsnorm", "diffattn_rope", "diffattn_kv_append_chunk_paged",
+                 "diffattn_chunk_paged"):
+        monkeypatch.setattr(da, name, lambda *a, name=name, **k: launched.append(name))
+    bf = torch.bfloat16
+    x, w_qkv, w_o = torch.zeros(3, 256, dtype=bf), torch.zeros(256, 512, dtype=bf), torch.zeros(128, 256, dtype=bf)
+    w_gu, w_down, ws = torch.zeros(256, 256, dtype=bf), torch.zeros(128, 256, dtype=bf), torch.zeros(1 << 20, dtype=torch.uint8)
+    i32 = lambda *s: torch.zeros(*s, dtype=torch.int32)  # noqa: E731
+    rest = (1, [torch.zeros(2, 1, 64, n, dtype=bf) for n in (64, 64, 128)], i32(1, 2), i32(2), i32(1), 0.5, 0.5, 100)
+    away = lambda t: torch.empty(t.shape, dtype=t.dtype, device=ELSEWHERE)  # noqa: E731
+    gain, one = torch.ones(256), torch.ones(1)
+    bad = [lambda: da.module_serve(x, away(w_qkv), w_o, *rest, ws=ws), lambda: da.module_serve(x, w_qkv, away(w_o), *rest, ws=ws),
+           lambda: da.module_serve(x, w_qkv, w_o, *rest, ws=away(ws)),
+           lambda: da.module_serve(x, w_qkv, w_o, *rest, ws=torch.zeros(1, dtype=torch.uint8).expand(1 << 20))]
+    for i, w in enumerate((w_qkv, w_o, w_gu, w_down)):
+        four = [w_qkv, w_o, w_gu, w_down]
+        four[i] = away(w)
+        bad.append(lambda four=four: da.layer_serve(x, *four, *rest, ws=ws))
+    for g in (away(gain), one, gain.to(bf), torch.ones(512)[::2]):
+        bad.append(lambda g=g: da.layer_serve(x, w_qkv, w_o, w_gu, w_down, *rest, ws=ws, norm1_weight=g))
+        bad.append(lambda g=g: da.layer_serve(x, w_qkv, w_o, w_gu, w_down, *rest, ws=ws, norm2_weight=g))
+    for call in bad:
+        with pytest.raises(ValueError):
+            call()
+    assert not launched
