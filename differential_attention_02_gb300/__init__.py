@@ -500,6 +500,8 @@ def _elsewhere(dev, stream):
         return None
     if dev.type != "cuda":
         raise ValueError("all tensors must be on one CUDA device")
+    if stream is not None and stream.device != dev:
+        raise ValueError("stream must be one of the operands' device")
     return torch.cuda.stream(stream if stream is not None else torch.cuda.current_stream(dev))
 
 

@@ -172,3 +172,18 @@ def test_served_models_refuse_operands_of_another_device(monkeypatch):
         with pytest.raises(ValueError):
             call()
     assert not launched
+
+
+def test_streams_of_another_device_are_refused(monkeypatch):
+    """The call would run on the operands' device's current stream, in no order with the one asked for."""
+    entered = []
+    monkeypatch.setattr(torch.cuda, "stream", lambda s: entered.append(s))
+    monkeypatch.setattr(da, "_current_device", lambda: 0)
+    stream = lambda i: type("Stream", (), {"device": torch.device("cuda", i)})()  # noqa: E731
+    for at in (1, 3):
+        with pytest.raises(ValueError, match="stream"):
+            da._elsewhere(torch.device("cuda", 0), stream(at))
+    assert not entered
+    same = stream(0)
+    da._elsewhere(torch.device("cuda", 0), same)
+    assert entered == [same] and da._elsewhere(torch.device("cuda", 0), None) is None
