@@ -446,6 +446,8 @@ class RopePlan:
     frequency table on one device, kept for as long as the plan is."""
 
     def __init__(self, freqs: torch.Tensor, rotary_dim: int, interleaved: bool, magnitude: float):
+        if freqs.dtype != torch.int64 or freqs.shape != (rotary_dim // 2,) or not freqs.is_contiguous():
+            raise ValueError("freqs must be a contiguous int64 tensor of rotary_dim / 2 values")
         self.freqs, self.rotary_dim, self.interleaved, self.magnitude = freqs, rotary_dim, interleaved, magnitude
         self._c = Rotation(freqs.data_ptr(), rotary_dim, int(interleaved), magnitude)
 
@@ -586,6 +588,8 @@ def diffattn_rope(tensors, rope: RopePlan, positions=None, backward: bool = Fals
     rotated operands to gradients of the operands. positions: int32 [B, N] or None (row n at position n).
     out: tensors to write (the operands themselves rotate in place), else new ones of out_dtype (default:
     the operands') in the operands' memory order. Returns them as a tuple."""
+    if not 1 <= len(tensors) <= 4:
+        raise ValueError("one to four operands [B, H, N, d]")
     x = tensors[0]
     dev, dtype = x.device, x.dtype
     ctx = _elsewhere(dev, stream)
@@ -593,7 +597,7 @@ def diffattn_rope(tensors, rope: RopePlan, positions=None, backward: bool = Fals
         with ctx:
             return diffattn_rope(tensors, rope, positions, backward, out, out_dtype)
     n = len(tensors)
-    if n > 4 or x.dim() != 4:
+    if x.dim() != 4:
         raise ValueError("one to four operands [B, H, N, d]")
     B, _, N, d = x.shape
     if rope.freqs.device != dev:

@@ -187,3 +187,15 @@ def test_streams_of_another_device_are_refused(monkeypatch):
     same = stream(0)
     da._elsewhere(torch.device("cuda", 0), same)
     assert entered == [same] and da._elsewhere(torch.device("cuda", 0), None) is None
+
+
+def test_rope_plans_have_their_whole_table():
+    """A kernel reads rotary_dim / 2 values behind the table's address."""
+    table, magnitude = da.rope_freqs(64)
+    da.RopePlan(table, 64, False, magnitude)
+    for bad in (table[:31], table[:16], table.to(torch.int32), table.double(), torch.zeros(64, dtype=torch.int64)[::2],
+                table.view(2, 16), torch.zeros(1, dtype=torch.int64).expand(32)):
+        with pytest.raises(ValueError, match="freqs"):
+            da.RopePlan(bad, 64, False, magnitude)
+    with pytest.raises(ValueError, match="operands"):
+        da.diffattn_rope([], da.RopePlan(table, 64, False, magnitude))
