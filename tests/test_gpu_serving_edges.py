@@ -89,6 +89,113 @@ def test_tail_behind_a_sink(d, n, nats, at):
     assert rms <= tol, f"rel-RMS {rms:.3e} against {tol:.3e}"
 
 
+@kinds
+@pytest.mark.parametrize("out_dtype", [torch.float32, BF, torch.float16])
+def test_output_types_gain_and_layouts(kind, out_dtype):
+    """16-bit outputs, the RMSNorm gain, queries as views of a projection and with heads outermost, pages whose
+    rows do not follow one another."""
+    c = _case(kind, seed=4)
+    d = c.d
+    gain = torch.linspace(0.5, 1.5, 2 * d)
+    got = c.run(out_dtype=out_dtype, norm_weight=gain.cuda())
+    want = c.want(norm_weight=gain)
+    c.check((got.float() / gain.cuda()).to(out_dtype), f"{kind} gain", want / gain.double())
+    proj = torch.cat(c.q, -1).cuda()
+    heads = [x.transpose(0, 1).contiguous().transpose(0, 1).cuda() for x in c.q]
+    padded = []
+    for p in c.pools:
+        big = torch.full((p.shape[0], p.shape[1], 66, p.shape[3] + 16), 0x7F, dtype=torch.uint8, device="cuda")  # NaN
+        big[:, :, :64, :p.shape[3]] = p.cuda().view(torch.uint8)
+        padded.append(big.view(F8)[:, :, :64, :p.shape[3]])
+    plain = c.run(out_dtype=out_dtype)
+    for q in ((proj[..., :d], proj[..., d:]), heads):
+        alt = da.diffattn_chunk_paged(*q, *padded, c.table.cuda(), _i32(c.starts), _i32(c.lens), LAM, LI, L=c.L, kv_group=2,
+                                      out_dtype=out_dtype, scales=c.scales)
+        assert torch.equal(alt, plain)
+
+
+@pytest.mark.parametrize("kind,n", [("few", [5, 4, 3, 4]), ("both", [5, 4, 3, 20]), ("many", [5, 40, 3, 140]),
+                                    ("wide", [5, 4, 3, 140])])
+def test_rows_without_keys_and_clamped_lengths(kind, n):
+    """Lengths below the chunk (rows before position 0 see nothing), zero and negative ones, and lengths
+    past L, which are clamped to it; the kernels' accumulators hold another call's values before."""
+    d = KINDS[kind][0]
+    full = [n[0], n[1], n[2], 300]
+    c = Case(n, full, 2, 1, d, True, seed=5)
+    c.run()  # leaves tensor memory and the workspace full
+    lens = [3, 0, -7, 300]
+    got = c.run(lens=lens)
+    assert bool((got[:n[0] - 3] == 0).all()) and bool((got[n[0]:n[0] + n[1] + n[2]] == 0).all())
+    c.check(got, f"{kind} short lengths", c.want(lens=[3, 0, 0, 300]))
+    c.check(c.run(lens=[*full[:3], 10_000], L=300), f"{kind} clamped")
+
+
+@pytest.mark.parametrize("d,group,n", [(64, g, [1, 50, 9]) for g in (3, 5, 7, 16, 100)] +
+                         [(128, g, [1, 50, 9]) for g in (3, 6, 100)] + [(64, g, [1, 1, 1, 0]) for g in (3, 5, 7, 16)])
+def test_group_sizes(d, group, n):
+    """Groups that divide a tile's rows and groups that leave some unused; n of at most a token: few rows."""
+    c = Case(n, [77, 50, 300, 64][:len(n)], group * (2 if group < 20 else 1), group, d, True, seed=group)
+    c.check(c.run(), f"group {group}")
+
+
+@kinds
+def test_deterministic(kind):
+    d, n, _ = KINDS[kind]
+    c = Case(n, [6000, 5000, 2300, 900][:len(n)], 4, 2, d, True, seed=8)
+    a = c.run()
+    c.check(a, kind)
+    for _ in range(3):
+        assert torch.equal(c.run(), a)
+
+
+def test_captured_call_whose_tiles_change_lists():
+    """A call of two lists, captured, replayed with starts and lengths that move tiles from one to the other and
+    leave either empty."""
+    c = Case([1, 9, 2, 1], [900, 3000, 700, 130], 4, 2, 64, True, seed=9)
+    dev = dict(q=[x.cuda() for x in c.q], pools=[p.cuda() for p in c.pools], table=c.table.cuda(), start=_i32(c.starts),
+               lens=_i32(c.lens), out=torch.empty(c.T, 4, 128, device="cuda"))
+
+    def call():
+        da.diffattn_chunk_paged(*dev["q"], *dev["pools"], dev["table"], dev["start"], dev["lens"], LAM, LI, L=c.L, kv_group=2,
+                                out=dev["out"], scales=c.scales)
+    call()
+    torch.cuda.synchronize()
+    graph = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(graph):
+        call()
+    for starts, lens in ((c.starts, c.lens), ([0, 9, 10, 12, 13], [900, 400, 700, 130]), ([0, 4, 7, 10, 13], [900, 3000, 700, 130]),
+                         ([0, 13, 13, 13, 13], [850, 3000, 700, 130]), ([0, 0, 1, 3, 3], [900, 3000, 700, 130])):
+        dev["start"].copy_(_i32(starts))
+        dev["lens"].copy_(_i32(lens))
+        dev["out"].fill_(7.0)
+        graph.replay()
+        torch.cuda.synchronize()
+        want = ref.chunk_attention(*c.q, c.pools, c.table, starts, lens, LAM, LI, group=2, scales=c.scales)
+        c.starts = starts
+        c.check(dev["out"], f"{starts}", want)
+        assert bool((dev["out"][starts[-1]:] == 7.0).all())
+
+
+@pytest.mark.parametrize("scale", [0.0113, 1.0, 2.0 ** -61, 2.0 ** 61])
+def test_append_fp8_stores_nan_as_the_single_token_append(scale):
+    """NaN of both signs and any payload among ordinary values and infinities: e4m3's NaN, the code of the
+    single-token append, with the quotient by the inverse (the first two scales) and by division."""
+    bits = torch.cat([torch.arange(0x7F81, 0x8000), torch.arange(0xFF81, 0x10000), torch.tensor([0x7F80, 0xFF80])])
+    nan = bits.to(torch.int32).to(torch.int16).view(BF)
+    x = torch.randn(2, 1, 256, generator=torch.Generator().manual_seed(1)).to(BF)
+    x.view(-1)[::2] = nan[:256]
+    rows = [t.cuda() for t in (x[..., :64], x[..., 64:128], x[..., 128:])]
+    make = lambda: [torch.zeros(1, 1, 64, w, dtype=torch.uint8, device="cuda") for w in (64, 64, 128)]  # noqa: E731
+    a, b = make(), make()
+    table = _i32([[0]])
+    da.diffattn_kv_append_chunk_paged(*rows, *a, table, _i32([0, 2]), _i32([2]), scales=(scale,) * 3)
+    for t in range(2):
+        da.diffattn_kv_append_paged(*(r[t:t + 1].contiguous() for r in rows), *b, table, _i32([t + 1]), scales=(scale,) * 3)
+    for p, q, r in zip(a, b, rows):
+        assert torch.equal(p, q)
+        assert torch.equal((p[0, 0, :2] & 0x7F) == 0x7F, r[:, 0].isnan())
+
+
 def test_error_word_of_a_kept_workspace():
     """A wait that runs out (the library's own test of it: a barrier that nothing completes, 1 s) in the
     workspace that a call without `ws` kept; the next call is right and leaves no error."""
