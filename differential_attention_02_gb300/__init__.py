@@ -983,8 +983,8 @@ def module_serve(x, w_qkv, w_o, n_heads: int, pages, block_table, q_start, seq_l
     module_fwd, h_kv = n_heads / kv_group; w_o [h*Dv, d_model]; x and the weights all bf16 or all fp16.
     pages = (k1_pages, k2_pages, v_pages), block_table, scales (fp8 pages) and L as in diffattn_chunk_paged. Q, K
     and V are bf16, the type that the paged attention reads. With rope, Q rotates at `positions` (int32 [T], the
-    token's place in its sequence: seq_lens[b] - q_start[b + 1] + row) and K as it is appended, at the
-    same place by construction. Rows of no sequence: their attention is zero.
+    token's place in its sequence: seq_lens[b] - q_start[b + 1] + row) and K as it is appended, at that
+    place by construction: nothing compares `positions` with it. Rows of no sequence: their attention is zero.
 
     Four launches of its own beside the two GEMMs: rotation of Q, append, plan and attention (a fifth joins
     sequences that were split). Calls on different streams and threads share no workspace unless `ws` is

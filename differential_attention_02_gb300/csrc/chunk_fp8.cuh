@@ -8,8 +8,9 @@
 // The conversion is the instruction cvt.rn.f16x2.e4m3x2 on the halves of a word. Through the
 // intrinsic, whose result comes in two halves that have to be joined again, it was slower than four
 // integer instructions a pair; written out it is faster: 2 x 1024 tokens at the end of 8192, 16 query and
-// 8 KV heads 262 -> 246 us, d = 128 (2 x 1024 of 4096, 8 heads) 184 -> 166 us, 16 x 5 drafted tokens over
-// 8192 keys 104 -> 84 us.
+// 8 KV heads 262 -> 211 us, d = 128 (2 x 1024 of 4096, 8 heads) 184 -> 152 us, 16 x 5 drafted tokens over
+// 8192 keys 104 -> 84 us (69 with the later steps of chunk_few_tcgen05.cu). Over a bf16 cache the two
+// prompts take 183 and 107 us: the rest is this conversion, done again by every query tile.
 //
 // What else the path cost on the way, on those drafted tokens in 128-row tiles: K to bf16 beside a
 // bf16 query 217 us, K to fp16 197, eight chunks of a thread loaded before the first is stored 164,
@@ -34,7 +35,7 @@ constexpr float kWeightShift = 7.f;  // log2 units
 // place in its swizzled boxes, by the thread that owns the row; returns 2^-shift. The row's
 // largest exponent goes to 2^15, so nothing overflows, and what falls below fp16's normal
 // range is smaller than the row's maximum by 2^-29 and more: less than the fp32 sums of the
-// scores keep. (Rows below 2^-111 keep a factor of 2^126, the last whose inverse is a normal
+// scores keep, unless K is zero in the row's largest channels. (Rows below 2^-111 keep a factor of 2^126, the last whose inverse is a normal
 // number; their values still come to 2^-7 and more, well inside fp16's normal range.)
 template <int D>
 __device__ __forceinline__ float q_row_to_f16(uint8_t* boxes, int r) {

@@ -18,7 +18,12 @@
 // batch of 428 items took 106 us cut and 102 whole, and cutting the whole row of items
 // at every multiple of W / C, which balances any batch within an entry, was no faster either
 // (four prompts' chunks 592 against 586 us, the mixed batch 110 against 104), since
-// every cut costs a partial state of 128 KB and its merge.
+// every cut costs a partial state of 128 KB and its merge. The rule looks at the number of
+// items alone and those batches were of like lengths: one sequence much longer than the others in a
+// batch of that size stays whole, one CTA per head, and sets the time.
+//
+// The costs per entry, state and merge step were fitted to the single-CTA kernels and are used for
+// the CTA pairs as well.
 #include <math.h>
 
 #include "common.cuh"
@@ -28,7 +33,7 @@ namespace da {
 namespace {
 
 constexpr int kPlanThreads = 512, kPlanWarps = kPlanThreads / 32;
-constexpr int kMaxParts = 64;
+constexpr int kMaxParts = 64;  // two estimates a lane; one sequence with one KV head leaves 88 of 152 SMs without work
 constexpr int kTilesInSmem = 2048;  // longer lists are read back from the workspace
 constexpr float kEntryCost = 3.f, kFewEntryCost = 6.f, kMergeCost = 3.f, kMergeStep = 0.45f;  // key tiles' times
 

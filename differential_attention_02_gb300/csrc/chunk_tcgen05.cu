@@ -30,6 +30,13 @@
 // query rows once (chunk_fp8.cuh). The K scales go into the maps' score scales, V's into
 // the epilogue.
 //
+// Weights. The operands of a product have one type, so beside a bf16 V the weights are bf16:
+// each is off by up to 2^-8 of itself, 1.66e-3 RMS per map, while their sum is fp32 of the
+// unrounded ones. On the operators' cases the two maps' difference is off by 2.0e-3 RMS and a
+// bf16 output by 2.6e-3, where fp32 weights (the decode kernels) give 1.7e-3; the
+// prefill kernels make the same choice. Weights in two bf16 parts would take 320 multiply-adds
+// a row, key and map instead of 192, on a tensor pipe that long prompts already keep 52% busy.
+//
 // Entries that finish their tile store the output; the others leave per row and map
 // the unnormalised accumulator, running maximum and sum (columns in quartets, rows
 // innermost, so that a warp's 32 rows store 512 contiguous bytes).

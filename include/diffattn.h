@@ -418,7 +418,9 @@ diffattn_status diffattn_kv_append_chunk_paged_fp8(diffattn_tensor k1_new, diffa
  * p = seq_lens[b] - n_b + i of sequence b and sees cache entries 0 .. p. The computation per
  * row is that of diffattn_decode_paged, on the tensor cores (P rounded to bf16, or to f16
  * over an fp8 cache, where a weight is off by 2^-32 of the row's largest at most if that
- * is more than half a step of f16).
+ * is more than half a step of f16; with bf16 P an output is off by 2.0e-3 relative RMS
+ * where the decode's fp32 weights give its own rounding alone). Scores times log2 e have
+ * to stay below 2^24 in magnitude, where fp32 tells units apart.
  *
  * q1, q2: [T, H, d] bf16, given by token stride (stride_n) and head stride (stride_h).
  * k1_pages .. num_pages, kv_group: as for diffattn_decode_paged; kv_group at most 128.
