@@ -21,7 +21,8 @@
 // Measured on 16 sequences x 5 drafted tokens over 8192 keys, 16 query and 8 KV heads (10 rows a
 // tile; the bytes take 40 us): 113 us in 128-row tiles; here 104 with the conversion's
 // result joined by hand, 84 with the instruction written out, 78 with steps of two tiles and
-// rings of their own, 74 with two issuers (69 to 72 with the lists' bounds of api.cu). A key tile takes 1,500 cycles, 1.2 times what the
+// rings of their own, 74 with two issuers (69 to 72 with the lists' bounds of api.cu). A
+// key tile takes 1,500 cycles, 1.2 times what the
 // bytes need on the 128 SMs that have an item; a start takes 8 us, most of it
 // instructions fetched for the first time. Slower were the exponentials of 32 rows (94 against 84 us),
 // two streams of tiles with accumulators of their own (98), loops over the rows with more code

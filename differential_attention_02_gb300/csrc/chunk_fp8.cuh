@@ -35,8 +35,9 @@ constexpr float kWeightShift = 7.f;  // log2 units
 // place in its swizzled boxes, by the thread that owns the row; returns 2^-shift. The row's
 // largest exponent goes to 2^15, so nothing overflows, and what falls below fp16's normal
 // range is smaller than the row's maximum by 2^-29 and more: less than the fp32 sums of the
-// scores keep, unless K is zero in the row's largest channels. (Rows below 2^-111 keep a factor of 2^126, the last whose inverse is a normal
-// number; their values still come to 2^-7 and more, well inside fp16's normal range.)
+// scores keep, unless K is zero in the row's largest channels. (Rows below 2^-111 keep a
+// factor of 2^126, the last whose inverse is a normal number; their values still come to
+// 2^-7 and more, well inside fp16's normal range.)
 template <int D>
 __device__ __forceinline__ float q_row_to_f16(uint8_t* boxes, int r) {
     uint32_t m = 0;  // largest magnitude of a packed pair's halves
