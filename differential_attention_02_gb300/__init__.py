@@ -12,6 +12,7 @@ import ctypes
 import os
 import struct
 import threading
+from collections import namedtuple
 
 import torch
 
@@ -32,7 +33,9 @@ EXPORTED = ("diffattn_status_string", "diffattn_lambda", "diffattn_fwd", "diffat
             "diffattn_fwd_host_buffer_size", "diffattn_train_saved_size", "diffattn_fwd_train",
             "diffattn_bwd_saved", "diffattn_rope_freqs", "diffattn_rope", "diffattn_kv_append_chunk_paged",
             "diffattn_kv_append_chunk_paged_fp8", "diffattn_chunk_paged", "diffattn_chunk_paged_fp8",
-            "diffattn_chunk_workspace_size")
+            "diffattn_chunk_workspace_size", "diffattn_beam_select", "diffattn_beam_workspace_size",
+            "diffattn_beam_reorder", "diffattn_pages_fork", "diffattn_pages_compact", "diffattn_pages_copy",
+            "diffattn_pages_workspace_size")
 
 
 class DiffAttnError(RuntimeError):
@@ -144,6 +147,20 @@ def load_library(path: str = LIB_PATH) -> ctypes.CDLL:
     lib.diffattn_chunk_paged_fp8.argtypes = chunk + [f32] * 3 + [i32, vp, sz, vp]
     lib.diffattn_chunk_workspace_size.restype = i32
     lib.diffattn_chunk_workspace_size.argtypes = [i32] * 7 + [ctypes.POINTER(sz)]
+    lib.diffattn_beam_select.restype = i32
+    lib.diffattn_beam_select.argtypes = [vp, i64, i64, i32, vp, vp, vp, i32, f32] + [i32] * 4 + [vp] * 6 + [sz, vp]
+    lib.diffattn_beam_workspace_size.restype = i32
+    lib.diffattn_beam_workspace_size.argtypes = [i32] * 4 + [ctypes.POINTER(sz)]
+    lib.diffattn_beam_reorder.restype = i32
+    lib.diffattn_beam_reorder.argtypes = [ctypes.c_char_p, i32, vp, vp, i32, i32, vp]
+    lib.diffattn_pages_fork.restype = i32
+    lib.diffattn_pages_fork.argtypes = [vp] * 6 + [i32] + [vp] * 5 + [i32] * 4 + [vp, sz, vp]
+    lib.diffattn_pages_compact.restype = i32
+    lib.diffattn_pages_compact.argtypes = [vp] * 7 + [i32, vp] + [i32] * 3 + [vp, sz, vp]
+    lib.diffattn_pages_copy.restype = i32
+    lib.diffattn_pages_copy.argtypes = [ctypes.c_char_p, i32, vp, vp, i32, i32, vp]
+    lib.diffattn_pages_workspace_size.restype = i32
+    lib.diffattn_pages_workspace_size.argtypes = [i32, i32, ctypes.POINTER(sz)]
     fpp = ctypes.POINTER(ctypes.c_float)
     lib.diffattn_lambda_bwd.restype = i32
     lib.diffattn_lambda_bwd.argtypes = [fpp] * 4 + [i32, f32] + [fpp] * 4
@@ -754,6 +771,318 @@ def diffattn_chunk_paged(q1, q2, k1_pages, k2_pages, v_pages, block_table, q_sta
         kept = _serving_workspace(chunk_workspace_bytes(T, B, H, kv_group, L, d, Dv), dev)
     _check(call(*args, code, kept.data_ptr(), kept.numel(), _raw_stream(dev.index)), name)
     return out
+
+
+# ------------------------------------------------------------------ beam search, pages of the cache
+BeamChoice = namedtuple("BeamChoice", "scores tokens parents finished lengths")
+BeamChoice.__doc__ = """What diffattn_beam_select chose, best first: scores fp32, tokens and parents int32, and finished (bool) and
+lengths (int32) where they were asked for, all [B, W]."""
+
+PagePlan = namedtuple("PagePlan", "table lens refs copies info moved", defaults=(None,))
+PagePlan.__doc__ = """A block table's state after diffattn_pages_fork or diffattn_pages_compact: table [S, max_pages], lens [S] and refs
+[num_pages] (the holders of each page), and the copies [n, 3] (page, new page, rows) that diffattn_pages_copy has to
+make, info [4]: copies, pages that could not be had, free and held pages. moved [num_pages]: each page's new
+place after a compaction. All int32."""
+
+
+def beam_workspace_bytes(B, K, V, width) -> int:
+    n = ctypes.c_size_t()
+    _check((_lib or load_library()).diffattn_beam_workspace_size(B, K, V, width, ctypes.byref(n)), "diffattn_beam_workspace_size")
+    return n.value
+
+
+def pages_workspace_bytes(rows, num_pages) -> int:
+    n = ctypes.c_size_t()
+    _check((_lib or load_library()).diffattn_pages_workspace_size(rows, num_pages, ctypes.byref(n)),
+           "diffattn_pages_workspace_size")
+    return n.value
+
+
+def _with_workspace(call, args, ws, dev, need, name):
+    """Calls with the kept workspace of this thread and stream, grown by need() when it is too small, or with ws."""
+    if ws is not None:
+        _workspace_arg(ws, dev)
+    kept = ws if ws is not None else _kept_workspace(dev)
+    status = ERR_WORKSPACE if kept is None else call(*args, kept.data_ptr(), kept.numel(), _raw_stream(dev.index))
+    if status == ERR_WORKSPACE and ws is None:
+        kept = _serving_workspace(need(), dev)
+        status = call(*args, kept.data_ptr(), kept.numel(), _raw_stream(dev.index))
+    _check(status, name)
+
+
+def _typed(t, dtype, dev, shape, what):
+    if t.dtype != dtype or t.shape != shape or t.device != dev or not t.is_contiguous():
+        raise ValueError(f"{what} must be a contiguous {dtype} tensor of shape {list(shape)} on the operands' device")
+
+
+def diffattn_beam_select(logits, scores, width: int | None = None, finished=None, lengths=None, eos: int | None = None,
+                         length_penalty: float = 0.0, out: BeamChoice | None = None, ws=None, stream=None) -> BeamChoice:
+    """The `width` (default: K) best continuations of each sequence over its beams and the vocabulary. logits [B, K, V]
+    fp32, bf16 or fp16 (last dimension contiguous), scores [B, K] fp32. A live beam offers every token v with
+    scores + log softmax(logits)[v]; a finished one (bool [B, K]) itself, as token `eos`. Candidates are ranked by
+    score / max(length, 1)^length_penalty, where lengths (int32 [B, K], needed for it) grow by one for live
+    beams; ties go to the lowest beam and token. Logits of -inf or NaN are no candidates; places that none is
+    left for hold score -inf, parent -1, token `eos` (or 0), finished and length 0. Returns a BeamChoice:
+    finished where `eos` is given, lengths where they are. out: its tensors are written (with width K they may
+    be the inputs themselves)."""
+    dev = logits.device
+    ctx = _elsewhere(dev, stream)
+    if ctx is not None:
+        with ctx:
+            return diffattn_beam_select(logits, scores, width, finished, lengths, eos, length_penalty, out, ws)
+    if logits.dim() != 3:
+        raise ValueError("logits must be [B, K, V]")
+    B, K, V = logits.shape
+    sb, sk, s1 = logits.stride()
+    if s1 != 1 and V > 1:
+        raise ValueError("logits must have a contiguous last dimension")
+    shape = (B, K)
+    _typed(scores, torch.float32, dev, shape, "scores")
+    if finished is not None:
+        if eos is None:
+            raise ValueError("finished goes with eos")
+        _typed(finished, torch.bool, dev, shape, "finished")
+    if lengths is not None:
+        _typed(lengths, _INT32, dev, shape, "lengths")
+    W = K if width is None else int(width)
+    if out is None:
+        new = lambda dtype: torch.empty((B, W), dtype=dtype, device=dev)  # noqa: E731
+        out = BeamChoice(new(torch.float32), new(_INT32), new(_INT32), None if eos is None else new(torch.bool),
+                         None if lengths is None else new(_INT32))
+    else:
+        for t, dtype, what in zip(out, (torch.float32, _INT32, _INT32, torch.bool, _INT32), BeamChoice._fields):
+            if t is not None or what in ("scores", "tokens", "parents"):
+                _typed(t, dtype, dev, (B, W), "out." + what)
+    o_s, o_t, o_p, o_f, o_l = out
+    args = (logits.data_ptr(), sb, sk, _dtype_code(logits.dtype), scores.data_ptr(), None if finished is None else finished.data_ptr(),
+            None if lengths is None else lengths.data_ptr(), -1 if eos is None else int(eos), float(length_penalty), B, K, V, W,
+            o_s.data_ptr(), o_t.data_ptr(), o_p.data_ptr(), None if o_f is None else o_f.data_ptr(),
+            None if o_l is None else o_l.data_ptr())
+    _with_workspace((_lib or load_library()).diffattn_beam_select, args, ws, dev, lambda: beam_workspace_bytes(B, K, V, W),
+                    "diffattn_beam_select")
+    return out
+
+
+_PACK_STATE = struct.Struct("=4q4i").pack
+
+
+def diffattn_beam_reorder(states, parents, lens=None, stream=None):
+    """Per-beam states take the rows of their parents, in place: row b K + k of each tensor becomes what row
+    b K + parents[b, k] was (parents int32 [B, K] as diffattn_beam_select gives them; -1 leaves a row as it
+    is). states: tensors of any type with B K rows, each row of one stride, or, with lens (int32 [B K]),
+    contiguous caches [B K, H, tokens, width] of which the first lens tokens of the parent are moved. Returns
+    the tensors."""
+    dev = parents.device
+    ctx = _elsewhere(dev, stream)
+    if ctx is not None:
+        with ctx:
+            return diffattn_beam_reorder(states, parents, lens)
+    if parents.dim() != 2:
+        raise ValueError("parents must be [B, K]")
+    B, K = shape = parents.shape
+    _int32(parents, dev, shape, "parents")
+    if lens is not None:
+        _int32(lens, dev, (B * K,), "lens")
+    packed = []
+    for t in states:
+        if t.device != dev or t.dim() < 1 or t.shape[0] != B * K:
+            raise ValueError("states must have B K rows and be on the parents' device")
+        size, strides = t.element_size(), t.stride()
+        if lens is not None:
+            if t.dim() != 4 or (strides[3] != 1 and t.shape[3] > 1):
+                raise ValueError("with lens, states must be caches [B K, H, tokens, width] with a contiguous last dimension")
+            _, parts, rows, width = t.shape
+            if (rows > 1 and strides[2] < width) or (parts > 1 and strides[1] < width) or (B * K > 1 and strides[0] < width):
+                raise ValueError("states must not overlap themselves")
+            packed.append(_PACK_STATE(t.data_ptr(), strides[0] * size, strides[1] * size, strides[2] * size, parts, rows, width * size, 1))
+        else:
+            n = t[0].numel() if t.shape[0] else 0
+            if t.shape[0] and (not t[0].is_contiguous() or (B * K > 1 and strides[0] < n)):
+                raise ValueError("the rows of states must be contiguous")
+            # long rows in parts of a MiB or less, so that their sizes stay within 31 bits
+            whole, row = n * size, 1 << 20
+            if whole <= row:
+                packed.append(_PACK_STATE(t.data_ptr(), strides[0] * size, 0, 0, 1, 1, whole, 0))
+            else:
+                packed.append(_PACK_STATE(t.data_ptr(), strides[0] * size, 0, row, 1, whole // row, row, 0))
+                if whole % row:
+                    packed.append(_PACK_STATE(t.data_ptr() + whole // row * row, strides[0] * size, 0, 0, 1, 1, whole % row, 0))
+    _check((_lib or load_library()).diffattn_beam_reorder(b"".join(packed), len(packed), parents.data_ptr(),
+                                                          None if lens is None else lens.data_ptr(), B, K, _raw_stream(dev.index)),
+           "diffattn_beam_reorder")
+    return states
+
+
+def _page_state(table, lens, refs):
+    """The device and sizes of a block table's state."""
+    dev = table.device
+    if table.dim() != 2 or refs.dim() != 1:
+        raise ValueError("table must be [S, max_pages] and refs [num_pages]")
+    (S, M), P = table.shape, refs.shape[0]
+    _int32(table, dev, (S, M), "table")
+    _int32(lens, dev, (S,), "lens")
+    _int32(refs, dev, (P,), "refs")
+    return dev, S, M, P
+
+
+def diffattn_pages_fork(table, lens, refs, parents=None, grow: int = 0, new_lens=None, done=None, out: PagePlan | None = None,
+                        ws=None, stream=None) -> PagePlan:
+    """Which pages the rows of a block table (int32 [S, max_pages], lens int32 [S]; refs int32 [num_pages], the
+    holders of each page, 0: free) hold after a step. Row b K + k continues row b K + parents[b, k] (int32 [B, K] with
+    B K = S, or None: each row itself; -1, or done (bool [S]): none) and has then new_lens[i] tokens (int32 [S]),
+    or without them its parent's and `grow` more (none without a parent). Whole pages of kept tokens are
+    shared, the begun page stays with the first row that keeps it and is listed in the plan's copies for the
+    others, further pages are the lowest free ones, and pages that no row holds any more are free. Ending
+    rows: done, or new_lens 0; starting ones: no parent and new_lens; taking tokens back: smaller new_lens;
+    beam search: the parents of diffattn_beam_select and grow=1. Returns a PagePlan; diffattn_pages_copy then copies the
+    begun pages, before anything is appended. out: a plan whose tensors are written (table, lens and refs may be the
+    inputs themselves). Where the pool or the table is full, info[1] tells how many pages were missing; their
+    entries are -1."""
+    dev = table.device
+    ctx = _elsewhere(dev, stream)
+    if ctx is not None:
+        with ctx:
+            return diffattn_pages_fork(table, lens, refs, parents, grow, new_lens, done, out, ws)
+    dev, S, M, P = _page_state(table, lens, refs)
+    K = max(S, 1)
+    if parents is not None:
+        if parents.dim() != 2 or parents.shape[0] * parents.shape[1] != S:
+            raise ValueError("parents must be [B, K] with B K rows of the table")
+        K = max(parents.shape[1], 1)
+        _int32(parents, dev, parents.shape, "parents")
+    if new_lens is not None:
+        _int32(new_lens, dev, (S,), "new_lens")
+    if done is not None:
+        _typed(done, torch.bool, dev, (S,), "done")
+    if out is None:
+        new = lambda *shape: torch.empty(shape, dtype=_INT32, device=dev)  # noqa: E731
+        out = PagePlan(new(S, M), new(S), new(P), new(S, 3), new(4))
+    else:
+        for t, shape, what in zip(out, ((S, M), (S,), (P,), (S, 3), (4,)), PagePlan._fields):
+            _int32(t, dev, shape, "out." + what)
+    args = (table.data_ptr(), lens.data_ptr(), refs.data_ptr(), None if parents is None else parents.data_ptr(),
+            None if new_lens is None else new_lens.data_ptr(), None if done is None else done.data_ptr(), int(grow),
+            out.table.data_ptr(), out.lens.data_ptr(), out.refs.data_ptr(), out.copies.data_ptr(), out.info.data_ptr(), S // K, K, M, P)
+    _with_workspace((_lib or load_library()).diffattn_pages_fork, args, ws, dev, lambda: pages_workspace_bytes(S, P),
+                    "diffattn_pages_fork")
+    return out
+
+
+def diffattn_pages_compact(table, lens, refs, out: PagePlan | None = None, ws=None, stream=None) -> PagePlan:
+    """The held pages moved to the front of the pool: the highest ones go to the lowest free places, as many as
+    `out.copies` has room for (default: all). table, lens and refs as in diffattn_pages_fork. Returns a PagePlan with the
+    table and counts of the new places, the copies for diffattn_pages_copy, and `moved` [num_pages], each page's new
+    place (-1: it was free) for others that hold pages. out: table and refs may be the inputs themselves; lens
+    are those given."""
+    dev = table.device
+    ctx = _elsewhere(dev, stream)
+    if ctx is not None:
+        with ctx:
+            return diffattn_pages_compact(table, lens, refs, out, ws)
+    dev, S, M, P = _page_state(table, lens, refs)
+    if out is None:
+        new = lambda *shape: torch.empty(shape, dtype=_INT32, device=dev)  # noqa: E731
+        out = PagePlan(new(S, M), lens, new(P), new(P // 2, 3), new(4), new(P))
+    else:
+        if out.copies.dim() != 2 or out.copies.shape[0] > P // 2 or out.moved is None:
+            raise ValueError("out.copies must be [n, 3] with at most num_pages / 2 entries, and out.moved [num_pages]")
+        for t, shape, what in zip(out, ((S, M), (S,), (P,), (out.copies.shape[0], 3), (4,), (P,)), PagePlan._fields):
+            _int32(t, dev, shape, "out." + what)
+        if out.lens is not lens:
+            out.lens.copy_(lens)
+    args = (table.data_ptr(), lens.data_ptr(), refs.data_ptr(), out.table.data_ptr(), out.refs.data_ptr(), out.moved.data_ptr(),
+            out.copies.data_ptr(), out.copies.shape[0], out.info.data_ptr(), S, M, P)
+    _with_workspace((_lib or load_library()).diffattn_pages_compact, args, ws, dev, lambda: pages_workspace_bytes(S, P),
+                    "diffattn_pages_compact")
+    return out
+
+
+class PagePools:
+    """The page tensors of a cache, all its layers', as diffattn_pages_copy takes them (made by page_pools). It keeps the
+    tensors, and their addresses: a tensor that is moved needs new pools."""
+
+    def __init__(self, tensors):
+        self.tensors = list(tensors)
+        if not self.tensors:
+            raise ValueError("at least one tensor of pages")
+        self.device, self.num_pages = self.tensors[0].device, self.tensors[0].shape[0]
+        packed = []
+        for t in self.tensors:
+            if t.dim() != 4 or t.shape[0] != self.num_pages or t.shape[2] != 64 or t.device != self.device:
+                raise ValueError("pages must be [num_pages, H_kv, 64, width] on one device")
+            (sp, sh, sr, s1), size, width = t.stride(), t.element_size(), t.shape[3]
+            heads = t.shape[1]
+            if s1 != 1 or sr < width or (heads > 1 and sh < width) or (self.num_pages > 1 and sp < width):
+                raise ValueError("pages must have a contiguous last dimension and not overlap")
+            packed.append(_PACK_POOL(t.data_ptr(), (sp if self.num_pages > 1 else 0) * size, (sh if heads > 1 else 0) * size,
+                                     sr * size, heads, width * size))
+        self._c, self._n = b"".join(packed), len(packed)
+
+
+_PACK_POOL = struct.Struct("=4q2i").pack
+
+
+def page_pools(*pages) -> PagePools:
+    """Pools of pages [num_pages, H_kv, 64, width] that share their page numbers: (k1_pages, k2_pages, v_pages) of a layer,
+    or any number of such tuples and tensors. Made once and kept, like a weight."""
+    flat = []
+    for p in pages:
+        flat.extend([p] if isinstance(p, torch.Tensor) else [t for q in p for t in ([q] if isinstance(q, torch.Tensor) else q)])
+    return PagePools(flat)
+
+
+def diffattn_pages_copy(pools: PagePools, copies, info=None, stream=None) -> None:
+    """pool[dst, :, :rows] = pool[src, :, :rows] for every entry (src, dst, rows) of copies (int32 [n, 3]) and every pool;
+    entries with a page outside the pool are skipped, and with `info` (of a plan) those behind its first
+    value. No page may be written by two entries, or written by one and read by another."""
+    dev = pools.device
+    ctx = _elsewhere(dev, stream)
+    if ctx is not None:
+        with ctx:
+            return diffattn_pages_copy(pools, copies, info)
+    n = copies.shape[0] if copies.dim() == 2 else 0
+    _int32(copies, dev, (n, 3), "copies")
+    if info is not None:
+        _int32(info, dev, (4,), "info")
+    _check((_lib or load_library()).diffattn_pages_copy(pools._c, pools._n, copies.data_ptr(), None if info is None else info.data_ptr(), n,
+                                                        pools.num_pages, _raw_stream(dev.index)), "diffattn_pages_copy")
+
+
+def beam_step(x, w_vocab, scores, pools: PagePools, table, lens, refs, finished=None, lengths=None, eos: int | None = None,
+              length_penalty: float = 0.0, vocabulary: int | None = None, choice: BeamChoice | None = None,
+              plan: PagePlan | None = None, ws=None, stream=None):
+    """A step of beam search over a paged cache, after the model has run on the beams' last tokens: the product with the
+    vocabulary, the selection of the K best continuations of each sequence, and the cache of each beam made
+    that of its parent, with a page for the next token. x [B K, d_model] and w_vocab [d_model, >= vocabulary] both
+    bf16 or both fp16 (logits are fp32; vocabulary, default all, leaves padding columns out); scores [B, K] and finished, lengths,
+    eos and length_penalty as in diffattn_beam_select; pools of all layers; table [B K, max_pages], lens and refs as in
+    diffattn_pages_fork. Finished beams hold no pages and have length 0: the serving calls give their rows zeros. choice and
+    plan are written where they are given (they may hold the inputs themselves), so that a step can be captured
+    and replayed. Returns (choice, plan). The next pass then takes choice.tokens as rows, plan.table, plan.lens as
+    seq_lens and q_start = 0, 1 .. B K. A search starts from scores (0, -inf, -inf ..): every beam then continues
+    the first, whose row holds the prompt."""
+    dev = x.device
+    ctx = _elsewhere(dev, stream)
+    if ctx is not None:
+        with ctx:
+            return beam_step(x, w_vocab, scores, pools, table, lens, refs, finished, lengths, eos, length_penalty, vocabulary,
+                             choice, plan, ws)
+    if x.dim() != 2 or scores.dim() != 2 or x.shape[0] != scores.numel() or table.shape[0] != x.shape[0]:
+        raise ValueError("x [B K, d_model], scores [B, K] and table [B K, max_pages]")
+    _on_device(dev, w_vocab, scores, table, lens, refs)
+    if pools.device != dev or pools.num_pages != refs.shape[0]:
+        raise ValueError("pools and refs must have the same pages, on the operands' device")
+    (B, K), V = scores.shape, w_vocab.shape[1] if vocabulary is None else int(vocabulary)
+    if not 0 < V <= w_vocab.shape[1]:
+        raise ValueError("vocabulary must be at most w_vocab's columns")
+    if ws is None:
+        ws = _serving_workspace(max(beam_workspace_bytes(B, K, V, K), pages_workspace_bytes(B * K, refs.shape[0])), dev)
+    logits = gemm(x, w_vocab, out_dtype=torch.float32, ws=ws).view(B, K, -1)[..., :V]
+    choice = diffattn_beam_select(logits, scores, None, finished, lengths, eos, length_penalty, out=choice, ws=ws)
+    done = None if choice.finished is None else choice.finished.view(-1)
+    plan = diffattn_pages_fork(table, lens, refs, choice.parents, grow=1, done=done, out=plan, ws=ws)
+    diffattn_pages_copy(pools, plan.copies, plan.info)
+    return choice, plan
 
 
 def add_rmsnorm(x, z=None, weight=None, eps: float = 1e-5, want_y: bool = False, want_n: bool = True,

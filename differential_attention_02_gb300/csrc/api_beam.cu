@@ -1,0 +1,247 @@
+// Host side of the beam search and page calls of the C ABI: argument checks and dispatch.
+#include <math.h>
+
+#include <algorithm>
+#include <cmath>
+
+#include "../../include/diffattn.h"
+#include "common.cuh"
+#include "kernels.h"
+
+using namespace da;
+
+namespace {
+diffattn_status cuda_status(cudaError_t e) { return e == cudaSuccess ? DIFFATTN_OK : DIFFATTN_ERR_CUDA; }
+size_t round256(size_t x) { return (x + 255) & ~(size_t)255; }
+bool aligned(const void* p, size_t n) { return (reinterpret_cast<uintptr_t>(p) & (n - 1)) == 0; }
+bool workspace_ok(const void* ws, size_t bytes, size_t need) {
+    return ws != nullptr && aligned(ws, 256) && bytes >= need;
+}
+
+// Workspace of the selection: control block, a row's best logits, its sum and its maximum.
+struct BeamLayout {
+    size_t keys, sums, maxima, total;
+};
+bool beam_layout(int B, int K, int V, int W, BeamLayout* l) {
+    if (B < 0 || K < 1 || K > kMaxBeams || V < 1 || V > DIFFATTN_MAX_VOCABULARY || W < 1 || W > kMaxBeamWidth || B > 65535)
+        return false;
+    const size_t rows = (size_t)B * K;
+    l->keys = kControlBytes;
+    l->sums = l->keys + round256(rows * W * sizeof(uint64_t));
+    l->maxima = l->sums + round256(rows * sizeof(double));
+    l->total = l->maxima + round256(rows * sizeof(float));
+    return true;
+}
+
+// Workspace of the page plans: control block, four values a row, one a page.
+struct PageLayout {
+    size_t tail, prefix, first, copy_at, claim, total;
+};
+bool page_layout(int S, int P, PageLayout* l) {
+    if (S < 0 || S > kMaxPageRows || P < 1) return false;
+    const size_t row = round256((size_t)(S + 1) * sizeof(int32_t));
+    l->tail = kControlBytes;
+    l->prefix = l->tail + row;
+    l->first = l->prefix + row;
+    l->copy_at = l->first + row;
+    l->claim = l->copy_at + row;
+    l->total = l->claim + round256((size_t)P * sizeof(int32_t));
+    return true;
+}
+
+// Whether [a, a + n) and [b, b + m) share bytes.
+bool overlap(const void* a, size_t n, const void* b, size_t m) {
+    const uintptr_t x = reinterpret_cast<uintptr_t>(a), y = reinterpret_cast<uintptr_t>(b);
+    return x < y + m && y < x + n;
+}
+// Two arrays of int32: apart, or one array for both.
+bool apart_or_same(const void* a, const void* b, int64_t n) {
+    return a == b || !overlap(a, (size_t)n * 4, b, (size_t)n * 4);
+}
+}  // namespace
+
+extern "C" {
+
+diffattn_status diffattn_beam_workspace_size(int B, int K, int V, int W, size_t* bytes) {
+    BeamLayout l;
+    if (!bytes || !beam_layout(B, K, V, W, &l)) return DIFFATTN_ERR_INVALID_ARG;
+    *bytes = l.total;
+    return DIFFATTN_OK;
+}
+
+diffattn_status diffattn_beam_select(const void* logits, int64_t stride_b, int64_t stride_k, int in_dtype,
+                                     const float* scores, const uint8_t* finished, const int32_t* lengths, int eos,
+                                     float length_penalty, int B, int K, int V, int W, float* scores_out,
+                                     int32_t* tokens, int32_t* parents, uint8_t* finished_out, int32_t* lengths_out,
+                                     void* workspace, size_t workspace_bytes, void* stream) {
+    BeamLayout l;
+    if (!beam_layout(B, K, V, W, &l) || W > (int64_t)K * V) return DIFFATTN_ERR_INVALID_ARG;
+    if (in_dtype != DIFFATTN_F32 && in_dtype != DIFFATTN_BF16 && in_dtype != DIFFATTN_F16) return DIFFATTN_ERR_INVALID_ARG;
+    if (eos < -1 || eos >= V || ((finished || finished_out) && eos < 0) || !std::isfinite(length_penalty) ||
+        ((length_penalty != 0.f || lengths_out) && !lengths))
+        return DIFFATTN_ERR_INVALID_ARG;
+    if (B == 0) return DIFFATTN_OK;
+    const size_t size = in_dtype == DIFFATTN_F32 ? 4 : 2;
+    if (!logits || !scores || !scores_out || !tokens || !parents || !aligned(logits, size) || !aligned(scores, 4) ||
+        !aligned(lengths, 4) || !aligned(scores_out, 4) || !aligned(tokens, 4) || !aligned(parents, 4) || !aligned(lengths_out, 4))
+        return DIFFATTN_ERR_INVALID_ARG;
+    if ((K > 1 && stride_k < 0) || (B > 1 && stride_b < 0)) return DIFFATTN_ERR_INVALID_ARG;
+    if (!workspace_ok(workspace, workspace_bytes, l.total)) return DIFFATTN_ERR_WORKSPACE;
+    uint8_t* ws = static_cast<uint8_t*>(workspace);
+    BeamParams p{};
+    p.logits = logits;
+    p.stride_b = B > 1 ? stride_b : 0;
+    p.stride_k = K > 1 ? stride_k : 0;
+    p.scores = scores;
+    p.finished = finished;
+    p.lengths = lengths;
+    p.eos = eos;
+    p.length_penalty = length_penalty;
+    p.B = B; p.K = K; p.V = V; p.W = W;
+    p.scores_out = scores_out;
+    p.tokens = tokens;
+    p.parents = parents;
+    p.finished_out = finished_out;
+    p.lengths_out = lengths_out;
+    p.keys = reinterpret_cast<uint64_t*>(ws + l.keys);
+    p.sums = reinterpret_cast<double*>(ws + l.sums);
+    p.maxima = reinterpret_cast<float*>(ws + l.maxima);
+    return cuda_status(launch_beam_select(p, in_dtype == DIFFATTN_F32 ? 0 : in_dtype == DIFFATTN_BF16 ? 1 : 2,
+                                          static_cast<cudaStream_t>(stream)));
+}
+
+diffattn_status diffattn_beam_reorder(const diffattn_beam_state* states, int count, const int32_t* parents,
+                                      const int32_t* lens, int B, int K, void* stream) {
+    if (count < 0 || B < 0 || B > 65535 || K < 1 || K > kMaxBeams || (count > 0 && !states)) return DIFFATTN_ERR_INVALID_ARG;
+    for (int i = 0; i < count; ++i) {
+        const diffattn_beam_state& s = states[i];
+        if (s.parts < 0 || s.rows < 0 || s.row_bytes < 0 || s.stride_state < 0 || s.stride_part < 0 || s.stride_row < 0)
+            return DIFFATTN_ERR_INVALID_ARG;
+        if (s.by_len && !lens) return DIFFATTN_ERR_INVALID_ARG;
+        // 2^39 units at most: 2^31 blocks of a thread each
+        if ((double)s.parts * s.rows * s.row_bytes > 0x1p38) return DIFFATTN_ERR_INVALID_ARG;
+        if (s.parts && s.rows && s.row_bytes && !s.ptr) return DIFFATTN_ERR_INVALID_ARG;
+    }
+    if (B == 0 || count == 0) return DIFFATTN_OK;
+    if (!parents || !aligned(parents, 4) || !aligned(lens, 4)) return DIFFATTN_ERR_INVALID_ARG;
+    // States are moved in the largest unit that their addresses and sizes allow, those of one unit in one launch.
+    for (int unit : {16, 4, 2, 1}) {
+        ReorderParams p{};
+        p.parents = parents;
+        p.lens = lens;
+        p.B = B; p.K = K;
+        int n = 0;
+        for (int i = 0; i <= count; ++i) {
+            if (i < count) {
+                const diffattn_beam_state& s = states[i];
+                const uint64_t bits = reinterpret_cast<uint64_t>(s.ptr) | s.stride_state | (s.parts > 1 ? s.stride_part : 0) |
+                                      (s.rows > 1 ? s.stride_row : 0) | (uint64_t)s.row_bytes;
+                const int fits = bits % 16 == 0 ? 16 : bits % 4 == 0 ? 4 : bits % 2 == 0 ? 2 : 1;
+                if (fits == unit && s.parts && s.rows && s.row_bytes)
+                    p.state[n++] = ReorderState{static_cast<uint8_t*>(s.ptr), s.stride_state, s.stride_part, s.stride_row,
+                                                s.parts, s.rows, s.row_bytes / unit, s.by_len};
+            }
+            if (n == kReorderStates || (i == count && n > 0)) {
+                const cudaError_t e = launch_beam_reorder(p, unit, n, static_cast<cudaStream_t>(stream));
+                if (e != cudaSuccess) return DIFFATTN_ERR_CUDA;
+                n = 0;
+            }
+        }
+    }
+    return DIFFATTN_OK;
+}
+
+diffattn_status diffattn_pages_workspace_size(int rows, int num_pages, size_t* bytes) {
+    PageLayout l;
+    if (!bytes || !page_layout(rows, num_pages, &l)) return DIFFATTN_ERR_INVALID_ARG;
+    *bytes = l.total;
+    return DIFFATTN_OK;
+}
+
+diffattn_status diffattn_pages_fork(const int32_t* table, const int32_t* lens, const int32_t* refs,
+                                    const int32_t* parents, const int32_t* new_lens, const uint8_t* done, int grow,
+                                    int32_t* table_out, int32_t* lens_out, int32_t* refs_out, int32_t* copies,
+                                    int32_t* info, int B, int K, int max_pages, int num_pages, void* workspace,
+                                    size_t workspace_bytes, void* stream) {
+    if (B < 0 || K < 1 || max_pages < 1 || num_pages < 1 || (int64_t)B * K > kMaxPageRows ||
+        (int64_t)B * K * max_pages > INT32_MAX)
+        return DIFFATTN_ERR_INVALID_ARG;
+    const int S = B * K;
+    PageLayout l;
+    if (!page_layout(S, num_pages, &l)) return DIFFATTN_ERR_INVALID_ARG;
+    for (const void* q : {(const void*)table, (const void*)lens, (const void*)table_out, (const void*)lens_out, (const void*)copies})
+        if ((S > 0 && !q) || !aligned(q, 4)) return DIFFATTN_ERR_INVALID_ARG;
+    for (const void* q : {(const void*)refs, (const void*)refs_out, (const void*)info})
+        if (!q || !aligned(q, 4)) return DIFFATTN_ERR_INVALID_ARG;
+    if (!aligned(parents, 4) || !aligned(new_lens, 4) || !apart_or_same(table, table_out, (int64_t)S * max_pages) ||
+        !apart_or_same(lens, lens_out, S) || !apart_or_same(refs, refs_out, num_pages))
+        return DIFFATTN_ERR_INVALID_ARG;
+    if (!workspace_ok(workspace, workspace_bytes, l.total)) return DIFFATTN_ERR_WORKSPACE;
+    uint8_t* ws = static_cast<uint8_t*>(workspace);
+    const auto at = [ws](size_t offset) { return reinterpret_cast<int32_t*>(ws + offset); };
+    ForkParams p{};
+    p.table = table; p.lens = lens; p.refs = refs; p.parents = parents; p.new_lens = new_lens; p.done = done;
+    p.grow = grow;
+    p.table_out = table_out; p.lens_out = lens_out; p.refs_out = refs_out; p.copies = copies; p.info = info;
+    p.S = S; p.K = K; p.M = max_pages; p.P = num_pages;
+    p.tail = at(l.tail); p.prefix = at(l.prefix); p.first = at(l.first); p.copy_at = at(l.copy_at); p.claim = at(l.claim);
+    return cuda_status(launch_pages_fork(p, static_cast<cudaStream_t>(stream)));
+}
+
+diffattn_status diffattn_pages_compact(const int32_t* table, const int32_t* lens, const int32_t* refs,
+                                       int32_t* table_out, int32_t* refs_out, int32_t* moved, int32_t* copies,
+                                       int max_copies, int32_t* info, int rows, int max_pages, int num_pages,
+                                       void* workspace, size_t workspace_bytes, void* stream) {
+    if (rows < 0 || rows > kMaxPageRows || max_pages < 1 || num_pages < 1 || max_copies < 0 || max_copies > num_pages / 2 ||
+        (int64_t)rows * max_pages > INT32_MAX)
+        return DIFFATTN_ERR_INVALID_ARG;
+    PageLayout l;
+    if (!page_layout(rows, num_pages, &l)) return DIFFATTN_ERR_INVALID_ARG;
+    for (const void* q : {(const void*)refs, (const void*)refs_out, (const void*)moved, (const void*)info})
+        if (!q || !aligned(q, 4)) return DIFFATTN_ERR_INVALID_ARG;
+    if (rows > 0 && (!table || !lens || !table_out || !aligned(table, 4) || !aligned(lens, 4) || !aligned(table_out, 4) ||
+                     !apart_or_same(table, table_out, (int64_t)rows * max_pages)))
+        return DIFFATTN_ERR_INVALID_ARG;
+    if ((max_copies > 0 && !copies) || !aligned(copies, 4) || !apart_or_same(refs, refs_out, num_pages))
+        return DIFFATTN_ERR_INVALID_ARG;
+    if (!workspace_ok(workspace, workspace_bytes, l.total)) return DIFFATTN_ERR_WORKSPACE;
+    uint8_t* ws = static_cast<uint8_t*>(workspace);
+    CompactParams p{};
+    p.table = table; p.lens = lens; p.refs = refs;
+    p.table_out = table_out; p.refs_out = refs_out; p.moved = moved; p.copies = copies; p.info = info;
+    p.S = rows; p.M = max_pages; p.P = num_pages; p.max_copies = max_copies;
+    p.src = reinterpret_cast<int32_t*>(ws + l.claim);  // num_pages / 2 values each
+    p.dst = p.src + num_pages / 2;
+    return cuda_status(launch_pages_compact(p, static_cast<cudaStream_t>(stream)));
+}
+
+diffattn_status diffattn_pages_copy(const diffattn_page_pool* pools, int count, const int32_t* copies,
+                                    const int32_t* n_copies, int max_copies, int num_pages, void* stream) {
+    if (count < 0 || max_copies < 0 || num_pages < 1 || (count > 0 && !pools)) return DIFFATTN_ERR_INVALID_ARG;
+    for (int i = 0; i < count; ++i) {
+        const diffattn_page_pool& q = pools[i];
+        if (!q.ptr || !aligned(q.ptr, 16) || q.heads < 1 || q.row_bytes < 16 || q.row_bytes % 16 || q.row_bytes > (1 << 20) ||
+            q.stride_page < 0 || q.stride_head < 0 || q.stride_row < 0 || q.stride_page % 16 || q.stride_head % 16 ||
+            q.stride_row % 16)
+            return DIFFATTN_ERR_INVALID_ARG;
+    }
+    if (count == 0 || max_copies == 0) return DIFFATTN_OK;
+    if (!copies || !aligned(copies, 4) || !aligned(n_copies, 4)) return DIFFATTN_ERR_INVALID_ARG;
+    for (int first = 0; first < count; first += kCopyPools) {
+        const int n = std::min(kCopyPools, count - first);
+        CopyParams p{};
+        for (int i = 0; i < n; ++i) {
+            const diffattn_page_pool& q = pools[first + i];
+            p.pool[i] = CopyPool{static_cast<uint8_t*>(q.ptr), q.stride_page, q.stride_head, q.stride_row, q.heads, q.row_bytes / 16};
+        }
+        p.copies = copies;
+        p.count = n_copies;
+        p.max_copies = max_copies;
+        p.P = num_pages;
+        const cudaError_t e = launch_pages_copy(p, n, static_cast<cudaStream_t>(stream));
+        if (e != cudaSuccess) return DIFFATTN_ERR_CUDA;
+    }
+    return DIFFATTN_OK;
+}
+
+}  // extern "C"

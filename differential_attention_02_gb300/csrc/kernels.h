@@ -201,6 +201,74 @@ cudaError_t launch_chunk_few(const ChunkParams& p, cudaStream_t stream);    // d
 cudaError_t launch_chunk_64(const ChunkParams& p, cudaStream_t stream);     // d = 64, Dv = 128
 cudaError_t launch_chunk_pair(const ChunkParams& p, cudaStream_t stream);   // d = 128, Dv = 256
 
+// Selection of the best continuations over a sequence's beams and the vocabulary (beam.cu).
+constexpr int kMaxBeams = 32;       // beams of a sequence, and of a group whose states are reordered
+constexpr int kMaxBeamWidth = 64;   // candidates kept per sequence
+struct BeamParams {
+    const void* logits;             // [B, K, V], rows stride_k apart, any alignment of an element
+    int64_t stride_b, stride_k;
+    const float* scores;            // [B, K]
+    const uint8_t* finished;        // [B, K] or null
+    const int32_t* lengths;         // [B, K] or null
+    int eos;                        // -1: none
+    double length_penalty;
+    int B, K, V, W;
+    float* scores_out;              // [B, W] and so on
+    int32_t *tokens, *parents;
+    uint8_t* finished_out;          // or null
+    int32_t* lengths_out;           // or null
+    uint64_t* keys;                 // workspace: [B K][W], a row's best logits
+    double* sums;                   // [B K]: sum of exp(x - max)
+    float* maxima;                  // [B K]
+};
+cudaError_t launch_beam_select(const BeamParams& p, int in_dtype, cudaStream_t stream);
+
+// Rows of per-beam states moved to the places of their children, in place (beam.cu).
+constexpr int kReorderStates = 48;  // of one launch
+struct ReorderState {
+    uint8_t* ptr;                                // [B K][parts][rows][row_bytes], strides in bytes
+    int64_t stride_state, stride_part, stride_row;
+    int parts, rows, units, by_len;              // a row has `units` units
+};
+struct ReorderParams {
+    ReorderState state[kReorderStates];
+    const int32_t *parents, *lens;               // [B, K]; lens [B K] or null
+    int B, K;
+};
+// `unit`: bytes moved at a time (16, 4, 2 or 1), `count` states.
+cudaError_t launch_beam_reorder(const ReorderParams& p, int unit, int count, cudaStream_t stream);
+
+// Which pages of a paged cache each sequence holds (pages.cu).
+constexpr int kMaxPageRows = 4096;  // sequences of one table
+struct ForkParams {
+    const int32_t *table, *lens, *refs, *parents, *new_lens;  // parents, new_lens: or null
+    const uint8_t* done;                                      // or null
+    int grow;
+    int32_t *table_out, *lens_out, *refs_out, *copies, *info;
+    int S, K, M, P;                 // rows, rows of a group, columns, pages
+    int32_t *tail, *prefix, *first, *copy_at, *claim;         // workspace: [S], [S + 1], [S], [S], [P]
+};
+cudaError_t launch_pages_fork(const ForkParams& p, cudaStream_t stream);
+struct CompactParams {
+    const int32_t *table, *lens, *refs;
+    int32_t *table_out, *refs_out, *moved, *copies, *info;
+    int S, M, P, max_copies;
+    int32_t *src, *dst;             // workspace: [max_copies] each
+};
+cudaError_t launch_pages_compact(const CompactParams& p, cudaStream_t stream);
+constexpr int kCopyPools = 48;      // of one launch
+struct CopyPool {
+    uint8_t* ptr;                   // [pages][heads][64][row_bytes], strides in bytes
+    int64_t stride_page, stride_head, stride_row;
+    int heads, row_vecs;            // 16-byte vectors of a row
+};
+struct CopyParams {
+    CopyPool pool[kCopyPools];
+    const int32_t *copies, *count;  // [max_copies][3]; count: or null
+    int max_copies, P;
+};
+cudaError_t launch_pages_copy(const CopyParams& p, int pools, cudaStream_t stream);
+
 struct AddNormParams {
     const void* x;        // [M, N] bf16 or fp32 (x_f32)
     int x_f32;

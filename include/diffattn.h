@@ -462,6 +462,122 @@ diffattn_status diffattn_chunk_paged_fp8(diffattn_tensor q1, diffattn_tensor q2,
 diffattn_status diffattn_chunk_workspace_size(int T, int B, int H, int kv_group, int L, int d, int Dv, size_t* bytes);
 
 /*
+ * diffattn_beam_select — a step of beam search: the W best continuations of each sequence over its K beams
+ * and the vocabulary. A live beam k with logits x offers every token v with the score
+ *   s = scores[k] + x_v - log(sum_u exp(x_u)),  length n = lengths[k] + 1;
+ * a finished beam offers itself alone: token `eos`, s = scores[k], n = lengths[k]. Candidates are
+ * ranked by s / max(n, 1)^length_penalty; equal ranks go to the lowest beam, in a beam to the larger
+ * logit and then to the lowest token. (The source pages end at the model; this is what a served one
+ * answers with.)
+ *
+ * logits: [B, K, V], in_dtype f32, bf16 or f16; rows stride_b and stride_k elements apart, aligned to an
+ *   element. A logit of -inf or NaN is no candidate and adds nothing to the sum; +inf ones share the
+ *   probability. A row without any other logit offers nothing; neither does a beam of score -inf or NaN.
+ * scores: [B, K]; finished: uint8 [B, K] or NULL; lengths: int32 [B, K] or NULL (needed with a
+ *   length_penalty or lengths_out); eos: a token, or -1 for none (needed with finished and finished_out).
+ * scores_out, tokens, parents: [B, W], best first; parents in [0, K). finished_out (uint8) and
+ *   lengths_out: [B, W] or NULL: whether the continuation is finished (its beam was, or it took
+ *   `eos`), and its n. Places without a candidate hold score -inf, parent -1, token `eos` (0 without
+ *   one), finished 1 and length 0. With W = K the outputs may be the inputs' own arrays.
+ * 1 <= K <= 32, 1 <= W <= 64, W <= K V, V <= DIFFATTN_MAX_VOCABULARY, B <= 65535. B equal to 0: DIFFATTN_OK.
+ * Scores are formed and compared in 64 bits from fp32 sums of exponentials (each term within 2^-22 of
+ *   itself) and rounded once to fp32. Results do not depend on scheduling.
+ * workspace: diffattn_beam_workspace_size() bytes, 256-byte aligned, for one call at a time.
+ */
+#define DIFFATTN_MAX_VOCABULARY (1 << 22)
+diffattn_status diffattn_beam_select(const void* logits, int64_t stride_b, int64_t stride_k, int in_dtype,
+                                     const float* scores, const uint8_t* finished, const int32_t* lengths, int eos,
+                                     float length_penalty, int B, int K, int V, int W, float* scores_out,
+                                     int32_t* tokens, int32_t* parents, uint8_t* finished_out, int32_t* lengths_out,
+                                     void* workspace, size_t workspace_bytes, void* stream);
+diffattn_status diffattn_beam_workspace_size(int B, int K, int V, int W, size_t* bytes);
+
+/* Per-beam rows of one tensor [B K][parts][rows][row_bytes]: a contiguous cache has its heads as parts and its
+ * tokens as rows. Strides in bytes; with by_len only the first tokens of a beam are moved. */
+typedef struct {
+    void* ptr;
+    int64_t stride_state, stride_part, stride_row;
+    int parts, rows, row_bytes, by_len;
+} diffattn_beam_state;
+
+/*
+ * diffattn_beam_reorder — per-beam states take the rows of their parents, in place: the state of beam k of
+ * group b becomes what that of beam parents[b, k] was. A beam that is its own parent, or whose parent is
+ * outside [0, K), stays as it is. by_len states move the first lens[b K + parent] rows of each part (lens
+ * clamped to [0, rows]); what lies behind stays.
+ * states: HOST array of `count` descriptors, any alignment and type (moved in units of 16, 4, 2 or 1 bytes,
+ *   whatever address, strides and width allow); tensors must not overlap each other or themselves.
+ * parents: int32 [B, K]; lens: int32 [B K], or NULL without by_len states. 1 <= K <= 32, B <= 65535; B or count equal
+ * to 0: DIFFATTN_OK.
+ */
+diffattn_status diffattn_beam_reorder(const diffattn_beam_state* states, int count, const int32_t* parents,
+                                      const int32_t* lens, int B, int K, void* stream);
+
+/*
+ * diffattn_pages_fork — which pages of a paged cache the rows of a block table hold after they continue
+ * others, grow, roll back, start or end. The state is the table [B K, max_pages], the tokens of each row
+ * (a row holds its first ceil(lens / 64) entries) and of each page the number of its holders; a page
+ * with a count of 0 or less is free. Others than these rows (a kept prefix, another table) hold a page
+ * by one more in its count.
+ *
+ * Row i = b K + k continues row b K + parents[b, k] (parents NULL: itself; a parent outside [0, K) or
+ * done[i] != 0: no row). It keeps the first min(lens[parent], new) of its tokens, where new is
+ * new_lens[i], or without them lens[parent] + grow (0 without a parent; done rows: 0):
+ *   - whole pages are shared;
+ *   - a begun page (kept tokens not a multiple of 64) stays with the first row that keeps it, if it has no
+ *     other holder, and is listed in `copies` for the others: (page, new page, rows);
+ *   - further pages up to ceil(new / 64) are the lowest free ones, rows in order;
+ *   - what no row holds any more is free, for this very call.
+ * So rows end by done or new_lens 0, a prompt starts without a parent, drafted tokens are taken back by a
+ * smaller new_lens, and beams are reordered by the parents of diffattn_beam_select. After the call
+ * diffattn_pages_copy has to copy the begun pages, in every pool, before new tokens are appended.
+ * table_out [B K, max_pages] (entries beyond a row's pages: -1), lens_out, refs_out (never negative):
+ *   either apart from table, lens and refs, or the same arrays.
+ * copies: int32 [B K, 3], -1 behind the last; info: int32 [4]: copies, pages that could not be had
+ *   (pool or table full; their entries are -1, which appends skip and attention reads as zeros), free
+ *   pages and held pages after the call.
+ * Table entries outside [0, num_pages) hold nothing. B K <= 4096 (0: the counts and info alone).
+ * workspace: diffattn_pages_workspace_size(B K, num_pages) bytes, 256-byte aligned, for one call at a time.
+ */
+diffattn_status diffattn_pages_fork(const int32_t* table, const int32_t* lens, const int32_t* refs,
+                                    const int32_t* parents, const int32_t* new_lens, const uint8_t* done, int grow,
+                                    int32_t* table_out, int32_t* lens_out, int32_t* refs_out, int32_t* copies,
+                                    int32_t* info, int B, int K, int max_pages, int num_pages, void* workspace,
+                                    size_t workspace_bytes, void* stream);
+
+/*
+ * diffattn_pages_compact — the held pages moved to the front of the pool: the i-th highest held page goes
+ * to the i-th lowest free place before it, max_copies (<= num_pages / 2) of them at most. The table's
+ * rows and the counts follow; `moved` [num_pages] tells other holders each page's new place (-1: it was free).
+ * copies: int32 [max_copies, 3] for diffattn_pages_copy, -1 behind the last; info: int32 [4]: copies, 0, free and
+ *   held pages. table_out and refs_out as for diffattn_pages_fork (rows 0: the counts alone). Workspace:
+ *   diffattn_pages_workspace_size(rows, num_pages).
+ */
+diffattn_status diffattn_pages_compact(const int32_t* table, const int32_t* lens, const int32_t* refs,
+                                       int32_t* table_out, int32_t* refs_out, int32_t* moved, int32_t* copies,
+                                       int max_copies, int32_t* info, int rows, int max_pages, int num_pages,
+                                       void* workspace, size_t workspace_bytes, void* stream);
+diffattn_status diffattn_pages_workspace_size(int rows, int num_pages, size_t* bytes);
+
+/* One tensor of pages [num_pages][heads][64][row_bytes]: K1, K2 or V pages of a layer. Strides in bytes; address,
+ * strides and row_bytes multiples of 16. */
+typedef struct {
+    void* ptr;
+    int64_t stride_page, stride_head, stride_row;
+    int heads, row_bytes;
+} diffattn_page_pool;
+
+/*
+ * diffattn_pages_copy — pool[dst, :, :rows] = pool[src, :, :rows] for every entry (src, dst, rows) of
+ * `copies` (int32 [max_copies, 3], on the device) and every pool; rows is clamped to [0, 64], and entries
+ * with a page outside [0, num_pages) are skipped. n_copies: device int32, the entries to look at (the info
+ * of a plan), or NULL for all. No page may be written by two entries, or written by one and read by
+ * another. pools: HOST array of `count` descriptors. Pages that no entry writes stay as they are.
+ */
+diffattn_status diffattn_pages_copy(const diffattn_page_pool* pools, int count, const int32_t* copies,
+                                    const int32_t* n_copies, int max_copies, int num_pages, void* stream);
+
+/*
  * diffattn_bwd — gradients of diffattn_fwd (the backward pass). The pages train
  * DIFF Transformers ("Differential Transformer: Transformer que cancela ruído
  * de atenção", section "Eficiência e estabilidade de treinamento") but print no

@@ -1,0 +1,128 @@
+"""References of beam search's selection and of the page plans, written from their definitions in
+plain Python and float64 (no package code), one candidate, row and page after the other."""
+
+import math
+
+import torch
+
+PAGE = 64
+
+
+def select(logits, scores, width, finished=None, lengths=None, eos=None, penalty=0.0):
+    """Lists [B][width] of (score, token, parent, finished, length), best first."""
+    B, K, V = logits.shape
+    out = []
+    for b in range(B):
+        found = []
+        for k in range(K):
+            score, n = float(scores[b, k]), 0 if lengths is None else int(lengths[b, k])
+            if not score > -math.inf:
+                continue
+            if finished is not None and bool(finished[b, k]):
+                found.append((score / max(n, 1) ** penalty, -k, math.inf, 0, (score, eos, k, True, n)))
+                continue
+            x = logits[b, k].double()
+            x = torch.where(torch.isnan(x), -math.inf, x)
+            m = float(x.max())
+            if m == -math.inf:
+                continue
+            d = torch.where(x == m, 0.0, x - m)
+            s = score + (d - math.log(float(torch.exp(d).sum())))
+            some = torch.nonzero(s > -math.inf)[:, 0]
+            top = some[torch.argsort(x[some], descending=True, stable=True)[:width]]  # equal logits: lowest token first
+            for v in top.tolist():
+                rank = float(s[v]) / max(n + 1, 1) ** penalty
+                found.append((rank, -k, float(x[v]), -v, (float(s[v]), v, k, v == eos, n + 1)))
+        found.sort(key=lambda f: f[:4], reverse=True)
+        got = [f[4] for f in found[:width]]
+        out.append(got + [(-math.inf, 0 if eos is None else eos, -1, True, 0)] * (width - len(got)))
+    return out
+
+
+def pages(n):
+    return -(-n // PAGE)
+
+
+def fork(table, lens, refs, parents=None, grow=0, new_lens=None, done=None):
+    """(table, lens, refs, copies, info) as lists; parents [B][K] or None."""
+    S, M, P = len(table), len(table[0]) if table else 0, len(refs)
+    inside = lambda p: 0 <= p < P  # noqa: E731
+    refs, most = list(refs), M * PAGE
+    old = [min(max(n, 0), most) for n in lens]
+    for row, n in zip(table, old):
+        for p in row[:pages(n)]:
+            if inside(p):
+                refs[p] -= 1
+    K = len(parents[0]) if parents else 1
+    rows, over = [], 0
+    for i in range(S):
+        p = i if parents is None else parents[i // K][i % K]
+        if parents is not None:
+            p = i // K * K + p if 0 <= p < K else -1
+        ended = done is not None and done[i]
+        if ended:
+            p = -1
+        before = 0 if p < 0 else old[p]
+        new = 0 if ended else new_lens[i] if new_lens is not None else 0 if p < 0 else before + grow
+        new = max(new, 0)
+        over += pages(max(0, new - most))
+        new = min(new, most)
+        kept = min(before, new)
+        row = [q if inside(q) else -1 for q in table[p][:kept // PAGE]] if p >= 0 else []
+        for q in row:
+            if q >= 0:
+                refs[q] += 1
+        tail = table[p][kept // PAGE] if kept % PAGE else -1
+        rows.append([new, kept, row, tail if inside(tail) else -1, False])
+    seen = {}
+    for i, r in enumerate(rows):
+        if r[3] >= 0:
+            first = r[3] not in seen
+            seen.setdefault(r[3], refs[r[3]])
+            r[4] = first and seen[r[3]] <= 0
+    for r in rows:
+        if r[4]:
+            refs[r[3]] = 1
+            r[2].append(r[3])
+    refs = [max(r, 0) for r in refs]
+    free = [p for p in range(P) if refs[p] == 0]
+    copies, missing, out = [], over, []
+    for new, kept, row, tail, stays in rows:
+        begin = len(row)
+        while len(row) < pages(new):
+            row.append(free.pop(0) if free else -1)
+            if row[-1] < 0:
+                missing += 1
+            else:
+                refs[row[-1]] = 1
+        if tail >= 0 and not stays and row[begin] >= 0:
+            copies.append([tail, row[begin], kept % PAGE])
+        out.append(row + [-1] * (M - len(row)))
+    info = [len(copies), missing, len(free), P - len(free)]
+    return out, [r[0] for r in rows], refs, copies + [[-1] * 3] * (S - len(copies)), info
+
+
+def compact(table, lens, refs, most=None):
+    """(table, refs, copies, info, moved) as lists."""
+    P = len(refs)
+    most = P // 2 if most is None else most
+    refs = [max(r, 0) for r in refs]
+    used, free = [p for p in range(P) if refs[p]], [p for p in range(P) if not refs[p]]
+    moved, copies = [p if refs[p] else -1 for p in range(P)], []
+    for src, dst in list(zip(reversed(used), free))[:most]:
+        if dst > src:
+            break
+        moved[src], refs[dst], refs[src] = dst, refs[src], 0
+        copies.append([src, dst, PAGE])
+    table = [[moved[p] if c < pages(max(n, 0)) and 0 <= p < P else -1 for c, p in enumerate(row)] for row, n in zip(table, lens)]
+    return table, refs, copies + [[-1] * 3] * (most - len(copies)), [len(copies), 0, len(free), len(used)], moved
+
+
+def copied(pool, copies):
+    """A pool [P, H, 64, w] after the copies, from its bytes before them."""
+    bits = pool.clone().view(torch.uint8) if pool.element_size() == 1 else pool.clone().view(torch.int16)
+    old, P = bits.clone(), pool.shape[0]
+    for src, dst, rows in copies:
+        if 0 <= src < P and 0 <= dst < P:
+            bits[dst, :, :min(max(rows, 0), PAGE)] = old[src, :, :min(max(rows, 0), PAGE)]
+    return bits.view(pool.dtype)
