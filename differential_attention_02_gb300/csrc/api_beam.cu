@@ -18,18 +18,29 @@ bool workspace_ok(const void* ws, size_t bytes, size_t need) {
     return ws != nullptr && aligned(ws, 256) && bytes >= need;
 }
 
-// Workspace of the selection: control block, a row's best logits, its sum and its maximum.
+// Chunks of a row, and the workspace of the selection: control block, a chunk's best logits, its sum and its maximum.
 struct BeamLayout {
+    int chunks, chunk_segments;
     size_t keys, sums, maxima, total;
 };
 bool beam_layout(int B, int K, int V, int W, BeamLayout* l) {
     if (B < 0 || K < 1 || K > kMaxBeams || V < 1 || V > DIFFATTN_MAX_VOCABULARY || W < 1 || W > kMaxBeamWidth || B > 65535)
         return false;
     const size_t rows = (size_t)B * K;
+    // A row that begins inside a 16-byte vector has up to 7 places before it.
+    const int segments = (V + 7 + kBeamSegment - 1) / kBeamSegment;
+    int sms = 0;
+    if (device_sm_count(&sms) != cudaSuccess || sms < 1) sms = 152;
+    const int least = (segments + kBeamSegments - 1) / kBeamSegments;
+    const int room = kBeamMergeBytes / (8 * K * W) - 3;  // of the merge's shared memory: 9 at K W = 2048, of which 9 are needed
+    const int most = std::min({kBeamChunks, room, (segments + 31) / 32});
+    const int want = rows > 0 ? (int)std::min<size_t>(kBeamChunks, (8 * (size_t)sms + rows - 1) / rows) : 1;
+    l->chunk_segments = (segments + std::max(least, std::min(want, most)) - 1) / std::max(least, std::min(want, most));
+    l->chunks = (segments + l->chunk_segments - 1) / l->chunk_segments;
     l->keys = kControlBytes;
-    l->sums = l->keys + round256(rows * W * sizeof(uint64_t));
-    l->maxima = l->sums + round256(rows * sizeof(double));
-    l->total = l->maxima + round256(rows * sizeof(float));
+    l->sums = l->keys + round256(rows * l->chunks * W * sizeof(uint64_t));
+    l->maxima = l->sums + round256(rows * l->chunks * sizeof(double));
+    l->total = l->maxima + round256(rows * l->chunks * sizeof(float));
     return true;
 }
 
@@ -103,6 +114,8 @@ diffattn_status diffattn_beam_select(const void* logits, int64_t stride_b, int64
     p.parents = parents;
     p.finished_out = finished_out;
     p.lengths_out = lengths_out;
+    p.chunks = l.chunks;
+    p.chunk_segments = l.chunk_segments;
     p.keys = reinterpret_cast<uint64_t*>(ws + l.keys);
     p.sums = reinterpret_cast<double*>(ws + l.sums);
     p.maxima = reinterpret_cast<float*>(ws + l.maxima);

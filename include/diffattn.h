@@ -484,7 +484,7 @@ diffattn_status diffattn_chunk_workspace_size(int T, int B, int H, int kv_group,
  *   itself) and rounded once to fp32. Results do not depend on scheduling.
  * workspace: diffattn_beam_workspace_size() bytes, 256-byte aligned, for one call at a time.
  */
-#define DIFFATTN_MAX_VOCABULARY (1 << 22)
+#define DIFFATTN_MAX_VOCABULARY (1 << 20)
 diffattn_status diffattn_beam_select(const void* logits, int64_t stride_b, int64_t stride_k, int in_dtype,
                                      const float* scores, const uint8_t* finished, const int32_t* lengths, int eos,
                                      float length_penalty, int B, int K, int V, int W, float* scores_out,

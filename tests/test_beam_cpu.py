@@ -29,7 +29,7 @@ def _select(lib, **kw):
 
 def test_select_refusals(lib):
     assert _select(lib, B=0) == da.OK and _select(lib, B=0, fin=0x40000, eos=5, fo=0x41000, lens=0x42000, lo=0x43000, pen=1.0) == da.OK
-    for kw in (dict(B=-1), dict(K=0), dict(K=33), dict(V=0), dict(V=(1 << 22) + 1), dict(W=0), dict(W=65), dict(W=3, K=1, V=2), dict(B=65536),
+    for kw in (dict(B=-1), dict(K=0), dict(K=33), dict(V=0), dict(V=(1 << 20) + 1), dict(W=0), dict(W=65), dict(W=3, K=1, V=2), dict(B=65536),
                dict(dt=7), dict(eos=-2), dict(eos=1000), dict(fin=0x40000), dict(fo=0x40000), dict(pen=NAN), dict(pen=INF), dict(pen=0.5),
                dict(lo=0x40000), dict(logits=None), dict(logits=0x10001), dict(logits=0x10002, dt=da.F32), dict(scores=None),
                dict(scores=0x20002), dict(so=None), dict(tok=None), dict(par=None), dict(par=0x32001), dict(sb=-4), dict(sk=-4),
