@@ -31,7 +31,6 @@ namespace {
 constexpr int kThreads = 256;
 constexpr int kWarps = kThreads / 32;
 constexpr int kSegment = kBeamSegment;  // a warp's step, eight logits a lane
-constexpr int kPerLane = kBeamSegments / 32;
 
 // ---------------------------------------------------------------- logits as keys
 // Bits whose order as unsigned numbers is that of the values; above -inf's for every candidate.
@@ -137,9 +136,10 @@ constexpr float kLog2e = 1.44269504f;
 constexpr double kLog2eRest = 1.4426950408889634 - (double)kLog2e, kLn2 = 0.69314718055994531;
 
 __device__ __forceinline__ bool plain_max(float m) { return fabsf(m) < 0x1p20f; }
-__device__ __forceinline__ float term(float x, float m, float c, bool plain) {
-    if (plain) return fast_exp2(fmaf(x, kLog2e, -c));
-    return x == m ? 1.f : x < m ? fast_exp2((x - m) * kLog2e) : 0.f;  // (NaN: 0)
+// Any maximum, and logits with NaN among them (which count as nothing).
+__device__ __forceinline__ float any_term(float x, float m, float c) {
+    if (plain_max(m)) return x == x ? fast_exp2(fmaf(x, kLog2e, -c)) : 0.f;
+    return x == m ? 1.f : x < m ? fast_exp2((x - m) * kLog2e) : 0.f;
 }
 // The factor between two bases: maxima m (0 behind it: none yet) with their c.
 __device__ __forceinline__ float rebase(float from, float to) {
@@ -155,6 +155,45 @@ __device__ __forceinline__ float rebase(float from, float to) {
 // The base's logarithm: the sum is total * exp(base).
 __device__ __forceinline__ double base_log(float m) {
     return plain_max(m) ? kLn2 * (ceilf(m * kLog2e) + kLog2eRest * (double)m) : (double)m;
+}
+
+// The sum of a lane's four vectors where that takes care; rare, and out of the way of the instruction cache.
+template <typename T>
+__device__ __noinline__ float any_sum(const uint4* v, float m, float c) {
+    float t = 0.f;
+#pragma unroll 1
+    for (int i = 0; i < 4; ++i) {
+        float x[RowView<T>::kVec];
+        RowView<T>::unpack(v[i], x);
+        for (int j = 0; j < RowView<T>::kVec; ++j) t += any_term(x[j], m, c);
+    }
+    return t;
+}
+
+// One warp: the segments of the W largest maxima, equal ones in order, up to 32 N of them. Returns how many
+// there are, and the last one's maximum.
+template <int N>
+__device__ __forceinline__ int choose_segments(const uint32_t* best, int segments, int W, int lane, int* chosen, uint32_t* last) {
+    uint32_t mine[N], u = 0;
+    int at = 0;
+#pragma unroll
+    for (int i = 0; i < N; ++i) mine[i] = i * 32 + lane < segments ? best[i * 32 + lane] : 0;
+    int n = 0;
+    for (; n < W; ++n) {
+        u = 0;
+#pragma unroll
+        for (int i = N - 1; i >= 0; --i)
+            if (mine[i] >= u) u = mine[i], at = i * 32 + lane;
+        const uint32_t top = __reduce_max_sync(0xffffffffu, u);
+        if (top == 0) break;
+        const int segment = __reduce_min_sync(0xffffffffu, u == top ? at : INT_MAX);
+        *last = top;
+        if (lane == 0) chosen[n] = segment;
+#pragma unroll
+        for (int i = 0; i < N; ++i)
+            if (segment == i * 32 + lane) mine[i] = 0;
+    }
+    return n;
 }
 
 // One block per chunk of a row: its sum of exponentials and its W best logits.
@@ -201,20 +240,23 @@ __global__ void __launch_bounds__(kThreads) beam_rows_kernel(const __grid_consta
             m = now;
             c = ceilf(m * kLog2e);
         }
-        const bool plain = plain_max(m);
+        float t = NAN;
+        if (plain_max(m)) {
+            float2 t2 = make_float2(0.f, 0.f);
 #pragma unroll
-        for (int i = 0; i < 4; ++i) {
-            float x[View::kVec], t = 0.f;
-            View::unpack(v[i], x);
+            for (int i = 0; i < 4; ++i) {
+                float x[View::kVec];
+                View::unpack(v[i], x);
 #pragma unroll
-            for (int j = 0; j < View::kVec; ++j) t += term(x[j], m, c, plain);
-            if (t != t) {  // NaN among them
-                t = 0.f;
-#pragma unroll
-                for (int j = 0; j < View::kVec; ++j) t += x[j] == x[j] ? term(x[j], m, c, plain) : 0.f;
+                for (int j = 0; j < View::kVec; j += 2) {
+                    const float2 y = __ffma2_rn(make_float2(x[j], x[j + 1]), make_float2(kLog2e, kLog2e), make_float2(-c, -c));
+                    t2 = __fadd2_rn(t2, make_float2(fast_exp2(y.x), fast_exp2(y.y)));
+                }
             }
-            sum += t;
+            t = t2.x + t2.y;
         }
+        if (t != t) t = any_sum<T>(v, m, c);
+        sum += t;
     }
     double total = sum;
 #pragma unroll
@@ -227,33 +269,10 @@ __global__ void __launch_bounds__(kThreads) beam_rows_kernel(const __grid_consta
 
     const int64_t out = (int64_t)row * p.chunks + chunk;
     if (warp == 0) {
-        // the segments of the W largest maxima, one after the other
-        uint32_t mine[kPerLane], u = 0;
-        int at = 0;
-#pragma unroll
-        for (int i = 0; i < kPerLane; ++i) mine[i] = i * 32 + lane < segments ? best[i * 32 + lane] : 0;
-        auto local = [&] {
-            u = 0;
-#pragma unroll
-            for (int i = 0; i < kPerLane; ++i)
-                if (mine[i] > u) u = mine[i], at = i;
-        };
-        local();
-        int n = 0;
         uint32_t last = 0;
-        for (; n < p.W; ++n) {
-            const uint32_t top = __reduce_max_sync(0xffffffffu, u);
-            if (top == 0) break;
-            const int segment = __reduce_min_sync(0xffffffffu, u == top ? at * 32 + lane : INT_MAX);
-            last = top;
-            if (lane == 0) chosen[n] = segment;
-            if (segment % 32 == lane) {
-#pragma unroll
-                for (int i = 0; i < kPerLane; ++i)
-                    if (segment / 32 == i) mine[i] = 0;
-                local();
-            }
-        }
+        const int n = segments <= 128   ? choose_segments<4>(best, segments, p.W, lane, chosen, &last)
+                      : segments <= 256 ? choose_segments<8>(best, segments, p.W, lane, chosen, &last)
+                                        : choose_segments<kBeamSegments / 32>(best, segments, p.W, lane, chosen, &last);
         if (lane == 0) {
             n_chosen = n;
             least = n == p.W ? last : 1;  // a logit below the last chosen maximum is not among the W best
@@ -283,22 +302,23 @@ __global__ void __launch_bounds__(kThreads) beam_rows_kernel(const __grid_consta
 #pragma unroll
             for (int j = 0; j < View::kVec; ++j) x[i * View::kVec + j] = candidate(f[j]);
         }
+        // a token's place in the segment, for the lane's j-th logit
+        const auto place = [lane](int j) { return (j / View::kVec * 32 + lane) * View::kVec + j % View::kVec; };
         int n = 0;
         for (; n < p.W; ++n) {
-            uint64_t key = 0;  // of the lane's best
+            uint32_t u = 0;
 #pragma unroll
-            for (int j = 0; j < 8; ++j) {
-                const uint64_t k = make_key(x[j], View::position(segment, lane, j / View::kVec) + j % View::kVec - view.off);
-                key = k > key ? k : key;
-            }
-            const uint64_t top = warp_max_key(key);
-            if ((uint32_t)(top >> 32) < least) break;
-            if (lane == 0) lists[w * p.W + n] = top;
-            if (key == top) {
+            for (int j = 0; j < 8; ++j) u = max(u, x[j]);
+            const uint32_t top = __reduce_max_sync(0xffffffffu, u);
+            if (top < least) break;
+            int at = kSegment;
 #pragma unroll
-                for (int j = 0; j < 8; ++j)
-                    if (View::position(segment, lane, j / View::kVec) + j % View::kVec - view.off == key_token(top)) x[j] = 0;
-            }
+            for (int j = 7; j >= 0; --j) at = x[j] == top ? place(j) : at;
+            at = __reduce_min_sync(0xffffffffu, at);
+            if (lane == 0) lists[w * p.W + n] = make_key(top, segment * kSegment + at - view.off);
+#pragma unroll
+            for (int j = 0; j < 8; ++j)
+                if (place(j) == at) x[j] = 0;
         }
         if (lane == 0 && n < p.W) lists[w * p.W + n] = 0;
     }
