@@ -20,26 +20,29 @@ bool workspace_ok(const void* ws, size_t bytes, size_t need) {
 
 // Chunks of a row, and the workspace of the selection: control block, a chunk's best logits, its sum and its maximum.
 struct BeamLayout {
-    int chunks, chunk_segments;
+    int chunks, chunk_rounds, wide;
     size_t keys, sums, maxima, total;
 };
-bool beam_layout(int B, int K, int V, int W, BeamLayout* l) {
+bool beam_layout(int B, int K, int V, int W, int in_dtype, BeamLayout* l) {
     if (B < 0 || K < 1 || K > kMaxBeams || V < 1 || V > DIFFATTN_MAX_VOCABULARY || W < 1 || W > kMaxBeamWidth || B > 65535)
         return false;
     const size_t rows = (size_t)B * K;
     // A row that begins inside a 16-byte vector has up to 7 places before it.
-    const int segments = (V + 7 + kBeamSegment - 1) / kBeamSegment;
+    const int round = kBeamRoundBytes / (in_dtype == DIFFATTN_F32 ? 4 : 2), parts = round / kBeamSegment;
+    const int rounds = (V + 7 + round - 1) / round;
     int sms = 0;
     if (device_sm_count(&sms) != cudaSuccess || sms < 1) sms = 152;
-    const int least = (segments + kBeamSegments - 1) / kBeamSegments;
+    const int least = (rounds * parts + kBeamSegments - 1) / kBeamSegments;
     const int room = kBeamMergeBytes / (8 * K * W) - 3;  // of the merge's shared memory: 9 at K W = 2048, of which 9 are needed
-    const int most = std::min({kBeamChunks, room, (segments + 31) / 32});
-    const int want = rows > 0 ? (int)std::min<size_t>(kBeamChunks, (8 * (size_t)sms + rows - 1) / rows) : 1;
-    l->chunk_segments = (segments + std::max(least, std::min(want, most)) - 1) / std::max(least, std::min(want, most));
-    l->chunks = (segments + l->chunk_segments - 1) / l->chunk_segments;
+    const int most = std::min({kBeamChunks, room, (rounds + 7) / 8});
+    const int want = rows > 0 ? (int)std::min<size_t>(kBeamChunks, (2 * (size_t)sms + rows - 1) / rows) : 1;
+    const int chunks = std::max(least, std::min(want, most));
+    l->chunk_rounds = (rounds + chunks - 1) / chunks;
+    l->chunks = (rounds + l->chunk_rounds - 1) / l->chunk_rounds;
+    l->wide = l->chunk_rounds >= 2 * W;
     l->keys = kControlBytes;
     l->sums = l->keys + round256(rows * l->chunks * W * sizeof(uint64_t));
-    l->maxima = l->sums + round256(rows * l->chunks * sizeof(double));
+    l->maxima = l->sums + round256(rows * l->chunks * sizeof(uint64_t));
     l->total = l->maxima + round256(rows * l->chunks * sizeof(float));
     return true;
 }
@@ -74,9 +77,10 @@ bool apart_or_same(const void* a, const void* b, int64_t n) {
 extern "C" {
 
 diffattn_status diffattn_beam_workspace_size(int B, int K, int V, int W, size_t* bytes) {
-    BeamLayout l;
-    if (!bytes || !beam_layout(B, K, V, W, &l)) return DIFFATTN_ERR_INVALID_ARG;
-    *bytes = l.total;
+    BeamLayout wide, narrow;
+    if (!bytes || !beam_layout(B, K, V, W, DIFFATTN_F32, &wide) || !beam_layout(B, K, V, W, DIFFATTN_BF16, &narrow))
+        return DIFFATTN_ERR_INVALID_ARG;
+    *bytes = std::max(wide.total, narrow.total);
     return DIFFATTN_OK;
 }
 
@@ -86,7 +90,7 @@ diffattn_status diffattn_beam_select(const void* logits, int64_t stride_b, int64
                                      int32_t* tokens, int32_t* parents, uint8_t* finished_out, int32_t* lengths_out,
                                      void* workspace, size_t workspace_bytes, void* stream) {
     BeamLayout l;
-    if (!beam_layout(B, K, V, W, &l) || W > (int64_t)K * V) return DIFFATTN_ERR_INVALID_ARG;
+    if (!beam_layout(B, K, V, W, in_dtype, &l) || W > (int64_t)K * V) return DIFFATTN_ERR_INVALID_ARG;
     if (in_dtype != DIFFATTN_F32 && in_dtype != DIFFATTN_BF16 && in_dtype != DIFFATTN_F16) return DIFFATTN_ERR_INVALID_ARG;
     if (eos < -1 || eos >= V || ((finished || finished_out) && eos < 0) || !std::isfinite(length_penalty) ||
         ((length_penalty != 0.f || lengths_out) && !lengths))
@@ -115,9 +119,10 @@ diffattn_status diffattn_beam_select(const void* logits, int64_t stride_b, int64
     p.finished_out = finished_out;
     p.lengths_out = lengths_out;
     p.chunks = l.chunks;
-    p.chunk_segments = l.chunk_segments;
+    p.chunk_rounds = l.chunk_rounds;
+    p.wide = l.wide;
     p.keys = reinterpret_cast<uint64_t*>(ws + l.keys);
-    p.sums = reinterpret_cast<double*>(ws + l.sums);
+    p.sums = reinterpret_cast<uint64_t*>(ws + l.sums);
     p.maxima = reinterpret_cast<float*>(ws + l.maxima);
     return cuda_status(launch_beam_select(p, in_dtype == DIFFATTN_F32 ? 0 : in_dtype == DIFFATTN_BF16 ? 1 : 2,
                                           static_cast<cudaStream_t>(stream)));

@@ -7,16 +7,16 @@
 // their length n. Within a beam the ranking is that of the logits, so a row only has to
 // give its W best logits, its maximum and its sum; the beams' lists are then merged.
 //
-// The sum's terms are fp32, each within 2^-22 of itself; partial sums are joined in 64
+// The sum's terms are fp32, each within 2^-22 of itself; lanes' sums are joined in 64
 // bits, and scores are formed and compared in 64 bits, so that the order of two
 // candidates of different beams does not hang on fp32's rounding of sums near -50.
 //
-// A row is read once. Blocks share a row in chunks; a warp reads segments of 256 logits,
-// adds their exponentials and keeps each segment's maximum. The W best logits of a chunk
-// lie in the W segments of the largest maxima (equal ones in order): any other segment has
-// W segments before it that each hold a logit to be preferred. So the selection looks at
-// the maxima, reads W segments once more (from L2), and its time does not hang on the
-// order of the logits.
+// A row is read once. Blocks share a row in chunks; a warp reads a round of four vectors
+// a lane, adds the exponentials and keeps the maximum of each segment (256 logits, or
+// the whole round where the chunk has many). The W best logits of a chunk lie in the W
+// segments of the largest maxima (equal ones in order): any other segment has W segments
+// before it that each hold a logit to be preferred. So the selection looks at the maxima,
+// and reads W segments once more (from L2).
 #include <limits.h>
 #include <math.h>
 
@@ -30,7 +30,8 @@ namespace {
 
 constexpr int kThreads = 256;
 constexpr int kWarps = kThreads / 32;
-constexpr int kSegment = kBeamSegment;  // a warp's step, eight logits a lane
+constexpr int kSegment = kBeamSegment;  // eight logits a lane
+constexpr int kFound = 512;             // logits that a chunk's selection compares with one another
 
 // ---------------------------------------------------------------- logits as keys
 // Bits whose order as unsigned numbers is that of the values; above -inf's for every candidate.
@@ -61,6 +62,7 @@ template <typename T>
 struct RowView {
     static constexpr int kVec = 16 / sizeof(T);  // logits of a vector
     static constexpr int kLoads = 8 / kVec;      // vectors of a lane in a segment
+    static constexpr int kRound = 4 * 32 * kVec; // logits of a warp's round
     const T* base;
     int off, end;
 
@@ -69,13 +71,15 @@ struct RowView {
         base = row - off;
         end = off + V;
     }
-    __device__ __forceinline__ static int position(int segment, int lane, int load) {
-        return segment * kSegment + (load * 32 + lane) * kVec;
+    __device__ __forceinline__ uint4 load_whole(int at) const {
+        uint4 v;
+        asm("ld.global.nc.v4.u32 {%0, %1, %2, %3}, [%4];" : "=r"(v.x), "=r"(v.y), "=r"(v.z), "=r"(v.w) : "l"(base + at));
+        return v;
     }
     __device__ __forceinline__ uint4 load(int at) const {
         uint4 v;
         if (at >= off && at + kVec <= end) {
-            asm("ld.global.nc.v4.u32 {%0, %1, %2, %3}, [%4];" : "=r"(v.x), "=r"(v.y), "=r"(v.z), "=r"(v.w) : "l"(base + at));
+            v = load_whole(at);
         } else {
             uint32_t w[4];
 #pragma unroll
@@ -141,45 +145,115 @@ __device__ __forceinline__ float any_term(float x, float m, float c) {
     if (plain_max(m)) return x == x ? fast_exp2(fmaf(x, kLog2e, -c)) : 0.f;
     return x == m ? 1.f : x < m ? fast_exp2((x - m) * kLog2e) : 0.f;
 }
-// The factor between two bases: maxima m (0 behind it: none yet) with their c.
-__device__ __forceinline__ float rebase(float from, float to) {
-    if (from == -INFINITY) return 0.f;
-    if (plain_max(from) && plain_max(to)) {
-        const float power = ceilf(from * kLog2e) - ceilf(to * kLog2e);  // not above 0
-        return power < -126.f ? 0.f : __int_as_float(((int)power + 127) << 23);
-    }
-    const double a = plain_max(from) ? kLn2 * ceilf(from * kLog2e) : (double)from;
-    const double b = plain_max(to) ? kLn2 * ceilf(to * kLog2e) : (double)to;
-    return (float)exp(a - b);
-}
+// 2^n for a whole n <= 0.
+__device__ __forceinline__ float power_of_two(float n) { return n < -126.f ? 0.f : __int_as_float(((int)n + 127) << 23); }
+__device__ __forceinline__ float whole_base(float m) { return ceilf(m * kLog2e); }
 // The base's logarithm: the sum is total * exp(base).
 __device__ __forceinline__ double base_log(float m) {
-    return plain_max(m) ? kLn2 * (ceilf(m * kLog2e) + kLog2eRest * (double)m) : (double)m;
+    return plain_max(m) ? kLn2 * (whole_base(m) + kLog2eRest * (double)m) : (double)m;
+}
+__device__ __noinline__ float any_rebase(float from, float to) {
+    const double a = plain_max(from) ? kLn2 * whole_base(from) : (double)from, b = plain_max(to) ? kLn2 * whole_base(to) : (double)to;
+    return (float)exp(a - b);
+}
+// The factor of a sum that changes from one maximum's base to a larger one's.
+__device__ __forceinline__ float rebase(float from, float to) {
+    if (from == to) return 1.f;
+    if (from == -INFINITY) return 0.f;
+    if (plain_max(from) && plain_max(to)) return power_of_two(whole_base(from) - whole_base(to));
+    return any_rebase(from, to);
+}
+// Sums of lanes, warps and chunks are whole numbers of 2^-40 (the largest term is half at least, and 2^20 terms
+// leave room in 64 bits): exact in any order, and without the 64-bit floating point unit, of which this GPU has two
+// lanes an SM.
+constexpr float kFixed = 0x1p40f;
+__device__ __forceinline__ uint64_t to_fixed(float sum) { return __float2ull_rn(sum * kFixed); }
+__device__ __forceinline__ uint64_t rebase_fixed(uint64_t sum, float from, float to) {
+    if (from == to) return sum;
+    if (from == -INFINITY) return 0;
+    if (plain_max(from) && plain_max(to)) {
+        const float power = whole_base(to) - whole_base(from);
+        return power > 63.f ? 0 : sum >> (int)power;
+    }
+    return __float2ull_rn(__ull2float_rn(sum) * any_rebase(from, to));
+}
+__device__ __forceinline__ uint64_t warp_sum_fixed(uint64_t v) {
+#pragma unroll
+    for (int o = 16; o > 0; o >>= 1) v += __shfl_xor_sync(0xffffffffu, v, o);
+    return v;
 }
 
-// The sum of a lane's four vectors where that takes care; rare, and out of the way of the instruction cache.
+// The sum of a vector's terms where that takes care; rare, and out of the way of the instruction cache. (By value: an
+// array's address would keep the round's vectors in local memory.)
 template <typename T>
-__device__ __noinline__ float any_sum(const uint4* v, float m, float c) {
-    float t = 0.f;
-#pragma unroll 1
-    for (int i = 0; i < 4; ++i) {
-        float x[RowView<T>::kVec];
-        RowView<T>::unpack(v[i], x);
-        for (int j = 0; j < RowView<T>::kVec; ++j) t += any_term(x[j], m, c);
-    }
+__device__ __noinline__ float any_sum(uint4 v, float m, float c) {
+    float x[RowView<T>::kVec], t = 0.f;
+    RowView<T>::unpack(v, x);
+#pragma unroll
+    for (int j = 0; j < RowView<T>::kVec; ++j) t += any_term(x[j], m, c);
     return t;
 }
 
-// One warp: the segments of the W largest maxima, equal ones in order, up to 32 N of them. Returns how many
-// there are, and the last one's maximum.
+// ---------------------------------------------------------------- the W largest of a few keys
+// Keys apart from each other, in shared memory, in any order: the place of each is the number of larger ones.
+// No step waits for the one before, so that 16 of 30 keys take a fifth of the time of 16 maxima one after
+// the other; beyond 64 keys a warp leaves it to those.
+constexpr int kCounted = 64;
+__device__ __forceinline__ void warp_place(const uint64_t* keys, int n, int W, int lane, uint64_t* out) {
+    const uint64_t a = lane < n ? keys[lane] : 0, b = lane + 32 < n ? keys[lane + 32] : 0;
+    int at = 0, bt = 0;
+#pragma unroll 4
+    for (int j = 0; j < n; ++j) {
+        const uint64_t k = keys[j];
+        at += k > a;
+        bt += k > b;
+    }
+    if (lane < n && at < W) out[at] = a;
+    if (lane + 32 < n && bt < W) out[bt] = b;
+    for (int i = n + lane; i < W; i += 32) out[i] = 0;
+}
+
+// One warp: the segments of the W largest maxima, equal ones in order, of up to 32 N. Returns how many there
+// are, and the last one's maximum. The W-th of the lanes' own maxima is a bound that W segments reach, and
+// few more do; where they are too many (equal maxima), or W more than the lanes, one is taken after the other.
 template <int N>
-__device__ __forceinline__ int choose_segments(const uint32_t* best, int segments, int W, int lane, int* chosen, uint32_t* last) {
-    uint32_t mine[N], u = 0;
-    int at = 0;
+__device__ __forceinline__ int choose_segments(const uint32_t* best, int segments, int W, int lane, uint64_t* few, uint64_t* sorted,
+                                               int* chosen, uint32_t* last) {
+    uint32_t mine[N];
 #pragma unroll
     for (int i = 0; i < N; ++i) mine[i] = i * 32 + lane < segments ? best[i * 32 + lane] : 0;
+    uint32_t u = 0;
+#pragma unroll
+    for (int i = 0; i < N; ++i) u = max(u, mine[i]);
+    if (W <= 32) {
+        int larger = 0;
+#pragma unroll
+        for (int j = 0; j < 32; ++j) {
+            const uint32_t k = __shfl_sync(0xffffffffu, u, j);
+            larger += k > u || (k == u && j < lane);
+        }
+        const uint32_t bound = max(__shfl_sync(0xffffffffu, u, __ffs(__ballot_sync(0xffffffffu, larger == W - 1)) - 1), 1u);
+        int n = 0;
+#pragma unroll
+        for (int i = 0; i < N; ++i) {
+            const uint32_t hit = __ballot_sync(0xffffffffu, mine[i] >= bound);
+            const int at = n + __popc(hit & ((1u << lane) - 1));
+            if (mine[i] >= bound && at < kCounted) few[at] = make_key(mine[i], i * 32 + lane);
+            n += __popc(hit);
+        }
+        __syncwarp();
+        if (n <= kCounted) {
+            warp_place(few, n, W, lane, sorted);
+            __syncwarp();
+            n = min(n, W);
+            if (lane < n) chosen[lane] = key_token(sorted[lane]);
+            *last = n > 0 ? (uint32_t)(sorted[n - 1] >> 32) : 0;
+            return n;
+        }
+    }
     int n = 0;
     for (; n < W; ++n) {
+        int at = 0;
         u = 0;
 #pragma unroll
         for (int i = N - 1; i >= 0; --i)
@@ -196,49 +270,64 @@ __device__ __forceinline__ int choose_segments(const uint32_t* best, int segment
     return n;
 }
 
-// One block per chunk of a row: its sum of exponentials and its W best logits.
-template <typename T>
-__global__ void __launch_bounds__(kThreads) beam_rows_kernel(const __grid_constant__ BeamParams p) {
+// One block per chunk of a row: its sum of exponentials and its W best logits. WIDE: a segment is a whole round.
+template <typename T, bool WIDE>
+__global__ void __launch_bounds__(kThreads, 4) beam_rows_kernel(const __grid_constant__ BeamParams p) {
     using View = RowView<T>;
-    constexpr int kStep = 4 / View::kLoads;  // segments of a warp's round: four vectors a lane in flight
-    __shared__ uint32_t best[kBeamSegments];  // a segment's largest logit
-    __shared__ double sums[kWarps];
+    constexpr int kParts = View::kRound / kSegment;   // pieces of 256 logits of a round
+    __shared__ uint32_t best[kBeamSegments];          // a segment's largest logit
+    __shared__ uint64_t sums[kWarps];
     __shared__ float maxima[kWarps];
     __shared__ int chosen[kMaxBeamWidth];
-    __shared__ int n_chosen;
+    __shared__ int n_chosen, n_above, n_found;
     __shared__ uint32_t least;
-    extern __shared__ uint64_t lists[];  // [W][W]: the best of each chosen segment
+    __shared__ uint64_t found[kFound];                // logits that may be among the W best
     const int row = blockIdx.x / p.chunks, chunk = blockIdx.x % p.chunks;
     const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
-    pdl_trigger();
     if (p.finished && p.finished[row]) return;
     const View view(static_cast<const T*>(p.logits) + row / p.K * p.stride_b + row % p.K * p.stride_k, p.V);
-    const int first = chunk * p.chunk_segments;
-    const int segments = min(p.chunk_segments, (view.end + kSegment - 1) / kSegment - first);  // may be none
+    const int begin = chunk * p.chunk_rounds * View::kRound;
+    const int rounds = min(p.chunk_rounds, (view.end - begin + View::kRound - 1) / View::kRound);  // may be none
 
     float m = -INFINITY, c = 0.f, sum = 0.f;
-    for (int s = warp * kStep; s < segments; s += kWarps * kStep) {
+    const auto load = [&](int r, uint4* v) {
+        const int at = begin + r * View::kRound + lane * View::kVec;
+        if (begin + r * View::kRound >= view.off && begin + (r + 1) * View::kRound <= view.end) {
+#pragma unroll
+            for (int i = 0; i < 4; ++i) v[i] = view.load_whole(at + i * 32 * View::kVec);
+        } else {
+#pragma unroll
+            for (int i = 0; i < 4; ++i) v[i] = view.load(at + i * 32 * View::kVec);
+        }
+    };
+    uint4 next[4];
+    if (warp < rounds) load(warp, next);
+    for (int r = warp; r < rounds; r += kWarps) {
         uint4 v[4];
 #pragma unroll
-        for (int i = 0; i < 4; ++i) {
-            const int segment = s + i / View::kLoads;  // one behind the chunk's last reads as nothing
-            v[i] = view.load(segment < segments ? View::position(first + segment, lane, i % View::kLoads) : view.end);
-        }
+        for (int i = 0; i < 4; ++i) v[i] = next[i];
+        if (r + kWarps < rounds) load(r + kWarps, next);  // the next round's are on their way
         uint32_t top = 0;
+        if constexpr (WIDE) {
+            const float x = fmaxf(fmaxf(View::largest(v[0]), View::largest(v[1])), fmaxf(View::largest(v[2]), View::largest(v[3])));
+            top = __reduce_max_sync(0xffffffffu, candidate(x));
+            if (lane == 0) best[r] = top;
+        } else {
 #pragma unroll
-        for (int i = 0; i < kStep; ++i) {
-            float x = View::largest(v[i * View::kLoads]);
-            if (View::kLoads == 2) x = fmaxf(x, View::largest(v[i * View::kLoads + 1]));
-            const uint32_t u = __reduce_max_sync(0xffffffffu, candidate(x));
-            if (lane == 0 && s + i < segments) best[s + i] = u;
-            top = max(top, u);
+            for (int i = 0; i < kParts; ++i) {
+                float x = View::largest(v[i * View::kLoads]);
+                if (View::kLoads == 2) x = fmaxf(x, View::largest(v[i * View::kLoads + 1]));
+                const uint32_t u = __reduce_max_sync(0xffffffffu, candidate(x));
+                if (lane == 0) best[r * kParts + i] = u;
+                top = max(top, u);
+            }
         }
         if (top == 0) continue;
         const float now = key_logit((uint64_t)top << 32);
         if (now > m) {
             sum *= rebase(m, now);
             m = now;
-            c = ceilf(m * kLog2e);
+            c = whole_base(m);
         }
         float t = NAN;
         if (plain_max(m)) {
@@ -255,12 +344,10 @@ __global__ void __launch_bounds__(kThreads) beam_rows_kernel(const __grid_consta
             }
             t = t2.x + t2.y;
         }
-        if (t != t) t = any_sum<T>(v, m, c);
+        if (t != t) t = any_sum<T>(v[0], m, c) + any_sum<T>(v[1], m, c) + (any_sum<T>(v[2], m, c) + any_sum<T>(v[3], m, c));
         sum += t;
     }
-    double total = sum;
-#pragma unroll
-    for (int o = 16; o > 0; o >>= 1) total += __shfl_xor_sync(0xffffffffu, total, o);
+    const uint64_t total = warp_sum_fixed(to_fixed(sum));
     if (lane == 0) {
         sums[warp] = total;
         maxima[warp] = m;
@@ -269,21 +356,26 @@ __global__ void __launch_bounds__(kThreads) beam_rows_kernel(const __grid_consta
 
     const int64_t out = (int64_t)row * p.chunks + chunk;
     if (warp == 0) {
+        const int segments = max(rounds, 0) * (WIDE ? 1 : kParts);
         uint32_t last = 0;
-        const int n = segments <= 128   ? choose_segments<4>(best, segments, p.W, lane, chosen, &last)
-                      : segments <= 256 ? choose_segments<8>(best, segments, p.W, lane, chosen, &last)
-                                        : choose_segments<kBeamSegments / 32>(best, segments, p.W, lane, chosen, &last);
+        uint64_t* sorted = found + kCounted;
+        const int n = segments <= 128   ? choose_segments<4>(best, segments, p.W, lane, found, sorted, chosen, &last)
+                      : segments <= 256 ? choose_segments<8>(best, segments, p.W, lane, found, sorted, chosen, &last)
+                                        : choose_segments<kBeamSegments / 32>(best, segments, p.W, lane, found, sorted, chosen, &last);
+        __syncwarp();
+        const uint32_t bound = n == p.W ? last : 1;  // a logit below the last chosen maximum is not among the W best
+        int above = 0;
+        for (int i = lane; i < n; i += 32) above += best[chosen[i]] > bound;
+        above = __reduce_add_sync(0xffffffffu, above);
         if (lane == 0) {
             n_chosen = n;
-            least = n == p.W ? last : 1;  // a logit below the last chosen maximum is not among the W best
+            n_above = above;
+            n_found = 0;
+            least = bound;
         }
     } else if (warp == 1) {
-        float top = lane < kWarps ? maxima[lane] : -INFINITY;
-        const float mine = top;
-        top = warp_max(top);
-        double s = lane < kWarps && mine > -INFINITY ? sums[lane] * (mine == top ? 1. : exp(base_log(mine) - base_log(top))) : 0.;
-#pragma unroll
-        for (int o = 4; o > 0; o >>= 1) s += __shfl_xor_sync(0xffffffffu, s, o);
+        const float mine = lane < kWarps ? maxima[lane] : -INFINITY, top = warp_max(mine);
+        const uint64_t s = warp_sum_fixed(lane < kWarps ? rebase_fixed(sums[lane], mine, top) : 0);
         if (lane == 0) {
             p.sums[out] = s;
             p.maxima[out] = top;
@@ -291,55 +383,140 @@ __global__ void __launch_bounds__(kThreads) beam_rows_kernel(const __grid_consta
     }
     __syncthreads();
 
-    // A warp per chosen segment: its logits that may be among the W best, best first.
+    // The chosen segments' logits that may be among the W best, collected by a warp each.
+    const uint32_t bound = least;
+    constexpr int kVecs = WIDE ? 4 : View::kLoads;  // vectors of a lane in a segment
+    const auto vector_at = [&](int w, int i) { return begin + (chosen[w] * kVecs + i) * 32 * View::kVec + lane * View::kVec; };
     for (int w = warp; w < n_chosen; w += kWarps) {
-        uint32_t x[8];
-        const int segment = first + chosen[w];
+        // Of those that equal the bound (many, where a mask leaves few others) the lowest W - n_above tokens are enough,
+        // one less for each earlier segment that has such alone.
+        int left = p.W - n_above - max(0, w - n_above);
+        uint4 v[kVecs];
 #pragma unroll
-        for (int i = 0; i < View::kLoads; ++i) {
+        for (int i = 0; i < kVecs; ++i) v[i] = view.load(vector_at(w, i));
+#pragma unroll
+        for (int i = 0; i < kVecs; ++i) {
+            if (!__any_sync(0xffffffffu, candidate(View::largest(v[i])) >= bound)) continue;
             float f[View::kVec];
-            View::unpack(view.load(View::position(segment, lane, i)), f);
+            View::unpack(v[i], f);
+            const int token = vector_at(w, i) - view.off;  // of the lane's first logit
+            uint32_t same = 0;
 #pragma unroll
-            for (int j = 0; j < View::kVec; ++j) x[i * View::kVec + j] = candidate(f[j]);
+            for (int j = 0; j < View::kVec; ++j) {
+                const uint32_t x = candidate(f[j]);
+                same |= (x == bound) << j;
+                if (x > bound) {
+                    const int to = atomicAdd(&n_found, 1);  // in any order
+                    if (to < kFound) found[to] = make_key(x, token + j);
+                }
+            }
+            if (left <= 0 || !__any_sync(0xffffffffu, same)) continue;
+            int before = __popc(same);
+#pragma unroll
+            for (int o = 1; o < 32; o <<= 1) {
+                const int y = __shfl_up_sync(0xffffffffu, before, o);
+                if (lane >= o) before += y;
+            }
+            const int all = __shfl_sync(0xffffffffu, before, 31);
+            before -= __popc(same);
+            for (; same && before < left; same &= same - 1, ++before) {
+                const int to = atomicAdd(&n_found, 1);
+                if (to < kFound) found[to] = make_key(bound, token + __ffs(same) - 1);
+            }
+            left -= all;
         }
-        // a token's place in the segment, for the lane's j-th logit
-        const auto place = [lane](int j) { return (j / View::kVec * 32 + lane) * View::kVec + j % View::kVec; };
-        int n = 0;
-        for (; n < p.W; ++n) {
-            uint32_t u = 0;
-#pragma unroll
-            for (int j = 0; j < 8; ++j) u = max(u, x[j]);
-            const uint32_t top = __reduce_max_sync(0xffffffffu, u);
-            if (top < least) break;
-            int at = kSegment;
-#pragma unroll
-            for (int j = 7; j >= 0; --j) at = x[j] == top ? place(j) : at;
-            at = __reduce_min_sync(0xffffffffu, at);
-            if (lane == 0) lists[w * p.W + n] = make_key(top, segment * kSegment + at - view.off);
-#pragma unroll
-            for (int j = 0; j < 8; ++j)
-                if (place(j) == at) x[j] = 0;
-        }
-        if (lane == 0 && n < p.W) lists[w * p.W + n] = 0;
     }
     __syncthreads();
-    if (warp == 0) {  // the segments' lists, two to a lane, into one
-        int at[2] = {0, 0};
-        uint64_t head[2];
-#pragma unroll
-        for (int i = 0; i < 2; ++i) head[i] = i * 32 + lane < n_chosen ? lists[(i * 32 + lane) * p.W] : 0;
-        for (int w = 0; w < p.W; ++w) {
-            const uint64_t top = warp_max_key(max(head[0], head[1]));
-            if (lane == 0) p.keys[out * p.W + w] = top;
-            if (top == 0) {
-                for (int i = w + 1 + lane; i < p.W; i += 32) p.keys[out * p.W + i] = 0;
-                break;
-            }
-#pragma unroll
-            for (int i = 0; i < 2; ++i)
-                if (head[i] == top) head[i] = ++at[i] < p.W ? lists[(i * 32 + lane) * p.W + at[i]] : 0;
-        }
+    pdl_trigger();  // not before: a merge that waits beside the rows costs them more (20 us of 36) than its start
+    const int n = n_found;
+    if (n <= kCounted) {
+        if (warp == 0) warp_place(found, n, p.W, lane, p.keys + out * p.W);
+        return;
     }
+    if (n <= kFound) {  // two to a thread (more than W: no place stays empty)
+        const uint64_t a = threadIdx.x < n ? found[threadIdx.x] : 0, b = threadIdx.x + kThreads < n ? found[threadIdx.x + kThreads] : 0;
+        int at = 0, bt = 0;
+        for (int j = 0; j < n; ++j) {
+            const uint64_t k = found[j];
+            at += k > a;
+            bt += k > b;
+        }
+        if (a != 0 && at < p.W) p.keys[out * p.W + at] = a;
+        if (b != 0 && bt < p.W) p.keys[out * p.W + bt] = b;
+        return;
+    }
+
+    // Too many, as of sorted logits, whose best lie side by side: the best of all, one after the other.
+    uint64_t last = ~0ull;
+    for (int i = 0; i < p.W; ++i) {
+        uint64_t key = 0;
+        for (int w = warp; w < n_chosen; w += kWarps) {
+#pragma unroll 1
+            for (int i = 0; i < kVecs; ++i) {
+                float f[View::kVec];
+                View::unpack(view.load(vector_at(w, i)), f);
+#pragma unroll
+                for (int j = 0; j < View::kVec; ++j) {
+                    const uint64_t k = make_key(candidate(f[j]), vector_at(w, i) - view.off + j);
+                    key = k < last && k > key ? k : key;
+                }
+            }
+        }
+        key = warp_max_key(key);
+        __syncthreads();  // the last round's keys have been read
+        if (lane == 0) found[warp] = key;
+        __syncthreads();
+        last = 0;
+#pragma unroll
+        for (int w = 0; w < kWarps; ++w) last = found[w] > last ? found[w] : last;
+        if (threadIdx.x == 0) p.keys[out * p.W + i] = last;
+    }
+}
+
+// The logarithm of a sum, within 2^-24: fp32's of a factor near one.
+__device__ __forceinline__ double log_sum(uint64_t fixed) {
+    if (fixed == 0) return -INFINITY;
+    int e = 63 - __clzll(fixed);
+    int64_t rest = (int64_t)(fixed << (63 - e)) & INT64_MAX;  // the factor in [1, 2) without its one, times 2^63
+    float f = (float)rest * 0x1p-63f;
+    if (f > 0.4f) f = (float)(rest - INT64_MAX - 1) * 0x1p-64f, ++e;  // half of it, less one: in [-0.3, 0)
+    return (e - 40) * kLn2 + (double)log1pf(f);
+}
+
+// n^-a in 64 bits: the series of the logarithm in z = (f - 1) / (f + 1) for n = 2^e f, |z| <= 0.172, to 2 z^13 / 13
+// (2e-11), and the exponential's to r^10 / 10!, |r| <= 0.35 (1e-12). (The library's power takes 5 us here.)
+__device__ __forceinline__ double inverse_power(int n, double a) {
+    if (n <= 1 || a == 0.) return 1.;
+    int e = 31 - __clz(n);
+    double f = (double)n * __longlong_as_double((int64_t)(1023 - e) << 52);
+    if (f > 1.4) f *= 0.5, ++e;
+    const double d = f + 1.;
+    double r = (double)__frcp_rn((float)d);
+    r = r * fma(-d, r, 2.);
+    r = r * fma(-d, r, 2.);
+    const double z = (f - 1.) * r, q = z * z;
+    double s = 1. / 13.;
+    s = fma(s, q, 1. / 11.);
+    s = fma(s, q, 1. / 9.);
+    s = fma(s, q, 1. / 7.);
+    s = fma(s, q, 1. / 5.);
+    s = fma(s, q, 1. / 3.);
+    s = fma(s, q, 1.);
+    const double x = -a * fma(2. * z, s, e * kLn2);  // log n^-a
+    if (!(fabs(x) < 700.)) return x < 0. ? 0. : INFINITY;
+    const double whole = rint(x * 1.4426950408889634), t = fma(whole, -kLn2, x);
+    double y = 1. / 3628800.;
+    y = fma(y, t, 1. / 362880.);
+    y = fma(y, t, 1. / 40320.);
+    y = fma(y, t, 1. / 5040.);
+    y = fma(y, t, 1. / 720.);
+    y = fma(y, t, 1. / 120.);
+    y = fma(y, t, 1. / 24.);
+    y = fma(y, t, 1. / 6.);
+    y = fma(y, t, 0.5);
+    y = fma(y, t, 1.);
+    y = fma(y, t, 1.);
+    return y * __longlong_as_double((int64_t)((int)whole + 1023) << 52);
 }
 
 // One block per sequence, a warp per beam: the beam's chunks are merged by their logits, then the
@@ -349,12 +526,14 @@ __global__ void __launch_bounds__(32 * kMaxBeams) beam_merge_kernel(const __grid
     const int b = blockIdx.x, warp = threadIdx.x >> 5, lane = threadIdx.x & 31, row = b * p.K + warp;
     const int n = p.chunks * p.W;
     uint64_t* in = shared + (int64_t)warp * n;
-    uint64_t* keys = shared + (int64_t)p.K * n;
-    double* scores = reinterpret_cast<double*>(keys + p.K * p.W);
+    uint64_t* all_keys = shared + (int64_t)p.K * n;
+    uint64_t* keys = all_keys + warp * p.W;
+    double* scores = reinterpret_cast<double*>(all_keys + p.K * p.W);
     uint64_t* ranks = reinterpret_cast<uint64_t*>(scores + p.K * p.W);
     __shared__ int s_length[kMaxBeams];
     __shared__ bool s_ended[kMaxBeams];
-    pdl_wait();
+    __shared__ uint64_t few[kMaxBeams][kCounted];
+    // The rows' kernel is an ordinary launch: what was written before it is there.
     const double score = p.scores[row];
     const bool ended = p.finished && p.finished[row];
     const int length = p.lengths ? p.lengths[row] : 0;
@@ -363,37 +542,54 @@ __global__ void __launch_bounds__(32 * kMaxBeams) beam_merge_kernel(const __grid
         s_length[warp] = after;
         s_ended[warp] = ended;
     }
-    const double weight = p.length_penalty == 0. ? 1. : pow((double)(after > 1 ? after : 1), p.length_penalty);
+    const double weight = inverse_power(after, p.length_penalty);
+    pdl_wait();
     double base = 0., lse = 0.;
     if (!ended) {
         const int64_t at = (int64_t)row * p.chunks;
         for (int i = lane; i < n; i += 32) in[i] = p.keys[at * p.W + i];
         float m[2];
-        double s[2];
+        uint64_t s[2];
 #pragma unroll
         for (int i = 0; i < 2; ++i) {
             m[i] = i * 32 + lane < p.chunks ? p.maxima[at + i * 32 + lane] : -INFINITY;
-            s[i] = m[i] > -INFINITY ? p.sums[at + i * 32 + lane] : 0.;
+            s[i] = i * 32 + lane < p.chunks ? p.sums[at + i * 32 + lane] : 0;
         }
         const float top = warp_max(fmaxf(m[0], m[1]));
-        double sum = 0.;
-#pragma unroll
-        for (int i = 0; i < 2; ++i) sum += m[i] == top || s[i] == 0. ? s[i] : s[i] * exp(base_log(m[i]) - base_log(top));
-#pragma unroll
-        for (int o = 16; o > 0; o >>= 1) sum += __shfl_xor_sync(0xffffffffu, sum, o);
+        const uint64_t sum = warp_sum_fixed(rebase_fixed(s[0], m[0], top) + rebase_fixed(s[1], m[1], top));
         base = base_log(top);
-        lse = log(sum);
+        lse = log_sum(sum);
         __syncwarp();
-        int from[2] = {0, 0};
-        uint64_t head[2];
+        // The W best of the chunks' lists: a bound that W logits reach is the least of what stands at place
+        // ceil(W / chunks) of each.
+        const int q = (p.W - 1) / p.chunks;
+        uint64_t bound = ~0ull;
+        for (int i = lane; i < p.chunks; i += 32) bound = min(bound, in[i * p.W + q]);
+        bound = ~warp_max_key(~bound);
+        if (bound == 0) bound = 1;
+        int found = 0;
+        for (int i0 = 0; i0 < n; i0 += 32) {
+            const uint64_t k = i0 + lane < n ? in[i0 + lane] : 0;
+            const uint32_t hit = __ballot_sync(0xffffffffu, k >= bound);
+            const int to = found + __popc(hit & ((1u << lane) - 1));
+            if (k >= bound && to < kCounted) few[warp][to] = k;
+            found += __popc(hit);
+        }
+        __syncwarp();
+        if (found <= kCounted) {
+            warp_place(few[warp], found, p.W, lane, keys);
+        } else {  // one after the other, two lists to a lane
+            int from[2] = {0, 0};
+            uint64_t head[2];
 #pragma unroll
-        for (int i = 0; i < 2; ++i) head[i] = i * 32 + lane < p.chunks ? in[(i * 32 + lane) * p.W] : 0;
-        for (int w = 0; w < p.W; ++w) {
-            const uint64_t best = warp_max_key(max(head[0], head[1]));
-            if (lane == 0) keys[warp * p.W + w] = best;
+            for (int i = 0; i < 2; ++i) head[i] = i * 32 + lane < p.chunks ? in[(i * 32 + lane) * p.W] : 0;
+            for (int w = 0; w < p.W; ++w) {
+                const uint64_t best = warp_max_key(max(head[0], head[1]));
+                if (lane == 0) keys[w] = best;
 #pragma unroll
-            for (int i = 0; i < 2; ++i)
-                if (best != 0 && head[i] == best) head[i] = ++from[i] < p.W ? in[(i * 32 + lane) * p.W + from[i]] : 0;
+                for (int i = 0; i < 2; ++i)
+                    if (best != 0 && head[i] == best) head[i] = ++from[i] < p.W ? in[(i * 32 + lane) * p.W + from[i]] : 0;
+            }
         }
         __syncwarp();
     }
@@ -401,39 +597,51 @@ __global__ void __launch_bounds__(32 * kMaxBeams) beam_merge_kernel(const __grid
         double s = -INFINITY;
         if (ended) {
             if (w == 0) s = score;
-        } else if (const uint64_t key = keys[warp * p.W + w]) {
+        } else if (const uint64_t key = keys[w]) {
             const double x = key_logit(key);
             s = score + ((x == base ? 0. : x - base) - lse);
         }
-        const double rank = s / weight;
+        const double rank = s * weight;
         const bool some = rank > -INFINITY && s > -INFINITY;
         scores[warp * p.W + w] = s;
         const uint64_t u = (uint64_t)__double_as_longlong(rank + 0.);
         ranks[warp * p.W + w] = !some ? 0 : u >> 63 ? ~u : u | 1ull << 63;
     }
     __syncthreads();
+    const auto write = [&](int w, int k, int i) {  // place w: candidate i of beam k, or none
+        const int64_t out = (int64_t)b * p.W + w;
+        const bool some = k >= 0;
+        const int token = !some ? max(p.eos, 0) : s_ended[k] ? p.eos : key_token(all_keys[k * p.W + i]);
+        p.scores_out[out] = some ? (float)scores[k * p.W + i] : -INFINITY;
+        p.tokens[out] = token;
+        p.parents[out] = k;
+        if (p.finished_out) p.finished_out[out] = !some || s_ended[k] || token == p.eos;
+        if (p.lengths_out) p.lengths_out[out] = some ? s_length[k] : 0;
+    };
+    const int total = p.K * p.W;
+    if (total <= kThreads && total <= 32 * p.K) {  // a candidate to a thread, its place counted (equal ranks: the beams in order)
+        const int t = threadIdx.x;
+        const uint64_t mine = t < total ? ranks[t] : 0;
+        int larger = 0, some = 0;
+#pragma unroll 4
+        for (int j = 0; j < total; ++j) {
+            const uint64_t k = ranks[j];
+            larger += k > mine || (k == mine && j < t);
+            some += k != 0;
+        }
+        if (mine != 0 && larger < p.W) write(larger, t / p.W, t % p.W);
+        if (t < p.W && t >= some) write(t, -1, 0);
+        return;
+    }
     if (warp > 0) return;
     int at = 0;
     uint64_t head = lane < p.K ? ranks[lane * p.W] : 0;
     for (int w = 0; w < p.W; ++w) {
-        const int64_t out = (int64_t)b * p.W + w;
         const uint64_t top = warp_max_key(head);
-        if (top == 0) {
-            if (lane == 0) {
-                p.scores_out[out] = -INFINITY;
-                p.tokens[out] = p.eos >= 0 ? p.eos : 0;
-                p.parents[out] = -1;
-                if (p.finished_out) p.finished_out[out] = 1;
-                if (p.lengths_out) p.lengths_out[out] = 0;
-            }
-        } else if (lane == __ffs(__ballot_sync(0xffffffffu, head == top)) - 1) {  // the lowest of equal beams
-            const int token = s_ended[lane] ? p.eos : key_token(keys[lane * p.W + at]);
-            p.scores_out[out] = (float)scores[lane * p.W + at];
-            p.tokens[out] = token;
-            p.parents[out] = lane;
-            if (p.finished_out) p.finished_out[out] = s_ended[lane] || token == p.eos;
-            if (p.lengths_out) p.lengths_out[out] = s_length[lane];
-            head = ++at < p.W ? ranks[lane * p.W + at] : 0;
+        const int from = __ffs(__ballot_sync(0xffffffffu, head == top)) - 1;  // the lowest of equal beams
+        if (lane == (top == 0 ? 0 : from)) {
+            write(w, top == 0 ? -1 : lane, at);
+            if (top != 0) head = ++at < p.W ? ranks[lane * p.W + at] : 0;
         }
         __syncwarp();
     }
@@ -477,14 +685,19 @@ cudaError_t launch_reorder_u(const ReorderParams& p, dim3 grid, cudaStream_t str
     return cudaGetLastError();
 }
 
+template <typename T>
+void launch_rows(const BeamParams& p, unsigned blocks, cudaStream_t stream) {
+    if (p.wide) beam_rows_kernel<T, true><<<blocks, kThreads, 0, stream>>>(p);
+    else beam_rows_kernel<T, false><<<blocks, kThreads, 0, stream>>>(p);
+}
+
 }  // namespace
 
 cudaError_t launch_beam_select(const BeamParams& p, int in_dtype, cudaStream_t stream) {
     const unsigned blocks = (unsigned)(p.B * p.K * p.chunks);
-    const size_t lists = (size_t)p.W * p.W * sizeof(uint64_t);
-    if (in_dtype == 0) beam_rows_kernel<float><<<blocks, kThreads, lists, stream>>>(p);
-    else if (in_dtype == 1) beam_rows_kernel<__nv_bfloat16><<<blocks, kThreads, lists, stream>>>(p);
-    else beam_rows_kernel<__half><<<blocks, kThreads, lists, stream>>>(p);
+    if (in_dtype == 0) launch_rows<float>(p, blocks, stream);
+    else if (in_dtype == 1) launch_rows<__nv_bfloat16>(p, blocks, stream);
+    else launch_rows<__half>(p, blocks, stream);
     cudaError_t e = cudaGetLastError();
     if (e != cudaSuccess) return e;
     e = prepare_once<beam_merge_kernel>(kBeamMergeBytes);

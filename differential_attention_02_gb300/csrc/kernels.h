@@ -217,15 +217,16 @@ struct BeamParams {
     int32_t *tokens, *parents;
     uint8_t* finished_out;          // or null
     int32_t* lengths_out;           // or null
-    int chunks, chunk_segments;     // blocks that share a row, and the segments of each
+    int chunks, chunk_rounds, wide; // blocks that share a row, the rounds of each; a segment is a round
     uint64_t* keys;                 // workspace: [B K][chunks][W], a chunk's best logits
-    double* sums;                   // [B K][chunks]: its sum of exponentials, scaled by its maximum's base
+    uint64_t* sums;                 // [B K][chunks]: its sum of exponentials, scaled by its maximum's base
     float* maxima;                  // [B K][chunks]
 };
 constexpr int kBeamSegment = 256;        // logits of which a chunk keeps one maximum
+constexpr int kBeamRoundBytes = 2048;    // of a row, read by a warp at a time
 constexpr int kBeamSegments = 512;       // at most, of a chunk
 constexpr int kBeamChunks = 64;          // at most, of a row
-constexpr int kBeamMergeBytes = 200 * 1024;  // shared memory of the merge, 8 K W (chunks + 3) at most
+constexpr int kBeamMergeBytes = 200 * 1024;  // shared memory of the merge, 8 K W (chunks + 3) at most, beside 17 KB
 cudaError_t launch_beam_select(const BeamParams& p, int in_dtype, cudaStream_t stream);
 
 // Rows of per-beam states moved to the places of their children, in place (beam.cu).
