@@ -21,7 +21,7 @@ bool workspace_ok(const void* ws, size_t bytes, size_t need) {
 // Chunks of a row, and the workspace of the selection: control block, a chunk's best logits, its sum and its maximum.
 struct BeamLayout {
     int chunks, chunk_rounds, wide;
-    size_t keys, sums, maxima, total;
+    size_t keys, sums, maxima, weights, total;
 };
 bool beam_layout(int B, int K, int V, int W, int in_dtype, BeamLayout* l) {
     if (B < 0 || K < 1 || K > kMaxBeams || V < 1 || V > DIFFATTN_MAX_VOCABULARY || W < 1 || W > kMaxBeamWidth || B > 65535)
@@ -43,7 +43,8 @@ bool beam_layout(int B, int K, int V, int W, int in_dtype, BeamLayout* l) {
     l->keys = kControlBytes;
     l->sums = l->keys + round256(rows * l->chunks * W * sizeof(uint64_t));
     l->maxima = l->sums + round256(rows * l->chunks * sizeof(uint64_t));
-    l->total = l->maxima + round256(rows * l->chunks * sizeof(float));
+    l->weights = l->maxima + round256(rows * l->chunks * sizeof(float));
+    l->total = l->weights + round256(rows * sizeof(double));
     return true;
 }
 
@@ -124,6 +125,7 @@ diffattn_status diffattn_beam_select(const void* logits, int64_t stride_b, int64
     p.keys = reinterpret_cast<uint64_t*>(ws + l.keys);
     p.sums = reinterpret_cast<uint64_t*>(ws + l.sums);
     p.maxima = reinterpret_cast<float*>(ws + l.maxima);
+    p.weights = reinterpret_cast<double*>(ws + l.weights);
     return cuda_status(launch_beam_select(p, in_dtype == DIFFATTN_F32 ? 0 : in_dtype == DIFFATTN_BF16 ? 1 : 2,
                                           static_cast<cudaStream_t>(stream)));
 }

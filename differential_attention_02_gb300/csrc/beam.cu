@@ -76,26 +76,37 @@ struct RowView {
         asm("ld.global.nc.v4.u32 {%0, %1, %2, %3}, [%4];" : "=r"(v.x), "=r"(v.y), "=r"(v.z), "=r"(v.w) : "l"(base + at));
         return v;
     }
-    __device__ __forceinline__ uint4 load(int at) const {
-        uint4 v;
-        if (at >= off && at + kVec <= end) {
-            v = load_whole(at);
-        } else {
-            uint32_t w[4];
+    __device__ __forceinline__ float at(int i) const {
+        if constexpr (std::is_same<T, float>::value) return base[i];
+        else if constexpr (std::is_same<T, __half>::value) return __half2float(base[i]);
+        else return __bfloat162float(base[i]);
+    }
+    // Any vector: logit by logit at the row's ends.
+    __device__ __noinline__ static uint4 load_edge(const T* base, int at, int off, int end) {
+        uint32_t w[4];
 #pragma unroll
-            for (int i = 0; i < 4; ++i) {
-                if constexpr (sizeof(T) == 4) {
-                    w[i] = at + i >= off && at + i < end ? *reinterpret_cast<const uint32_t*>(base + at + i) : 0xff800000u;
-                } else {
-                    constexpr uint32_t none = std::is_same<T, __half>::value ? 0xfc00u : 0xff80u;
-                    const int lo = at + 2 * i, hi = lo + 1;
-                    w[i] = (lo >= off && lo < end ? *reinterpret_cast<const uint16_t*>(base + lo) : none) |
-                           (hi >= off && hi < end ? *reinterpret_cast<const uint16_t*>(base + hi) : none) << 16;
-                }
+        for (int i = 0; i < 4; ++i) {
+            if constexpr (sizeof(T) == 4) {
+                w[i] = at + i >= off && at + i < end ? *reinterpret_cast<const uint32_t*>(base + at + i) : 0xff800000u;
+            } else {
+                constexpr uint32_t none = std::is_same<T, __half>::value ? 0xfc00u : 0xff80u;
+                const int lo = at + 2 * i, hi = lo + 1;
+                w[i] = (lo >= off && lo < end ? *reinterpret_cast<const uint16_t*>(base + lo) : none) |
+                       (hi >= off && hi < end ? *reinterpret_cast<const uint16_t*>(base + hi) : none) << 16;
             }
-            v = make_uint4(w[0], w[1], w[2], w[3]);
         }
-        return v;
+        return make_uint4(w[0], w[1], w[2], w[3]);
+    }
+    // The vectors at `at` and every 32 vectors behind it of a warp whose logits begin at `first`.
+    template <int N>
+    __device__ __forceinline__ void load(int first, int at, uint4* v) const {
+        if (first >= off && first + N * 32 * kVec <= end) {
+#pragma unroll
+            for (int i = 0; i < N; ++i) v[i] = load_whole(at + i * 32 * kVec);
+        } else {
+#pragma unroll
+            for (int i = 0; i < N; ++i) v[i] = load_edge(base, at + i * 32 * kVec, off, end);
+        }
     }
     // The logits of one vector, and the largest of them (NaN left out unless all are).
     __device__ __forceinline__ static void unpack(uint4 v, float* x) {
@@ -177,10 +188,15 @@ __device__ __forceinline__ uint64_t rebase_fixed(uint64_t sum, float from, float
     }
     return __float2ull_rn(__ull2float_rn(sum) * any_rebase(from, to));
 }
-__device__ __forceinline__ uint64_t warp_sum_fixed(uint64_t v) {
-#pragma unroll
-    for (int o = 16; o > 0; o >>= 1) v += __shfl_xor_sync(0xffffffffu, v, o);
-    return v;
+__device__ __forceinline__ uint64_t warp_sum_fixed(uint64_t v) {  // of less than 2^64, in three parts of 22 bits
+    const uint64_t lo = __reduce_add_sync(0xffffffffu, (uint32_t)v & 0x3fffffu);
+    const uint64_t mid = __reduce_add_sync(0xffffffffu, (uint32_t)(v >> 22) & 0x3fffffu);
+    const uint64_t hi = __reduce_add_sync(0xffffffffu, (uint32_t)(v >> 44));
+    return lo + (mid << 22) + (hi << 44);
+}
+__device__ __forceinline__ float warp_max_logit(float x) {  // -inf for none
+    const uint32_t u = __reduce_max_sync(0xffffffffu, candidate(x));
+    return u == 0 ? -INFINITY : key_logit((uint64_t)u << 32);
 }
 
 // The sum of a vector's terms where that takes care; rare, and out of the way of the instruction cache. (By value: an
@@ -195,14 +211,13 @@ __device__ __noinline__ float any_sum(uint4 v, float m, float c) {
 }
 
 // ---------------------------------------------------------------- the W largest of a few keys
-// Keys apart from each other, in shared memory, in any order: the place of each is the number of larger ones.
-// No step waits for the one before, so that 16 of 30 keys take a fifth of the time of 16 maxima one after
-// the other; beyond 64 keys a warp leaves it to those.
+// Keys apart from each other, in shared memory, in any order: the place of each is the number of larger ones, and
+// no step waits for the one before. Beyond 64 keys (two a lane) it is left to others.
 constexpr int kCounted = 64;
 __device__ __forceinline__ void warp_place(const uint64_t* keys, int n, int W, int lane, uint64_t* out) {
     const uint64_t a = lane < n ? keys[lane] : 0, b = lane + 32 < n ? keys[lane + 32] : 0;
     int at = 0, bt = 0;
-#pragma unroll 4
+#pragma unroll 2
     for (int j = 0; j < n; ++j) {
         const uint64_t k = keys[j];
         at += k > a;
@@ -213,61 +228,105 @@ __device__ __forceinline__ void warp_place(const uint64_t* keys, int n, int W, i
     for (int i = n + lane; i < W; i += 32) out[i] = 0;
 }
 
-// One warp: the segments of the W largest maxima, equal ones in order, of up to 32 N. Returns how many there
-// are, and the last one's maximum. The W-th of the lanes' own maxima is a bound that W segments reach, and
-// few more do; where they are too many (equal maxima), or W more than the lanes, one is taken after the other.
-template <int N>
-__device__ __forceinline__ int choose_segments(const uint32_t* best, int segments, int W, int lane, uint64_t* few, uint64_t* sorted,
-                                               int* chosen, uint32_t* last) {
-    uint32_t mine[N];
-#pragma unroll
-    for (int i = 0; i < N; ++i) mine[i] = i * 32 + lane < segments ? best[i * 32 + lane] : 0;
-    uint32_t u = 0;
-#pragma unroll
-    for (int i = 0; i < N; ++i) u = max(u, mine[i]);
-    if (W <= 32) {
-        int larger = 0;
-#pragma unroll
-        for (int j = 0; j < 32; ++j) {
-            const uint32_t k = __shfl_sync(0xffffffffu, u, j);
-            larger += k > u || (k == u && j < lane);
+// One warp: the segments of the W largest maxima as keys, best first, equal ones in order; places beyond the last are
+// 0. Of more than 64 segments, the W-th of the lanes' own maxima is a bound that W segments reach, and few more
+// do; where they are too many (equal maxima), or W more than the lanes, one is taken after the other (and `best` is
+// used up).
+__device__ __forceinline__ void choose_segments(uint32_t* best, int segments, int W, int lane, uint64_t* few, uint64_t* sorted) {
+    if (W <= 32 || segments <= kCounted) {
+        uint32_t bound = 1;
+        if (segments > kCounted) {
+            uint32_t u = 0;
+#pragma unroll 1
+            for (int i = 0; i < segments; i += 32) u = max(u, i + lane < segments ? best[i + lane] : 0u);
+            uint32_t* lanes = reinterpret_cast<uint32_t*>(sorted);
+            lanes[lane] = u;
+            __syncwarp();
+            int larger = 0;
+#pragma unroll 2
+            for (int j = 0; j < 32; j += 4) {
+                const uint4 k = *reinterpret_cast<const uint4*>(lanes + j);
+                larger += (int)(k.x > u) | ((int)(k.x == u) & (int)(j < lane));
+                larger += (int)(k.y > u) | ((int)(k.y == u) & (int)(j + 1 < lane));
+                larger += (int)(k.z > u) | ((int)(k.z == u) & (int)(j + 2 < lane));
+                larger += (int)(k.w > u) | ((int)(k.w == u) & (int)(j + 3 < lane));
+            }
+            bound = max(__reduce_max_sync(0xffffffffu, larger == W - 1 ? u : 0u), 1u);
+            __syncwarp();
         }
-        const uint32_t bound = max(__shfl_sync(0xffffffffu, u, __ffs(__ballot_sync(0xffffffffu, larger == W - 1)) - 1), 1u);
         int n = 0;
-#pragma unroll
-        for (int i = 0; i < N; ++i) {
-            const uint32_t hit = __ballot_sync(0xffffffffu, mine[i] >= bound);
+#pragma unroll 1
+        for (int i = 0; i < segments; i += 32) {
+            const uint32_t x = i + lane < segments ? best[i + lane] : 0;
+            const uint32_t hit = __ballot_sync(0xffffffffu, x >= bound);
             const int at = n + __popc(hit & ((1u << lane) - 1));
-            if (mine[i] >= bound && at < kCounted) few[at] = make_key(mine[i], i * 32 + lane);
+            if (x >= bound && at < kCounted) few[at] = make_key(x, i + lane);
             n += __popc(hit);
         }
         __syncwarp();
         if (n <= kCounted) {
             warp_place(few, n, W, lane, sorted);
-            __syncwarp();
-            n = min(n, W);
-            if (lane < n) chosen[lane] = key_token(sorted[lane]);
-            *last = n > 0 ? (uint32_t)(sorted[n - 1] >> 32) : 0;
-            return n;
+            return;
         }
     }
-    int n = 0;
-    for (; n < W; ++n) {
-        int at = 0;
-        u = 0;
-#pragma unroll
-        for (int i = N - 1; i >= 0; --i)
-            if (mine[i] >= u) u = mine[i], at = i * 32 + lane;
-        const uint32_t top = __reduce_max_sync(0xffffffffu, u);
-        if (top == 0) break;
-        const int segment = __reduce_min_sync(0xffffffffu, u == top ? at : INT_MAX);
-        *last = top;
-        if (lane == 0) chosen[n] = segment;
-#pragma unroll
-        for (int i = 0; i < N; ++i)
-            if (segment == i * 32 + lane) mine[i] = 0;
+#pragma unroll 1
+    for (int n = 0; n < W; ++n) {
+        uint64_t key = 0;
+#pragma unroll 1
+        for (int i = lane; i < segments; i += 32) {
+            const uint64_t k = make_key(best[i], i);
+            key = k > key ? k : key;
+        }
+        key = warp_max_key(key);
+        if (lane == 0) sorted[n] = key;
+        if (key != 0 && key_token(key) % 32 == lane) best[key_token(key)] = 0;
     }
-    return n;
+}
+
+// The logarithm of a sum, within 2^-24: fp32's of a factor near one.
+__device__ __forceinline__ double log_sum(uint64_t fixed) {
+    if (fixed == 0) return -INFINITY;
+    int e = 63 - __clzll(fixed);
+    int64_t rest = (int64_t)(fixed << (63 - e)) & INT64_MAX;  // the factor in [1, 2) without its one, times 2^63
+    float f = (float)rest * 0x1p-63f;
+    if (f > 0.4f) f = (float)(rest - INT64_MAX - 1) * 0x1p-64f, ++e;  // half of it, less one: in [-0.3, 0)
+    return (e - 40) * kLn2 + (double)log1pf(f);
+}
+
+// n^-a in 64 bits: the series of the logarithm in z = (f - 1) / (f + 1) for n = 2^e f, |z| <= 0.177, to 2 z^13 / 13
+// (the next term is 7e-13), and the exponential's to t^10 / 10!, |t| <= 0.35 (the next: 2e-13).
+__device__ __forceinline__ double inverse_power(int n, double a) {
+    if (n <= 1 || a == 0.) return 1.;
+    int e = 31 - __clz(n);
+    double f = (double)n * __longlong_as_double((int64_t)(1023 - e) << 52);
+    if (f > 1.4) f *= 0.5, ++e;
+    const double d = f + 1.;
+    double r = (double)__frcp_rn((float)d);
+    r = r * fma(-d, r, 2.);
+    r = r * fma(-d, r, 2.);
+    const double z = (f - 1.) * r, q = z * z;
+    double s = 1. / 13.;
+    s = fma(s, q, 1. / 11.);
+    s = fma(s, q, 1. / 9.);
+    s = fma(s, q, 1. / 7.);
+    s = fma(s, q, 1. / 5.);
+    s = fma(s, q, 1. / 3.);
+    s = fma(s, q, 1.);
+    const double x = -a * fma(2. * z, s, e * kLn2);  // log n^-a
+    if (!(fabs(x) < 700.)) return x < 0. ? 0. : INFINITY;
+    const double whole = rint(x * 1.4426950408889634), t = fma(whole, -kLn2, x);
+    double y = 1. / 3628800.;
+    y = fma(y, t, 1. / 362880.);
+    y = fma(y, t, 1. / 40320.);
+    y = fma(y, t, 1. / 5040.);
+    y = fma(y, t, 1. / 720.);
+    y = fma(y, t, 1. / 120.);
+    y = fma(y, t, 1. / 24.);
+    y = fma(y, t, 1. / 6.);
+    y = fma(y, t, 0.5);
+    y = fma(y, t, 1.);
+    y = fma(y, t, 1.);
+    return y * __longlong_as_double((int64_t)((int)whole + 1023) << 52);
 }
 
 // One block per chunk of a row: its sum of exponentials and its W best logits. WIDE: a segment is a whole round.
@@ -278,30 +337,30 @@ __global__ void __launch_bounds__(kThreads, 4) beam_rows_kernel(const __grid_con
     __shared__ uint32_t best[kBeamSegments];          // a segment's largest logit
     __shared__ uint64_t sums[kWarps];
     __shared__ float maxima[kWarps];
-    __shared__ int chosen[kMaxBeamWidth];
+    __shared__ __align__(16) uint64_t chosen[kMaxBeamWidth];  // segments of the W largest maxima
     __shared__ int n_chosen, n_above, n_found;
-    __shared__ uint32_t least;
     __shared__ uint64_t found[kFound];                // logits that may be among the W best
     const int row = blockIdx.x / p.chunks, chunk = blockIdx.x % p.chunks;
     const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
-    if (p.finished && p.finished[row]) return;
+    const bool ended = p.finished && p.finished[row];
     const View view(static_cast<const T*>(p.logits) + row / p.K * p.stride_b + row % p.K * p.stride_k, p.V);
     const int begin = chunk * p.chunk_rounds * View::kRound;
     const int rounds = min(p.chunk_rounds, (view.end - begin + View::kRound - 1) / View::kRound);  // may be none
 
     float m = -INFINITY, c = 0.f, sum = 0.f;
     const auto load = [&](int r, uint4* v) {
-        const int at = begin + r * View::kRound + lane * View::kVec;
-        if (begin + r * View::kRound >= view.off && begin + (r + 1) * View::kRound <= view.end) {
-#pragma unroll
-            for (int i = 0; i < 4; ++i) v[i] = view.load_whole(at + i * 32 * View::kVec);
-        } else {
-#pragma unroll
-            for (int i = 0; i < 4; ++i) v[i] = view.load(at + i * 32 * View::kVec);
-        }
+        const int first = begin + r * View::kRound;
+        view.template load<4>(first, first + lane * View::kVec, v);
     };
     uint4 next[4];
     if (warp < rounds) load(warp, next);
+    // The power that weighs lengths takes 2 us in 64 bits: one warp takes it while the first logits are on their way.
+    if (p.length_penalty != 0. && chunk == 0 && warp == kWarps - 1) {
+        const int n = p.lengths[row];
+        const double weight = inverse_power(n < INT_MAX && !ended ? n + 1 : n, p.length_penalty);
+        if (lane == 0) p.weights[row] = weight;
+    }
+    if (ended) return;
     for (int r = warp; r < rounds; r += kWarps) {
         uint4 v[4];
 #pragma unroll
@@ -356,25 +415,23 @@ __global__ void __launch_bounds__(kThreads, 4) beam_rows_kernel(const __grid_con
 
     const int64_t out = (int64_t)row * p.chunks + chunk;
     if (warp == 0) {
-        const int segments = max(rounds, 0) * (WIDE ? 1 : kParts);
-        uint32_t last = 0;
-        uint64_t* sorted = found + kCounted;
-        const int n = segments <= 128   ? choose_segments<4>(best, segments, p.W, lane, found, sorted, chosen, &last)
-                      : segments <= 256 ? choose_segments<8>(best, segments, p.W, lane, found, sorted, chosen, &last)
-                                        : choose_segments<kBeamSegments / 32>(best, segments, p.W, lane, found, sorted, chosen, &last);
+        choose_segments(best, max(rounds, 0) * (WIDE ? 1 : kParts), p.W, lane, found, chosen);
         __syncwarp();
-        const uint32_t bound = n == p.W ? last : 1;  // a logit below the last chosen maximum is not among the W best
-        int above = 0;
-        for (int i = lane; i < n; i += 32) above += best[chosen[i]] > bound;
+        const uint32_t last = (uint32_t)(chosen[p.W - 1] >> 32);
+        int n = 0, above = 0;
+        for (int i = lane; i < p.W; i += 32) {
+            n += chosen[i] != 0;
+            above += (uint32_t)(chosen[i] >> 32) > last;
+        }
+        n = __reduce_add_sync(0xffffffffu, n);
         above = __reduce_add_sync(0xffffffffu, above);
         if (lane == 0) {
             n_chosen = n;
             n_above = above;
             n_found = 0;
-            least = bound;
         }
     } else if (warp == 1) {
-        const float mine = lane < kWarps ? maxima[lane] : -INFINITY, top = warp_max(mine);
+        const float mine = lane < kWarps ? maxima[lane] : -INFINITY, top = warp_max_logit(mine);
         const uint64_t s = warp_sum_fixed(lane < kWarps ? rebase_fixed(sums[lane], mine, top) : 0);
         if (lane == 0) {
             p.sums[out] = s;
@@ -383,46 +440,50 @@ __global__ void __launch_bounds__(kThreads, 4) beam_rows_kernel(const __grid_con
     }
     __syncthreads();
 
-    // The chosen segments' logits that may be among the W best, collected by a warp each.
-    const uint32_t bound = least;
+    // The chosen segments' logits that may be among the W best, collected by a warp each: those that reach the least
+    // of the chosen maxima, or all where fewer segments hold any.
     constexpr int kVecs = WIDE ? 4 : View::kLoads;  // vectors of a lane in a segment
-    const auto vector_at = [&](int w, int i) { return begin + (chosen[w] * kVecs + i) * 32 * View::kVec + lane * View::kVec; };
+    const float bound = n_chosen == p.W ? key_logit(chosen[p.W - 1]) : -INFINITY;
+    const auto first_of = [&](int w) { return begin + key_token(chosen[w]) * kVecs * 32 * View::kVec; };
+    const auto collect = [&](int at) {
+        const int to = atomicAdd(&n_found, 1);  // in any order
+        if (to < kFound) found[to] = make_key(candidate(view.at(at)), at - view.off);
+    };
+#pragma unroll 1
     for (int w = warp; w < n_chosen; w += kWarps) {
         // Of those that equal the bound (many, where a mask leaves few others) the lowest W - n_above tokens are enough,
         // one less for each earlier segment that has such alone.
-        int left = p.W - n_above - max(0, w - n_above);
+        int left = n_chosen < p.W ? 0 : p.W - n_above - max(0, w - n_above);
+        const int mine = first_of(w) + lane * View::kVec;
         uint4 v[kVecs];
-#pragma unroll
-        for (int i = 0; i < kVecs; ++i) v[i] = view.load(vector_at(w, i));
-#pragma unroll
+        view.template load<kVecs>(first_of(w), mine, v);
+#pragma unroll 1
         for (int i = 0; i < kVecs; ++i) {
-            if (!__any_sync(0xffffffffu, candidate(View::largest(v[i])) >= bound)) continue;
+            uint4 x = v[0];
+#pragma unroll
+            for (int k = 1; k < kVecs; ++k)
+                if (i == k) x = v[k];
+            if (!__any_sync(0xffffffffu, View::largest(x) >= bound)) continue;
             float f[View::kVec];
-            View::unpack(v[i], f);
-            const int token = vector_at(w, i) - view.off;  // of the lane's first logit
-            uint32_t same = 0;
+            View::unpack(x, f);
+            uint32_t more = 0, same = 0;
 #pragma unroll
             for (int j = 0; j < View::kVec; ++j) {
-                const uint32_t x = candidate(f[j]);
-                same |= (x == bound) << j;
-                if (x > bound) {
-                    const int to = atomicAdd(&n_found, 1);  // in any order
-                    if (to < kFound) found[to] = make_key(x, token + j);
-                }
+                more |= (f[j] > bound) << j;
+                same |= (f[j] == bound) << j;
             }
+            const int at = mine + i * 32 * View::kVec;
+            for (; more; more &= more - 1) collect(at + __ffs(more) - 1);
             if (left <= 0 || !__any_sync(0xffffffffu, same)) continue;
             int before = __popc(same);
-#pragma unroll
+#pragma unroll 1
             for (int o = 1; o < 32; o <<= 1) {
                 const int y = __shfl_up_sync(0xffffffffu, before, o);
                 if (lane >= o) before += y;
             }
             const int all = __shfl_sync(0xffffffffu, before, 31);
             before -= __popc(same);
-            for (; same && before < left; same &= same - 1, ++before) {
-                const int to = atomicAdd(&n_found, 1);
-                if (to < kFound) found[to] = make_key(bound, token + __ffs(same) - 1);
-            }
+            for (; same && before < left; same &= same - 1, ++before) collect(at + __ffs(same) - 1);
             left -= all;
         }
     }
@@ -450,16 +511,13 @@ __global__ void __launch_bounds__(kThreads, 4) beam_rows_kernel(const __grid_con
     uint64_t last = ~0ull;
     for (int i = 0; i < p.W; ++i) {
         uint64_t key = 0;
+#pragma unroll 1
         for (int w = warp; w < n_chosen; w += kWarps) {
 #pragma unroll 1
-            for (int i = 0; i < kVecs; ++i) {
-                float f[View::kVec];
-                View::unpack(view.load(vector_at(w, i)), f);
-#pragma unroll
-                for (int j = 0; j < View::kVec; ++j) {
-                    const uint64_t k = make_key(candidate(f[j]), vector_at(w, i) - view.off + j);
-                    key = k < last && k > key ? k : key;
-                }
+            for (int j = lane; j < kVecs * 32 * View::kVec; j += 32) {
+                const int at = first_of(w) + j;
+                const uint64_t k = at >= view.off && at < view.end ? make_key(candidate(view.at(at)), at - view.off) : 0;
+                key = k < last && k > key ? k : key;
             }
         }
         key = warp_max_key(key);
@@ -467,56 +525,10 @@ __global__ void __launch_bounds__(kThreads, 4) beam_rows_kernel(const __grid_con
         if (lane == 0) found[warp] = key;
         __syncthreads();
         last = 0;
-#pragma unroll
+#pragma unroll 1
         for (int w = 0; w < kWarps; ++w) last = found[w] > last ? found[w] : last;
         if (threadIdx.x == 0) p.keys[out * p.W + i] = last;
     }
-}
-
-// The logarithm of a sum, within 2^-24: fp32's of a factor near one.
-__device__ __forceinline__ double log_sum(uint64_t fixed) {
-    if (fixed == 0) return -INFINITY;
-    int e = 63 - __clzll(fixed);
-    int64_t rest = (int64_t)(fixed << (63 - e)) & INT64_MAX;  // the factor in [1, 2) without its one, times 2^63
-    float f = (float)rest * 0x1p-63f;
-    if (f > 0.4f) f = (float)(rest - INT64_MAX - 1) * 0x1p-64f, ++e;  // half of it, less one: in [-0.3, 0)
-    return (e - 40) * kLn2 + (double)log1pf(f);
-}
-
-// n^-a in 64 bits: the series of the logarithm in z = (f - 1) / (f + 1) for n = 2^e f, |z| <= 0.172, to 2 z^13 / 13
-// (2e-11), and the exponential's to r^10 / 10!, |r| <= 0.35 (1e-12). (The library's power takes 5 us here.)
-__device__ __forceinline__ double inverse_power(int n, double a) {
-    if (n <= 1 || a == 0.) return 1.;
-    int e = 31 - __clz(n);
-    double f = (double)n * __longlong_as_double((int64_t)(1023 - e) << 52);
-    if (f > 1.4) f *= 0.5, ++e;
-    const double d = f + 1.;
-    double r = (double)__frcp_rn((float)d);
-    r = r * fma(-d, r, 2.);
-    r = r * fma(-d, r, 2.);
-    const double z = (f - 1.) * r, q = z * z;
-    double s = 1. / 13.;
-    s = fma(s, q, 1. / 11.);
-    s = fma(s, q, 1. / 9.);
-    s = fma(s, q, 1. / 7.);
-    s = fma(s, q, 1. / 5.);
-    s = fma(s, q, 1. / 3.);
-    s = fma(s, q, 1.);
-    const double x = -a * fma(2. * z, s, e * kLn2);  // log n^-a
-    if (!(fabs(x) < 700.)) return x < 0. ? 0. : INFINITY;
-    const double whole = rint(x * 1.4426950408889634), t = fma(whole, -kLn2, x);
-    double y = 1. / 3628800.;
-    y = fma(y, t, 1. / 362880.);
-    y = fma(y, t, 1. / 40320.);
-    y = fma(y, t, 1. / 5040.);
-    y = fma(y, t, 1. / 720.);
-    y = fma(y, t, 1. / 120.);
-    y = fma(y, t, 1. / 24.);
-    y = fma(y, t, 1. / 6.);
-    y = fma(y, t, 0.5);
-    y = fma(y, t, 1.);
-    y = fma(y, t, 1.);
-    return y * __longlong_as_double((int64_t)((int)whole + 1023) << 52);
 }
 
 // One block per sequence, a warp per beam: the beam's chunks are merged by their logits, then the
@@ -530,23 +542,18 @@ __global__ void __launch_bounds__(32 * kMaxBeams) beam_merge_kernel(const __grid
     uint64_t* keys = all_keys + warp * p.W;
     double* scores = reinterpret_cast<double*>(all_keys + p.K * p.W);
     uint64_t* ranks = reinterpret_cast<uint64_t*>(scores + p.K * p.W);
-    __shared__ int s_length[kMaxBeams];
-    __shared__ bool s_ended[kMaxBeams];
     __shared__ uint64_t few[kMaxBeams][kCounted];
     // The rows' kernel is an ordinary launch: what was written before it is there.
     const double score = p.scores[row];
     const bool ended = p.finished && p.finished[row];
     const int length = p.lengths ? p.lengths[row] : 0;
     const int after = length < INT_MAX && !ended ? length + 1 : length;
-    if (lane == 0) {
-        s_length[warp] = after;
-        s_ended[warp] = ended;
-    }
-    const double weight = inverse_power(after, p.length_penalty);
     pdl_wait();
+    const double weight = p.length_penalty == 0. ? 1. : p.weights[row];
     double base = 0., lse = 0.;
     if (!ended) {
         const int64_t at = (int64_t)row * p.chunks;
+#pragma unroll 2
         for (int i = lane; i < n; i += 32) in[i] = p.keys[at * p.W + i];
         float m[2];
         uint64_t s[2];
@@ -555,19 +562,24 @@ __global__ void __launch_bounds__(32 * kMaxBeams) beam_merge_kernel(const __grid
             m[i] = i * 32 + lane < p.chunks ? p.maxima[at + i * 32 + lane] : -INFINITY;
             s[i] = i * 32 + lane < p.chunks ? p.sums[at + i * 32 + lane] : 0;
         }
-        const float top = warp_max(fmaxf(m[0], m[1]));
+        const float top = warp_max_logit(fmaxf(m[0], m[1]));
         const uint64_t sum = warp_sum_fixed(rebase_fixed(s[0], m[0], top) + rebase_fixed(s[1], m[1], top));
         base = base_log(top);
         lse = log_sum(sum);
         __syncwarp();
-        // The W best of the chunks' lists: a bound that W logits reach is the least of what stands at place
-        // ceil(W / chunks) of each.
-        const int q = (p.W - 1) / p.chunks;
-        uint64_t bound = ~0ull;
-        for (int i = lane; i < p.chunks; i += 32) bound = min(bound, in[i * p.W + q]);
-        bound = ~warp_max_key(~bound);
-        if (bound == 0) bound = 1;
+        // The W best of the chunks' lists. Of more than 64 logits, a bound that W reach is the least of what stands at
+        // place ceil(W / chunks) of each.
+        uint64_t bound = 1;
+        if (n > kCounted) {
+            const int q = (p.W - 1) / p.chunks;
+            bound = ~0ull;
+#pragma unroll 1
+            for (int i = lane; i < p.chunks; i += 32) bound = min(bound, in[i * p.W + q]);
+            bound = ~warp_max_key(~bound);
+            if (bound == 0) bound = 1;
+        }
         int found = 0;
+#pragma unroll 1
         for (int i0 = 0; i0 < n; i0 += 32) {
             const uint64_t k = i0 + lane < n ? in[i0 + lane] : 0;
             const uint32_t hit = __ballot_sync(0xffffffffu, k >= bound);
@@ -583,6 +595,7 @@ __global__ void __launch_bounds__(32 * kMaxBeams) beam_merge_kernel(const __grid
             uint64_t head[2];
 #pragma unroll
             for (int i = 0; i < 2; ++i) head[i] = i * 32 + lane < p.chunks ? in[(i * 32 + lane) * p.W] : 0;
+#pragma unroll 1
             for (int w = 0; w < p.W; ++w) {
                 const uint64_t best = warp_max_key(max(head[0], head[1]));
                 if (lane == 0) keys[w] = best;
@@ -608,42 +621,48 @@ __global__ void __launch_bounds__(32 * kMaxBeams) beam_merge_kernel(const __grid
         ranks[warp * p.W + w] = !some ? 0 : u >> 63 ? ~u : u | 1ull << 63;
     }
     __syncthreads();
-    const auto write = [&](int w, int k, int i) {  // place w: candidate i of beam k, or none
-        const int64_t out = (int64_t)b * p.W + w;
-        const bool some = k >= 0;
-        const int token = !some ? max(p.eos, 0) : s_ended[k] ? p.eos : key_token(all_keys[k * p.W + i]);
-        p.scores_out[out] = some ? (float)scores[k * p.W + i] : -INFINITY;
+    // The beams' lists by their ranks, equal ones in the beams' order: a candidate's place is its own in its list and
+    // the number of better ones in each other list, found by halving, four lists at a time.
+    const int halves = 1 << (31 - __clz(p.W));
+    int some = 0;
+#pragma unroll 1
+    for (int i0 = 0; i0 < p.W; i0 += 32) {
+        const int i = i0 + lane, t = warp * p.W + i;
+        const uint64_t mine = i < p.W ? ranks[t] : 0;
+        some += __syncthreads_count(mine != 0);
+        if (mine == 0) continue;
+        int place = i;
+#pragma unroll 1
+        for (int first = 0; first < p.K; first += 4) {
+            int lo[4] = {0, 0, 0, 0};
+#pragma unroll 1
+            for (int step = halves; step > 0; step >>= 1) {
+#pragma unroll
+                for (int u = 0; u < 4; ++u) {
+                    const uint64_t k = ranks[min(first + u, p.K - 1) * p.W + min(lo[u] + step, p.W) - 1];
+                    const int better = (int)(k > mine) | ((int)(k == mine) & (int)(first + u < warp));
+                    lo[u] += step * (better & (int)(lo[u] + step <= p.W));
+                }
+            }
+#pragma unroll
+            for (int u = 0; u < 4; ++u) place += first + u < p.K && first + u != warp ? lo[u] : 0;
+        }
+        if (place >= p.W) continue;
+        const int64_t out = (int64_t)b * p.W + place;
+        const int token = ended ? p.eos : key_token(keys[i]);
+        p.scores_out[out] = (float)scores[t];
         p.tokens[out] = token;
-        p.parents[out] = k;
-        if (p.finished_out) p.finished_out[out] = !some || s_ended[k] || token == p.eos;
-        if (p.lengths_out) p.lengths_out[out] = some ? s_length[k] : 0;
-    };
-    const int total = p.K * p.W;
-    if (total <= kThreads && total <= 32 * p.K) {  // a candidate to a thread, its place counted (equal ranks: the beams in order)
-        const int t = threadIdx.x;
-        const uint64_t mine = t < total ? ranks[t] : 0;
-        int larger = 0, some = 0;
-#pragma unroll 4
-        for (int j = 0; j < total; ++j) {
-            const uint64_t k = ranks[j];
-            larger += k > mine || (k == mine && j < t);
-            some += k != 0;
-        }
-        if (mine != 0 && larger < p.W) write(larger, t / p.W, t % p.W);
-        if (t < p.W && t >= some) write(t, -1, 0);
-        return;
+        p.parents[out] = warp;
+        if (p.finished_out) p.finished_out[out] = ended || token == p.eos;
+        if (p.lengths_out) p.lengths_out[out] = after;
     }
-    if (warp > 0) return;
-    int at = 0;
-    uint64_t head = lane < p.K ? ranks[lane * p.W] : 0;
-    for (int w = 0; w < p.W; ++w) {
-        const uint64_t top = warp_max_key(head);
-        const int from = __ffs(__ballot_sync(0xffffffffu, head == top)) - 1;  // the lowest of equal beams
-        if (lane == (top == 0 ? 0 : from)) {
-            write(w, top == 0 ? -1 : lane, at);
-            if (top != 0) head = ++at < p.W ? ranks[lane * p.W + at] : 0;
-        }
-        __syncwarp();
+    for (int w = some + threadIdx.x; w < p.W; w += blockDim.x) {  // places that no candidate is left for
+        const int64_t out = (int64_t)b * p.W + w;
+        p.scores_out[out] = -INFINITY;
+        p.tokens[out] = max(p.eos, 0);
+        p.parents[out] = -1;
+        if (p.finished_out) p.finished_out[out] = 1;
+        if (p.lengths_out) p.lengths_out[out] = 0;
     }
 }
 

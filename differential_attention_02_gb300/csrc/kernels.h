@@ -221,6 +221,7 @@ struct BeamParams {
     uint64_t* keys;                 // workspace: [B K][chunks][W], a chunk's best logits
     uint64_t* sums;                 // [B K][chunks]: its sum of exponentials, scaled by its maximum's base
     float* maxima;                  // [B K][chunks]
+    double* weights;                // [B K]: length^-length_penalty
 };
 constexpr int kBeamSegment = 256;        // logits of which a chunk keeps one maximum
 constexpr int kBeamRoundBytes = 2048;    // of a row, read by a warp at a time
