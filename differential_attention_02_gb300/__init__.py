@@ -34,8 +34,7 @@ EXPORTED = ("diffattn_status_string", "diffattn_lambda", "diffattn_fwd", "diffat
             "diffattn_bwd_saved", "diffattn_rope_freqs", "diffattn_rope", "diffattn_kv_append_chunk_paged",
             "diffattn_kv_append_chunk_paged_fp8", "diffattn_chunk_paged", "diffattn_chunk_paged_fp8",
             "diffattn_chunk_workspace_size", "diffattn_beam_select", "diffattn_beam_workspace_size",
-            "diffattn_beam_reorder", "diffattn_pages_fork", "diffattn_pages_compact", "diffattn_pages_copy",
-            "diffattn_pages_workspace_size")
+            "diffattn_beam_reorder", "diffattn_pages_fork", "diffattn_pages_compact", "diffattn_pages_copy")
 
 
 class DiffAttnError(RuntimeError):
@@ -154,13 +153,11 @@ def load_library(path: str = LIB_PATH) -> ctypes.CDLL:
     lib.diffattn_beam_reorder.restype = i32
     lib.diffattn_beam_reorder.argtypes = [ctypes.c_char_p, i32, vp, vp, i32, i32, vp]
     lib.diffattn_pages_fork.restype = i32
-    lib.diffattn_pages_fork.argtypes = [vp] * 6 + [i32] + [vp] * 5 + [i32] * 4 + [vp, sz, vp]
+    lib.diffattn_pages_fork.argtypes = [vp] * 6 + [i32] + [vp] * 5 + [i32] * 4 + [vp]
     lib.diffattn_pages_compact.restype = i32
-    lib.diffattn_pages_compact.argtypes = [vp] * 7 + [i32, vp] + [i32] * 3 + [vp, sz, vp]
+    lib.diffattn_pages_compact.argtypes = [vp] * 7 + [i32, vp] + [i32] * 3 + [vp]
     lib.diffattn_pages_copy.restype = i32
     lib.diffattn_pages_copy.argtypes = [ctypes.c_char_p, i32, vp, vp, i32, i32, vp]
-    lib.diffattn_pages_workspace_size.restype = i32
-    lib.diffattn_pages_workspace_size.argtypes = [i32, i32, ctypes.POINTER(sz)]
     fpp = ctypes.POINTER(ctypes.c_float)
     lib.diffattn_lambda_bwd.restype = i32
     lib.diffattn_lambda_bwd.argtypes = [fpp] * 4 + [i32, f32] + [fpp] * 4
@@ -791,25 +788,6 @@ def beam_workspace_bytes(B, K, V, width) -> int:
     return n.value
 
 
-def pages_workspace_bytes(rows, num_pages) -> int:
-    n = ctypes.c_size_t()
-    _check((_lib or load_library()).diffattn_pages_workspace_size(rows, num_pages, ctypes.byref(n)),
-           "diffattn_pages_workspace_size")
-    return n.value
-
-
-def _with_workspace(call, args, ws, dev, need, name):
-    """Calls with the kept workspace of this thread and stream, grown by need() when it is too small, or with ws."""
-    if ws is not None:
-        _workspace_arg(ws, dev)
-    kept = ws if ws is not None else _kept_workspace(dev)
-    status = ERR_WORKSPACE if kept is None else call(*args, kept.data_ptr(), kept.numel(), _raw_stream(dev.index))
-    if status == ERR_WORKSPACE and ws is None:
-        kept = _serving_workspace(need(), dev)
-        status = call(*args, kept.data_ptr(), kept.numel(), _raw_stream(dev.index))
-    _check(status, name)
-
-
 def _typed(t, dtype, dev, shape, what):
     if t.dtype != dtype or t.shape != shape or t.device != dev or not t.is_contiguous():
         raise ValueError(f"{what} must be a contiguous {dtype} tensor of shape {list(shape)} on the operands' device")
@@ -845,6 +823,8 @@ def diffattn_beam_select(logits, scores, width: int | None = None, finished=None
     if lengths is not None:
         _typed(lengths, _INT32, dev, shape, "lengths")
     W = K if width is None else int(width)
+    if ws is not None:
+        _workspace_arg(ws, dev)
     if out is None:
         new = lambda dtype: torch.empty((B, W), dtype=dtype, device=dev)  # noqa: E731
         out = BeamChoice(new(torch.float32), new(_INT32), new(_INT32), None if eos is None else new(torch.bool),
@@ -858,8 +838,15 @@ def diffattn_beam_select(logits, scores, width: int | None = None, finished=None
             None if lengths is None else lengths.data_ptr(), -1 if eos is None else int(eos), float(length_penalty), B, K, V, W,
             o_s.data_ptr(), o_t.data_ptr(), o_p.data_ptr(), None if o_f is None else o_f.data_ptr(),
             None if o_l is None else o_l.data_ptr())
-    _with_workspace((_lib or load_library()).diffattn_beam_select, args, ws, dev, lambda: beam_workspace_bytes(B, K, V, W),
-                    "diffattn_beam_select")
+    call, kept = (_lib or load_library()).diffattn_beam_select, ws
+    if ws is None:  # the kept workspace, unless the call says that it is too small
+        kept = _kept_workspace(dev)
+        status = ERR_WORKSPACE if kept is None else call(*args, kept.data_ptr(), kept.numel(), _raw_stream(dev.index))
+        if status != ERR_WORKSPACE:
+            _check(status, "diffattn_beam_select")
+            return out
+        kept = _serving_workspace(beam_workspace_bytes(B, K, V, W), dev)
+    _check(call(*args, kept.data_ptr(), kept.numel(), _raw_stream(dev.index)), "diffattn_beam_select")
     return out
 
 
@@ -926,7 +913,7 @@ def _page_state(table, lens, refs):
 
 
 def diffattn_pages_fork(table, lens, refs, parents=None, grow: int = 0, new_lens=None, done=None, out: PagePlan | None = None,
-                        ws=None, stream=None) -> PagePlan:
+                        stream=None) -> PagePlan:
     """Which pages the rows of a block table (int32 [S, max_pages], lens int32 [S]; refs int32 [num_pages], the
     holders of each page, 0: free) hold after a step. Row b K + k continues row b K + parents[b, k] (int32 [B, K] with
     B K = S, or None: each row itself; -1, or done (bool [S]): none) and has then new_lens[i] tokens (int32 [S]),
@@ -942,7 +929,7 @@ def diffattn_pages_fork(table, lens, refs, parents=None, grow: int = 0, new_lens
     ctx = _elsewhere(dev, stream)
     if ctx is not None:
         with ctx:
-            return diffattn_pages_fork(table, lens, refs, parents, grow, new_lens, done, out, ws)
+            return diffattn_pages_fork(table, lens, refs, parents, grow, new_lens, done, out)
     dev, S, M, P = _page_state(table, lens, refs)
     K = max(S, 1)
     if parents is not None:
@@ -963,12 +950,11 @@ def diffattn_pages_fork(table, lens, refs, parents=None, grow: int = 0, new_lens
     args = (table.data_ptr(), lens.data_ptr(), refs.data_ptr(), None if parents is None else parents.data_ptr(),
             None if new_lens is None else new_lens.data_ptr(), None if done is None else done.data_ptr(), int(grow),
             out.table.data_ptr(), out.lens.data_ptr(), out.refs.data_ptr(), out.copies.data_ptr(), out.info.data_ptr(), S // K, K, M, P)
-    _with_workspace((_lib or load_library()).diffattn_pages_fork, args, ws, dev, lambda: pages_workspace_bytes(S, P),
-                    "diffattn_pages_fork")
+    _check((_lib or load_library()).diffattn_pages_fork(*args, _raw_stream(dev.index)), "diffattn_pages_fork")
     return out
 
 
-def diffattn_pages_compact(table, lens, refs, out: PagePlan | None = None, ws=None, stream=None) -> PagePlan:
+def diffattn_pages_compact(table, lens, refs, out: PagePlan | None = None, stream=None) -> PagePlan:
     """The held pages moved to the front of the pool: the highest ones go to the lowest free places, as many as
     `out.copies` has room for (default: all). table, lens and refs as in diffattn_pages_fork. Returns a PagePlan with the
     table and counts of the new places, the copies for diffattn_pages_copy, and `moved` [num_pages], each page's new
@@ -978,7 +964,7 @@ def diffattn_pages_compact(table, lens, refs, out: PagePlan | None = None, ws=No
     ctx = _elsewhere(dev, stream)
     if ctx is not None:
         with ctx:
-            return diffattn_pages_compact(table, lens, refs, out, ws)
+            return diffattn_pages_compact(table, lens, refs, out)
     dev, S, M, P = _page_state(table, lens, refs)
     if out is None:
         new = lambda *shape: torch.empty(shape, dtype=_INT32, device=dev)  # noqa: E731
@@ -992,8 +978,7 @@ def diffattn_pages_compact(table, lens, refs, out: PagePlan | None = None, ws=No
             out.lens.copy_(lens)
     args = (table.data_ptr(), lens.data_ptr(), refs.data_ptr(), out.table.data_ptr(), out.refs.data_ptr(), out.moved.data_ptr(),
             out.copies.data_ptr(), out.copies.shape[0], out.info.data_ptr(), S, M, P)
-    _with_workspace((_lib or load_library()).diffattn_pages_compact, args, ws, dev, lambda: pages_workspace_bytes(S, P),
-                    "diffattn_pages_compact")
+    _check((_lib or load_library()).diffattn_pages_compact(*args, _raw_stream(dev.index)), "diffattn_pages_compact")
     return out
 
 
@@ -1076,11 +1061,11 @@ def beam_step(x, w_vocab, scores, pools: PagePools, table, lens, refs, finished=
     if not 0 < V <= w_vocab.shape[1]:
         raise ValueError("vocabulary must be at most w_vocab's columns")
     if ws is None:
-        ws = _serving_workspace(max(beam_workspace_bytes(B, K, V, K), pages_workspace_bytes(B * K, refs.shape[0])), dev)
+        ws = _serving_workspace(beam_workspace_bytes(B, K, V, K), dev)
     logits = gemm(x, w_vocab, out_dtype=torch.float32, ws=ws).view(B, K, -1)[..., :V]
     choice = diffattn_beam_select(logits, scores, None, finished, lengths, eos, length_penalty, out=choice, ws=ws)
     done = None if choice.finished is None else choice.finished.view(-1)
-    plan = diffattn_pages_fork(table, lens, refs, choice.parents, grow=1, done=done, out=plan, ws=ws)
+    plan = diffattn_pages_fork(table, lens, refs, choice.parents, grow=1, done=done, out=plan)
     diffattn_pages_copy(pools, plan.copies, plan.info)
     return choice, plan
 

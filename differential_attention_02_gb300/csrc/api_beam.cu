@@ -48,22 +48,6 @@ bool beam_layout(int B, int K, int V, int W, int in_dtype, BeamLayout* l) {
     return true;
 }
 
-// Workspace of the page plans: control block, four values a row, one a page.
-struct PageLayout {
-    size_t tail, prefix, first, copy_at, claim, total;
-};
-bool page_layout(int S, int P, PageLayout* l) {
-    if (S < 0 || S > kMaxPageRows || P < 1) return false;
-    const size_t row = round256((size_t)(S + 1) * sizeof(int32_t));
-    l->tail = kControlBytes;
-    l->prefix = l->tail + row;
-    l->first = l->prefix + row;
-    l->copy_at = l->first + row;
-    l->claim = l->copy_at + row;
-    l->total = l->claim + round256((size_t)P * sizeof(int32_t));
-    return true;
-}
-
 // Whether [a, a + n) and [b, b + m) share bytes.
 bool overlap(const void* a, size_t n, const void* b, size_t m) {
     const uintptr_t x = reinterpret_cast<uintptr_t>(a), y = reinterpret_cast<uintptr_t>(b);
@@ -171,24 +155,14 @@ diffattn_status diffattn_beam_reorder(const diffattn_beam_state* states, int cou
     return DIFFATTN_OK;
 }
 
-diffattn_status diffattn_pages_workspace_size(int rows, int num_pages, size_t* bytes) {
-    PageLayout l;
-    if (!bytes || !page_layout(rows, num_pages, &l)) return DIFFATTN_ERR_INVALID_ARG;
-    *bytes = l.total;
-    return DIFFATTN_OK;
-}
-
 diffattn_status diffattn_pages_fork(const int32_t* table, const int32_t* lens, const int32_t* refs,
                                     const int32_t* parents, const int32_t* new_lens, const uint8_t* done, int grow,
                                     int32_t* table_out, int32_t* lens_out, int32_t* refs_out, int32_t* copies,
-                                    int32_t* info, int B, int K, int max_pages, int num_pages, void* workspace,
-                                    size_t workspace_bytes, void* stream) {
+                                    int32_t* info, int B, int K, int max_pages, int num_pages, void* stream) {
     if (B < 0 || K < 1 || max_pages < 1 || num_pages < 1 || (int64_t)B * K > kMaxPageRows ||
         (int64_t)B * K * max_pages > INT32_MAX)
         return DIFFATTN_ERR_INVALID_ARG;
     const int S = B * K;
-    PageLayout l;
-    if (!page_layout(S, num_pages, &l)) return DIFFATTN_ERR_INVALID_ARG;
     for (const void* q : {(const void*)table, (const void*)lens, (const void*)table_out, (const void*)lens_out, (const void*)copies})
         if ((S > 0 && !q) || !aligned(q, 4)) return DIFFATTN_ERR_INVALID_ARG;
     for (const void* q : {(const void*)refs, (const void*)refs_out, (const void*)info})
@@ -196,27 +170,21 @@ diffattn_status diffattn_pages_fork(const int32_t* table, const int32_t* lens, c
     if (!aligned(parents, 4) || !aligned(new_lens, 4) || !apart_or_same(table, table_out, (int64_t)S * max_pages) ||
         !apart_or_same(lens, lens_out, S) || !apart_or_same(refs, refs_out, num_pages))
         return DIFFATTN_ERR_INVALID_ARG;
-    if (!workspace_ok(workspace, workspace_bytes, l.total)) return DIFFATTN_ERR_WORKSPACE;
-    uint8_t* ws = static_cast<uint8_t*>(workspace);
-    const auto at = [ws](size_t offset) { return reinterpret_cast<int32_t*>(ws + offset); };
     ForkParams p{};
     p.table = table; p.lens = lens; p.refs = refs; p.parents = parents; p.new_lens = new_lens; p.done = done;
     p.grow = grow;
     p.table_out = table_out; p.lens_out = lens_out; p.refs_out = refs_out; p.copies = copies; p.info = info;
     p.S = S; p.K = K; p.M = max_pages; p.P = num_pages;
-    p.tail = at(l.tail); p.prefix = at(l.prefix); p.first = at(l.first); p.copy_at = at(l.copy_at); p.claim = at(l.claim);
     return cuda_status(launch_pages_fork(p, static_cast<cudaStream_t>(stream)));
 }
 
 diffattn_status diffattn_pages_compact(const int32_t* table, const int32_t* lens, const int32_t* refs,
                                        int32_t* table_out, int32_t* refs_out, int32_t* moved, int32_t* copies,
                                        int max_copies, int32_t* info, int rows, int max_pages, int num_pages,
-                                       void* workspace, size_t workspace_bytes, void* stream) {
+                                       void* stream) {
     if (rows < 0 || rows > kMaxPageRows || max_pages < 1 || num_pages < 1 || max_copies < 0 || max_copies > num_pages / 2 ||
         (int64_t)rows * max_pages > INT32_MAX)
         return DIFFATTN_ERR_INVALID_ARG;
-    PageLayout l;
-    if (!page_layout(rows, num_pages, &l)) return DIFFATTN_ERR_INVALID_ARG;
     for (const void* q : {(const void*)refs, (const void*)refs_out, (const void*)moved, (const void*)info})
         if (!q || !aligned(q, 4)) return DIFFATTN_ERR_INVALID_ARG;
     if (rows > 0 && (!table || !lens || !table_out || !aligned(table, 4) || !aligned(lens, 4) || !aligned(table_out, 4) ||
@@ -224,14 +192,10 @@ diffattn_status diffattn_pages_compact(const int32_t* table, const int32_t* lens
         return DIFFATTN_ERR_INVALID_ARG;
     if ((max_copies > 0 && !copies) || !aligned(copies, 4) || !apart_or_same(refs, refs_out, num_pages))
         return DIFFATTN_ERR_INVALID_ARG;
-    if (!workspace_ok(workspace, workspace_bytes, l.total)) return DIFFATTN_ERR_WORKSPACE;
-    uint8_t* ws = static_cast<uint8_t*>(workspace);
     CompactParams p{};
     p.table = table; p.lens = lens; p.refs = refs;
     p.table_out = table_out; p.refs_out = refs_out; p.moved = moved; p.copies = copies; p.info = info;
     p.S = rows; p.M = max_pages; p.P = num_pages; p.max_copies = max_copies;
-    p.src = reinterpret_cast<int32_t*>(ws + l.claim);  // num_pages / 2 values each
-    p.dst = p.src + num_pages / 2;
     return cuda_status(launch_pages_compact(p, static_cast<cudaStream_t>(stream)));
 }
 

@@ -253,14 +253,12 @@ struct ForkParams {
     int grow;
     int32_t *table_out, *lens_out, *refs_out, *copies, *info;
     int S, K, M, P;                 // rows, rows of a group, columns, pages
-    int32_t *tail, *prefix, *first, *copy_at, *claim;         // workspace: [S], [S + 1], [S], [S], [P]
 };
 cudaError_t launch_pages_fork(const ForkParams& p, cudaStream_t stream);
 struct CompactParams {
     const int32_t *table, *lens, *refs;
     int32_t *table_out, *refs_out, *moved, *copies, *info;
     int S, M, P, max_copies;
-    int32_t *src, *dst;             // workspace: [max_copies] each
 };
 cudaError_t launch_pages_compact(const CompactParams& p, cudaStream_t stream);
 constexpr int kCopyPools = 48;      // of one launch

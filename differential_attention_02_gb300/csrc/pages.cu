@@ -4,9 +4,12 @@
 //
 // State: a table [S, M] of page numbers, the tokens of each row, and of each page the
 // number of its holders; a page without holders is free. Both planning kernels are one
-// block that passes over the table and the counts. Counts change by integer atomics,
-// whose order does not matter; free pages are handed out lowest first, to the rows in
-// order, so that equal states give equal results.
+// cluster of eight blocks: the table's columns and the pages are dealt to them, and they
+// meet at cluster barriers, which every thread reaches on every path. Counts change by
+// integer atomics, whose order does not matter; free pages are handed out lowest first,
+// to the rows in order, so that equal states give equal results.
+// They move a few hundred kilobytes and are bound by latencies, one after the other:
+// row lengths, table, counts, begun pages, free pages.
 #include <limits.h>
 
 #include "common.cuh"
@@ -17,6 +20,19 @@ namespace {
 
 constexpr int kPage = 64;
 constexpr int kPlanThreads = 1024;
+constexpr int kPlanBlocks = 8;  // of the cluster
+
+// All threads of the cluster; what they wrote before is seen behind it.
+__device__ __forceinline__ void cluster_sync() {
+    asm volatile("barrier.cluster.arrive.release;\n\tbarrier.cluster.wait.acquire;" ::: "memory");
+}
+// Writes v to the same place of shared memory in every block of the cluster.
+__device__ __forceinline__ void store_everywhere(int* place, int v) {
+    const uint32_t at = smem_u32(place);
+#pragma unroll
+    for (uint32_t b = 0; b < kPlanBlocks; ++b)
+        asm volatile("st.shared::cluster.u32 [%0], %1;" ::"r"(mapa_shared(at, b)), "r"(v) : "memory");
+}
 
 __device__ __forceinline__ int pages_of(int tokens) { return (int)(((int64_t)tokens + kPage - 1) / kPage); }
 
@@ -49,19 +65,12 @@ struct Row {  // what becomes of a row
     int tokens;  // tokens after
     int over;    // pages wanted beyond the table's columns
 };
-__device__ __forceinline__ int row_tokens(const ForkParams& p, int i) {
-    return min(max(p.lens[i], 0), (int)min((int64_t)p.M * kPage, (int64_t)INT_MAX));
-}
-__device__ __forceinline__ Row row_after(const ForkParams& p, int i) {
-    const bool done = p.done && p.done[i];
-    int parent = i;
-    if (p.parents) {
-        const int k = p.parents[i];
-        parent = k < 0 || k >= p.K ? -1 : i / p.K * p.K + k;
-    }
+// `lens`: the rows' lengths, clamped to the table.
+__device__ __forceinline__ Row row_after(const ForkParams& p, const int* lens, int i, int parent, int new_len, bool done) {
+    parent = !p.parents ? i : parent < 0 || parent >= p.K ? -1 : i / p.K * p.K + parent;
     if (done) parent = -1;
-    const int before = parent < 0 ? 0 : row_tokens(p, parent);
-    int64_t want = p.new_lens ? p.new_lens[i] : parent < 0 ? 0 : (int64_t)before + p.grow;
+    const int before = parent < 0 ? 0 : lens[parent];
+    int64_t want = p.new_lens ? new_len : parent < 0 ? 0 : (int64_t)before + p.grow;
     if (done || want < 0) want = 0;
     const int64_t most = min((int64_t)p.M * kPage, (int64_t)INT_MAX);
     Row r;
@@ -72,131 +81,191 @@ __device__ __forceinline__ Row row_after(const ForkParams& p, int i) {
     return r;
 }
 
-__global__ void __launch_bounds__(kPlanThreads) pages_fork_kernel(const __grid_constant__ ForkParams p, int cols) {
+// Shared memory: five values a row, and a place for columns of all rows, later for the begun pages' table (at least
+// two places a row, a power of two) and what the rows need.
+__host__ __device__ constexpr int claim_places(int S) {
+    int n = 64;
+    while (n < 2 * S) n *= 2;
+    return n;
+}
+constexpr int kColumns = 8;  // of a row, read together: 32 bytes
+__host__ __device__ constexpr size_t fork_bytes(int S, int tiles) {
+    const size_t columns = (size_t)S * tiles * kColumns * 4, rest = ((size_t)claim_places(S) * 2 + 2 * (size_t)S + 1) * 4;
+    return (size_t)S * 20 + (columns > rest ? columns : rest);
+}
+
+__global__ void __launch_bounds__(kPlanThreads) pages_fork_kernel(const __grid_constant__ ForkParams p, int tiles) {
     extern __shared__ int shared[];
     __shared__ int scan[32];
     __shared__ int s_over;
-    int* parent = shared;         // [S] each
+    __shared__ int s_free[kPlanBlocks];
+    int* lens = shared;            // [S] each
+    int* parent = lens + p.S;
     int* kept = parent + p.S;
     int* tokens = kept + p.S;
-    int* held = tokens + p.S;     // pages of the old row
-    int* stage = held + p.S;      // [S][cols]
-    const int tid = threadIdx.x;
+    int* tail = tokens + p.S;      // the page that a row begins with half full, or -1
+    int* stage = tail + p.S;       // [S][tiles][8]
+    const int places = claim_places(p.S);
+    int* claim_page = stage;       // behind the columns
+    int* claim_row = claim_page + places;
+    int* prefix = claim_row + places;  // [S + 1]: entries that the rows before need
+    int* copy_at = prefix + p.S + 1;   // [S]: a row's place among the copies, or -1
+    const int tid = threadIdx.x, rank = (int)cluster_ctarank();
+    pdl_trigger();  // the copies' blocks may start, and wait for the plan
     if (tid == 0) s_over = 0;
+
+    const int most = (int)min((int64_t)p.M * kPage, (int64_t)INT_MAX);
+    for (int i = tid; i < p.S; i += kPlanThreads) {
+        lens[i] = min(max(p.lens[i], 0), most);
+        parent[i] = p.parents ? p.parents[i] : i;
+        kept[i] = p.new_lens ? p.new_lens[i] : 0;
+        tokens[i] = p.done ? p.done[i] : 0;
+        tail[i] = -1;
+    }
+    const int share = (p.P + kPlanBlocks - 1) / kPlanBlocks, page0 = min(rank * share, p.P), page1 = min(page0 + share, p.P);
+    if (p.refs_out != p.refs)
+        for (int i = page0 + tid; i < page1; i += kPlanThreads) p.refs_out[i] = p.refs[i];
     __syncthreads();
     for (int i = tid; i < p.S; i += kPlanThreads) {
-        const Row r = row_after(p, i);
+        const Row r = row_after(p, lens, i, parent[i], kept[i], tokens[i] != 0);
         parent[i] = r.parent;
         kept[i] = r.kept;
         tokens[i] = r.tokens;
-        held[i] = pages_of(row_tokens(p, i));
-        p.tail[i] = -1;
         if (r.over) atomicAdd(&s_over, r.over);
     }
-    for (int i = tid; i < p.P; i += kPlanThreads) p.refs_out[i] = p.refs[i];
-    __syncthreads();
-    for (int i = tid; i < p.S; i += kPlanThreads) p.lens_out[i] = tokens[i];  // lens may be the same array
+    cluster_sync();  // counts are there to be changed, and every block has read the lengths
+    if (rank == 0)
+        for (int i = tid; i < p.S; i += kPlanThreads) p.lens_out[i] = tokens[i];
 
-    // Columns of all rows through shared memory: the table may be rewritten in place, and the counts
-    // follow the pages that rows lose and gain. What a row keeps of itself changes nothing.
-    for (int c0 = 0; c0 < p.M; c0 += cols) {
-        const int n = min(cols, p.M - c0);
-        for (int t = tid; t < p.S * n; t += kPlanThreads) {
-            const int i = t / n, c = c0 + t % n;
-            const int page = c < held[i] ? p.table[(int64_t)i * p.M + c] : -1;
-            stage[t] = page >= 0 && page < p.P ? page : -1;
+    // Columns of all rows through shared memory, eight at a time and dealt to the blocks: the table may be rewritten
+    // in place, and the counts follow the pages that rows lose and gain. What a row keeps of itself changes nothing.
+    const int all_tiles = (p.M + kColumns - 1) / kColumns, j = tid % kColumns;
+    for (int first = rank; first < all_tiles; first += kPlanBlocks * tiles) {
+        const int n = min(tiles, (all_tiles - first + kPlanBlocks - 1) / kPlanBlocks);
+        for (int t = tid / kColumns; t < p.S * n; t += kPlanThreads / kColumns) {
+            const int i = t / n, c = (first + t % n * kPlanBlocks) * kColumns + j;
+            const int page = c < pages_of(lens[i]) ? p.table[(int64_t)i * p.M + c] : -1;
+            stage[t * kColumns + j] = page >= 0 && page < p.P ? page : -1;
         }
         __syncthreads();
-        for (int t = tid; t < p.S * n; t += kPlanThreads) {
-            const int i = t / n, j = t % n, c = c0 + j, from = parent[i], full = kept[i] / kPage;
-            const int got = from >= 0 && c < full ? stage[from * n + j] : -1;
+        for (int t = tid / kColumns; t < p.S * n; t += kPlanThreads / kColumns) {
+            const int i = t / n, c = (first + t % n * kPlanBlocks) * kColumns + j, from = parent[i], full = kept[i] / kPage;
+            if (c >= p.M) continue;
+            const int old = stage[t * kColumns + j], taken = from >= 0 ? stage[(from * n + t % n) * kColumns + j] : -1;
+            const int got = c < full ? taken : -1;
             const bool same = from == i && c < full;
             p.table_out[(int64_t)i * p.M + c] = got;
-            if (stage[t] >= 0 && !same) atomicAdd(&p.refs_out[stage[t]], -1);
+            if (old >= 0 && !same) atomicAdd(&p.refs_out[old], -1);
             if (got >= 0 && !same) atomicAdd(&p.refs_out[got], 1);
-            if (from >= 0 && c == full && kept[i] % kPage) p.tail[i] = stage[from * n + j];
+            if (c == full && kept[i] % kPage && taken >= 0) store_everywhere(&tail[i], taken);
         }
         __syncthreads();
     }
+    for (int i = tid; i < places; i += kPlanThreads) {
+        claim_page[i] = -1;
+        claim_row[i] = INT_MAX;
+    }
+    cluster_sync();  // the counts without the begun pages, and the begun pages
 
-    // The begun page stays with the first row that has it, if it has no other holder.
-    for (int i = tid; i < p.S; i += kPlanThreads)
-        if (__ldcg(&p.tail[i]) >= 0) p.claim[__ldcg(&p.tail[i])] = INT_MAX;
-    __syncthreads();
-    for (int i = tid; i < p.S; i += kPlanThreads)
-        if (__ldcg(&p.tail[i]) >= 0) atomicMin(&p.claim[__ldcg(&p.tail[i])], i);
+    // The begun page stays with the first row that has it, if it has no other holder. Every block finds that out for
+    // itself: the rows' pages in a table by their low bits, with the lowest row of each.
+    for (int i = tid; i < p.S; i += kPlanThreads) {
+        const int t = tail[i];
+        if (t < 0) continue;
+        int at = t & (places - 1);
+        for (int k = 0; k < places; ++k, at = (at + 1) & (places - 1)) {  // (a place is free for every row)
+            const int there = atomicCAS(&claim_page[at], -1, t);
+            if (there == -1 || there == t) break;
+        }
+        atomicMin(&claim_row[at], i);
+    }
     __syncthreads();
     int base = 0, copies = 0;
     for (int i0 = 0; i0 < p.S; i0 += kPlanThreads) {
         const int i = i0 + tid;
         int need = 0, copy = 0;
         if (i < p.S) {
-            const int t = __ldcg(&p.tail[i]), full = kept[i] / kPage;
-            const bool stays = t >= 0 && __ldcg(&p.claim[t]) == i && __ldcg(&p.refs_out[t]) <= 0;
-            copy = t >= 0 && !stays;
-            need = pages_of(tokens[i]) - full - stays;
-            p.first[i] = full + stays;
+            const int t = tail[i];
+            bool stays = false;
+            if (t >= 0) {
+                int at = t & (places - 1);
+                for (int k = 0; k < places && claim_page[at] != t; ++k) at = (at + 1) & (places - 1);
+                stays = claim_row[at] == i && __ldcg(&p.refs_out[t]) <= 0;
+                copy = !stays;
+            }
+            need = pages_of(tokens[i]) - kept[i] / kPage - stays;
+            if (stays) tail[i] = ~t - 1;  // (below -1)
         }
         int total, total_copies;
-        const int at = block_scan(need, scan, &total), copy_at = block_scan(copy, scan, &total_copies);
+        const int at = block_scan(need, scan, &total), at_copy = block_scan(copy, scan, &total_copies);
         if (i < p.S) {
-            p.prefix[i] = base + at;
-            p.copy_at[i] = copy ? copies + copy_at : -1;
+            prefix[i] = base + at;
+            copy_at[i] = copy ? copies + at_copy : -1;
         }
         base += total;
         copies += total_copies;
     }
-    __syncthreads();  // all claims have seen the counts
+    const int wanted = base;
+    cluster_sync();  // every block has seen the counts
     for (int i = tid; i < p.S; i += kPlanThreads) {
-        const int full = kept[i] / kPage;
-        if (__ldcg(&p.first[i]) > full) {
-            const int t = __ldcg(&p.tail[i]);
+        if (tail[i] >= -1) continue;
+        const int t = ~(tail[i] + 1);
+        if (t >= page0 && t < page1) {  // its page's block
             p.refs_out[t] = 1;
-            p.table_out[(int64_t)i * p.M + full] = t;
+            p.table_out[(int64_t)i * p.M + kept[i] / kPage] = t;
         }
     }
     __syncthreads();
 
-    // Free pages, lowest first, to the entries that need one, in the rows' order.
-    const int wanted = base;
+    // Free pages, lowest first, to the entries that need one, in the rows' order: each block knows its own and, from
+    // the others, how many lie before them. A thread has pages side by side.
+    const int each = (share + kPlanThreads - 1) / kPlanThreads;
+    const int first_page = min(page0 + tid * each, page1), last_page = min(first_page + each, page1);
+    int mine = 0;
+    for (int i = first_page; i < last_page; ++i) mine += __ldcg(&p.refs_out[i]) <= 0;
+    int total;
+    int number = block_scan(mine, scan, &total);
+    if (tid == 0) store_everywhere(&s_free[rank], total);
+    cluster_sync();
     int free_pages = 0;
-    for (int p0 = 0; p0 < p.P; p0 += kPlanThreads) {
-        const int page = p0 + tid;
-        const int count = page < p.P ? __ldcg(&p.refs_out[page]) : 1;
-        int total;
-        const int number = free_pages + block_scan(count <= 0, scan, &total);
-        if (count <= 0) {
+    for (int i = 0; i < kPlanBlocks; ++i) {
+        number += i < rank ? s_free[i] : 0;
+        free_pages += s_free[i];
+    }
+    if (mine > 0) {
+        for (int i = first_page; i < last_page; ++i) {
+            const int count = __ldcg(&p.refs_out[i]);
+            if (count > 0) continue;
             if (number < wanted) {
                 int lo = 0, hi = p.S - 1;  // the last row whose entries begin at or before `number`
                 while (lo < hi) {
                     const int mid = (lo + hi + 1) / 2;
-                    if (__ldcg(&p.prefix[mid]) <= number) lo = mid;
+                    if (prefix[mid] <= number) lo = mid;
                     else hi = mid - 1;
                 }
-                const int begin = __ldcg(&p.prefix[lo]), first = __ldcg(&p.first[lo]);
-                p.table_out[(int64_t)lo * p.M + first + (number - begin)] = page;
-                p.refs_out[page] = 1;
-                const int at = __ldcg(&p.copy_at[lo]);
-                if (number == begin && at >= 0) {
-                    p.copies[3 * at] = __ldcg(&p.tail[lo]);
-                    p.copies[3 * at + 1] = page;
-                    p.copies[3 * at + 2] = kept[lo] % kPage;
+                const int nth = number - prefix[lo], start = kept[lo] / kPage + (tail[lo] < -1);
+                p.table_out[(int64_t)lo * p.M + start + nth] = i;
+                p.refs_out[i] = 1;
+                if (nth == 0 && copy_at[lo] >= 0) {
+                    int* copy = p.copies + 3 * copy_at[lo];
+                    copy[0] = tail[lo];
+                    copy[1] = i;
+                    copy[2] = kept[lo] % kPage;
                 }
             } else if (count < 0) {
-                p.refs_out[page] = 0;
+                p.refs_out[i] = 0;
             }
+            ++number;
         }
-        free_pages += total;
     }
+    if (rank > 0) return;
     // The copies whose page was found come first, in the rows' order.
     int done = 0;
     for (int i0 = 0; i0 < p.S; i0 += kPlanThreads) {
         const int i = i0 + tid;
-        int total;
-        block_scan(i < p.S && __ldcg(&p.copy_at[i]) >= 0 && __ldcg(&p.prefix[i]) < free_pages, scan, &total);
-        done += total;
+        done += __syncthreads_count(i < p.S && copy_at[i] >= 0 && prefix[i] < free_pages);
     }
-    for (int i = done + tid; i < p.S; i += kPlanThreads) p.copies[3 * i] = p.copies[3 * i + 1] = p.copies[3 * i + 2] = -1;
+    for (int i = 3 * done + tid; i < 3 * p.S; i += kPlanThreads) p.copies[i] = -1;
     if (tid == 0) {
         const int given = min(wanted, free_pages);
         p.info[0] = done;
@@ -208,52 +277,61 @@ __global__ void __launch_bounds__(kPlanThreads) pages_fork_kernel(const __grid_c
 
 __global__ void __launch_bounds__(kPlanThreads) pages_compact_kernel(const __grid_constant__ CompactParams p) {
     __shared__ int scan[32];
-    const int tid = threadIdx.x;
+    __shared__ int s_used[kPlanBlocks], s_behind[kPlanBlocks];
+    const int tid = threadIdx.x, rank = (int)cluster_ctarank();
+    const int share = (p.P + kPlanBlocks - 1) / kPlanBlocks, page0 = min(rank * share, p.P), page1 = min(page0 + share, p.P);
+    const int each = (share + kPlanThreads - 1) / kPlanThreads;  // a thread has pages side by side
+    const int first_page = min(page0 + tid * each, page1), last_page = min(first_page + each, page1);
+    pdl_trigger();
+    int mine = 0, total;
+    for (int i = first_page; i < last_page; ++i) mine += p.refs[i] > 0;
+    int below = block_scan(mine, scan, &total);
+    if (tid == 0) store_everywhere(&s_used[rank], total);
+    cluster_sync();
     int used = 0;
-    for (int p0 = 0; p0 < p.P; p0 += kPlanThreads) {
-        int total;
-        block_scan(p0 + tid < p.P && p.refs[p0 + tid] > 0, scan, &total);
-        used += total;
+    for (int i = 0; i < kPlanBlocks; ++i) {
+        below += i < rank ? s_used[i] : 0;
+        used += s_used[i];
     }
     // The i-th highest held page behind place `used` moves to the i-th lowest free one before it.
-    int below = 0, behind = 0;  // held pages before this place; of them behind place `used`
-    for (int p0 = 0; p0 < p.P; p0 += kPlanThreads) {
-        const int page = p0 + tid;
-        const int count = page < p.P ? p.refs[page] : 0;
+    int behind = 0;
+    for (int i = first_page; i < last_page; ++i) {
+        const int count = p.refs[i];
         const bool held = count > 0;
-        int total;
-        const int at = below + block_scan(held, scan, &total);
-        if (page < p.P) {
-            p.refs_out[page] = held ? count : 0;
-            p.moved[page] = held ? page : -1;
-            if (held && page >= used && used - 1 - at < p.max_copies) p.src[used - 1 - at] = page;
-            if (!held && page < used && page - at < p.max_copies) p.dst[page - at] = page;
+        p.refs_out[i] = held ? count : 0;
+        p.moved[i] = held ? i : -1;
+        if (held && i >= used) {
+            ++behind;
+            if (used - 1 - below < p.max_copies) p.copies[3 * (used - 1 - below)] = i;
         }
-        below += total;
-        block_scan(held && page >= used, scan, &total);
-        behind += total;
+        if (!held && i < used && i - below < p.max_copies) p.copies[3 * (i - below) + 1] = i;
+        below += held;
     }
-    __syncthreads();
-    const int moves = min(behind, p.max_copies);
-    for (int i = tid; i < p.max_copies; i += kPlanThreads) {
+    block_scan(behind, scan, &total);
+    if (tid == 0) store_everywhere(&s_behind[rank], total);
+    cluster_sync();
+    int moves = 0;
+    for (int i = 0; i < kPlanBlocks; ++i) moves += s_behind[i];
+    moves = min(moves, p.max_copies);
+    for (int i = rank * kPlanThreads + tid; i < p.max_copies; i += kPlanBlocks * kPlanThreads) {
         const bool some = i < moves;
-        const int src = some ? p.src[i] : -1, dst = some ? p.dst[i] : -1;
-        p.copies[3 * i] = src;
-        p.copies[3 * i + 1] = dst;
         p.copies[3 * i + 2] = some ? kPage : -1;
-        if (some) {
+        if (!some) {
+            p.copies[3 * i] = p.copies[3 * i + 1] = -1;
+        } else {
+            const int src = __ldcg(&p.copies[3 * i]), dst = __ldcg(&p.copies[3 * i + 1]);
             p.moved[src] = dst;
-            p.refs_out[dst] = p.refs_out[src];
+            p.refs_out[dst] = __ldcg(&p.refs_out[src]);
             p.refs_out[src] = 0;
         }
     }
-    __syncthreads();
-    for (int64_t t = tid; t < (int64_t)p.S * p.M; t += kPlanThreads) {
+    cluster_sync();
+    for (int64_t t = rank * kPlanThreads + tid; t < (int64_t)p.S * p.M; t += kPlanBlocks * kPlanThreads) {
         const int i = (int)(t / p.M), c = (int)(t % p.M);
         const int page = c < pages_of(max(p.lens[i], 0)) ? p.table[t] : -1;
-        p.table_out[t] = page >= 0 && page < p.P ? p.moved[page] : -1;
+        p.table_out[t] = page >= 0 && page < p.P ? __ldcg(&p.moved[page]) : -1;
     }
-    if (tid == 0) {
+    if (rank == 0 && tid == 0) {
         p.info[0] = moves;
         p.info[1] = 0;
         p.info[2] = p.P - used;
@@ -261,10 +339,14 @@ __global__ void __launch_bounds__(kPlanThreads) pages_compact_kernel(const __gri
     }
 }
 
-// grid.x: blocks over (copy, head); grid.y: pools.
+// grid.x: blocks over (copy, head); grid.y: pools. A block moves the rows of one head of a page, four vectors a thread
+// on their way at once. It starts beside the plan that lists the copies (dependent launch).
+constexpr int kCopyBatch = 4;
 __global__ void __launch_bounds__(256) pages_copy_kernel(const __grid_constant__ CopyParams p) {
     const CopyPool& pool = p.pool[blockIdx.y];
+    pdl_wait();
     const int n = p.count ? min(max(*p.count, 0), p.max_copies) : p.max_copies;
+    const bool packed = pool.stride_row == (int64_t)pool.row_vecs * 16;  // rows follow one another
     for (int64_t u = blockIdx.x; u < (int64_t)n * pool.heads; u += gridDim.x) {
         const int64_t i = u / pool.heads;
         const int head = (int)(u % pool.heads);
@@ -272,28 +354,53 @@ __global__ void __launch_bounds__(256) pages_copy_kernel(const __grid_constant__
         if (src < 0 || src >= p.P || dst < 0 || dst >= p.P || src == dst) continue;
         const uint8_t* from = pool.ptr + src * pool.stride_page + head * pool.stride_head;
         uint8_t* to = pool.ptr + dst * pool.stride_page + head * pool.stride_head;
-        for (int t = threadIdx.x; t < rows * pool.row_vecs; t += 256) {
-            const int64_t at = (t / pool.row_vecs) * pool.stride_row + (t % pool.row_vecs) * 16;
-            *reinterpret_cast<uint4*>(to + at) = *reinterpret_cast<const uint4*>(from + at);
+        for (int t0 = threadIdx.x; t0 < rows * pool.row_vecs; t0 += 256 * kCopyBatch) {
+            uint4 v[kCopyBatch];
+            int64_t at[kCopyBatch];
+#pragma unroll
+            for (int k = 0; k < kCopyBatch; ++k) {
+                const int t = t0 + k * 256;
+                at[k] = packed ? (int64_t)t * 16 : (t / pool.row_vecs) * pool.stride_row + (t % pool.row_vecs) * 16;
+                if (t < rows * pool.row_vecs) v[k] = *reinterpret_cast<const uint4*>(from + at[k]);
+            }
+#pragma unroll
+            for (int k = 0; k < kCopyBatch; ++k)
+                if (t0 + k * 256 < rows * pool.row_vecs) *reinterpret_cast<uint4*>(to + at[k]) = v[k];
         }
     }
 }
 
 }  // namespace
 
+// A planning kernel: one cluster.
+template <typename... KArgs, typename... Args>
+cudaError_t launch_plan(void (*kernel)(KArgs...), size_t smem, cudaStream_t stream, Args... args) {
+    cudaLaunchConfig_t cfg = {};
+    cfg.gridDim = dim3(kPlanBlocks);
+    cfg.blockDim = dim3(kPlanThreads);
+    cfg.dynamicSmemBytes = smem;
+    cfg.stream = stream;
+    cudaLaunchAttribute attr[1];
+    attr[0].id = cudaLaunchAttributeClusterDimension;
+    attr[0].val.clusterDim.x = kPlanBlocks;
+    attr[0].val.clusterDim.y = attr[0].val.clusterDim.z = 1;
+    cfg.attrs = attr;
+    cfg.numAttrs = 1;
+    return cudaLaunchKernelEx(&cfg, kernel, args...);
+}
+
 cudaError_t launch_pages_fork(const ForkParams& p, cudaStream_t stream) {
-    // Rows of 16 bytes in shared memory, and columns for up to 96 KB beside them.
-    const int cols = p.S == 0 ? 1 : p.S * 8 > 24576 ? 8 : min(p.M, 24576 / p.S);
-    const size_t smem = (size_t)p.S * (16 + 4 * cols);
-    cudaError_t e = prepare_once<pages_fork_kernel>(200 * 1024);
+    // A block's columns at once, or as many as 128 KB hold (at 4096 rows: eight).
+    const int all = (p.M + kColumns * kPlanBlocks - 1) / (kColumns * kPlanBlocks);
+    const int room = p.S == 0 ? all : 131072 / (p.S * kColumns * 4);
+    const int tiles = room < 1 ? 1 : all < room ? all : room;
+    cudaError_t e = prepare_once<pages_fork_kernel>((int)fork_bytes(kMaxPageRows, 1));
     if (e != cudaSuccess) return e;
-    pages_fork_kernel<<<1, kPlanThreads, smem, stream>>>(p, cols);
-    return cudaGetLastError();
+    return launch_plan(pages_fork_kernel, fork_bytes(p.S, tiles), stream, p, tiles);
 }
 
 cudaError_t launch_pages_compact(const CompactParams& p, cudaStream_t stream) {
-    pages_compact_kernel<<<1, kPlanThreads, 0, stream>>>(p);
-    return cudaGetLastError();
+    return launch_plan(pages_compact_kernel, 0, stream, p);
 }
 
 cudaError_t launch_pages_copy(const CopyParams& p, int pools, cudaStream_t stream) {
@@ -304,8 +411,7 @@ cudaError_t launch_pages_copy(const CopyParams& p, int pools, cudaStream_t strea
     for (int i = 0; i < pools; ++i) heads = p.pool[i].heads > heads ? p.pool[i].heads : heads;
     const int64_t units = (int64_t)p.max_copies * heads, most = (int64_t)sms * 8;
     const dim3 grid((unsigned)(units < most ? units : most), (unsigned)pools);
-    pages_copy_kernel<<<grid, 256, 0, stream>>>(p);
-    return cudaGetLastError();
+    return launch_pdl(pages_copy_kernel, grid, dim3(256), 0, stream, p);
 }
 
 }  // namespace da

@@ -537,27 +537,23 @@ diffattn_status diffattn_beam_reorder(const diffattn_beam_state* states, int cou
  *   (pool or table full; their entries are -1, which appends skip and attention reads as zeros), free
  *   pages and held pages after the call.
  * Table entries outside [0, num_pages) hold nothing. B K <= 4096 (0: the counts and info alone).
- * workspace: diffattn_pages_workspace_size(B K, num_pages) bytes, 256-byte aligned, for one call at a time.
  */
 diffattn_status diffattn_pages_fork(const int32_t* table, const int32_t* lens, const int32_t* refs,
                                     const int32_t* parents, const int32_t* new_lens, const uint8_t* done, int grow,
                                     int32_t* table_out, int32_t* lens_out, int32_t* refs_out, int32_t* copies,
-                                    int32_t* info, int B, int K, int max_pages, int num_pages, void* workspace,
-                                    size_t workspace_bytes, void* stream);
+                                    int32_t* info, int B, int K, int max_pages, int num_pages, void* stream);
 
 /*
  * diffattn_pages_compact — the held pages moved to the front of the pool: the i-th highest held page goes
  * to the i-th lowest free place before it, max_copies (<= num_pages / 2) of them at most. The table's
  * rows and the counts follow; `moved` [num_pages] tells other holders each page's new place (-1: it was free).
  * copies: int32 [max_copies, 3] for diffattn_pages_copy, -1 behind the last; info: int32 [4]: copies, 0, free and
- *   held pages. table_out and refs_out as for diffattn_pages_fork (rows 0: the counts alone). Workspace:
- *   diffattn_pages_workspace_size(rows, num_pages).
+ *   held pages. table_out and refs_out as for diffattn_pages_fork (rows 0: the counts alone).
  */
 diffattn_status diffattn_pages_compact(const int32_t* table, const int32_t* lens, const int32_t* refs,
                                        int32_t* table_out, int32_t* refs_out, int32_t* moved, int32_t* copies,
                                        int max_copies, int32_t* info, int rows, int max_pages, int num_pages,
-                                       void* workspace, size_t workspace_bytes, void* stream);
-diffattn_status diffattn_pages_workspace_size(int rows, int num_pages, size_t* bytes);
+                                       void* stream);
 
 /* One tensor of pages [num_pages][heads][64][row_bytes]: K1, K2 or V pages of a layer. Strides in bytes; address,
  * strides and row_bytes multiples of 16. */

@@ -43,10 +43,7 @@ def test_workspace_sizes(lib):
     n = ctypes.c_size_t()
     assert lib.diffattn_beam_workspace_size(2, 4, 1000, 8, None) == da.ERR_INVALID_ARG
     assert lib.diffattn_beam_workspace_size(2, 33, 1000, 8, ctypes.byref(n)) == da.ERR_INVALID_ARG
-    assert lib.diffattn_pages_workspace_size(4097, 10, ctypes.byref(n)) == da.ERR_INVALID_ARG
-    assert lib.diffattn_pages_workspace_size(4, 0, ctypes.byref(n)) == da.ERR_INVALID_ARG
-    assert da.beam_workspace_bytes(0, 1, 1, 1) >= 256 and da.pages_workspace_bytes(0, 1) >= 256
-    assert da.beam_workspace_bytes(64, 8, 1000, 16) >= 512 * 16 * 8 and da.pages_workspace_bytes(10, 9000) >= 36000
+    assert da.beam_workspace_bytes(0, 1, 1, 1) >= 256 and da.beam_workspace_bytes(64, 8, 1000, 16) >= 512 * 16 * 8
 
 
 def _state(**kw):
@@ -68,7 +65,7 @@ def test_reorder_refusals(lib):
 
 def _fork(lib, **kw):
     a = dict(table=0x10000, lens=0x20000, refs=0x30000, parents=0x40000, new=None, done=None, grow=1, to=0x50000, lo=0x60000, ro=0x70000,
-             copies=0x80000, info=0x90000, B=2, K=4, M=16, P=100, ws=0x100000, wsb=1 << 30)
+             copies=0x80000, info=0x90000, B=2, K=4, M=16, P=100)
     a.update(kw)
     return lib.diffattn_pages_fork(*a.values(), None)
 
@@ -78,22 +75,18 @@ def test_fork_refusals(lib):
                dict(to=None), dict(lo=None), dict(ro=None), dict(copies=None), dict(info=None), dict(table=0x10002), dict(parents=0x40001),
                dict(new=0x40002), dict(to=0x10004), dict(lo=0x20004), dict(ro=0x30004), dict(ro=0x30000 - 396)):
         assert _fork(lib, **kw) == da.ERR_INVALID_ARG, kw
-    for kw in (dict(ws=None), dict(ws=0x100040), dict(wsb=500)):
-        assert _fork(lib, **kw) == da.ERR_WORKSPACE, kw
 
 
 def test_compact_refusals(lib):
     def call(**kw):
         a = dict(table=0x10000, lens=0x20000, refs=0x30000, to=0x50000, ro=0x70000, moved=0x80000, copies=0x90000, most=50, info=0xa0000,
-                 S=8, M=16, P=100, ws=0x100000, wsb=1 << 30)
+                 S=8, M=16, P=100)
         a.update(kw)
         return lib.diffattn_pages_compact(*a.values(), None)
     for kw in (dict(S=-1), dict(S=4097), dict(M=0), dict(P=0), dict(most=-1), dict(most=51), dict(table=None), dict(lens=None), dict(refs=None),
                dict(to=None), dict(ro=None), dict(moved=None), dict(copies=None), dict(info=None), dict(to=0x10004), dict(ro=0x30008),
                dict(moved=0x80001)):
         assert call(**kw) == da.ERR_INVALID_ARG, kw
-    for kw in (dict(ws=None), dict(wsb=300)):
-        assert call(**kw) == da.ERR_WORKSPACE, kw
 
 
 def test_copy_refusals(lib):
@@ -114,7 +107,8 @@ ELSEWHERE = torch.device("meta")  # another device than the operands', without m
 @pytest.fixture
 def no_launch(monkeypatch):
     monkeypatch.setattr(da, "_elsewhere", lambda dev, stream: None)
-    monkeypatch.setattr(da, "_with_workspace", lambda *a: pytest.fail("launched"))
+    monkeypatch.setattr(da, "_check", lambda *a: pytest.fail("launched"))
+    monkeypatch.setattr(da, "_raw_stream", lambda index: pytest.fail("launched"))
 
 
 def test_select_checks_its_tensors(no_launch):
