@@ -851,6 +851,7 @@ def diffattn_beam_select(logits, scores, width: int | None = None, finished=None
 
 
 _PACK_STATE = struct.Struct("=4q4i").pack
+_REORDER_ROW = 1 << 20
 
 
 def diffattn_beam_reorder(states, parents, lens=None, stream=None):
@@ -883,17 +884,21 @@ def diffattn_beam_reorder(states, parents, lens=None, stream=None):
                 raise ValueError("states must not overlap themselves")
             packed.append(_PACK_STATE(t.data_ptr(), strides[0] * size, strides[1] * size, strides[2] * size, parts, rows, width * size, 1))
         else:
-            n = t[0].numel() if t.shape[0] else 0
-            if t.shape[0] and (not t[0].is_contiguous() or (B * K > 1 and strides[0] < n)):
-                raise ValueError("the rows of states must be contiguous")
-            # long rows in parts of a MiB or less, so that their sizes stay within 31 bits
-            whole, row = n * size, 1 << 20
-            if whole <= row:
-                packed.append(_PACK_STATE(t.data_ptr(), strides[0] * size, 0, 0, 1, 1, whole, 0))
+            if t.is_contiguous():
+                whole = (t.numel() // max(B * K, 1)) * size
             else:
-                packed.append(_PACK_STATE(t.data_ptr(), strides[0] * size, 0, row, 1, whole // row, row, 0))
-                if whole % row:
-                    packed.append(_PACK_STATE(t.data_ptr() + whole // row * row, strides[0] * size, 0, 0, 1, 1, whole % row, 0))
+                if not t[:1].is_contiguous() or strides[0] < t[:1].numel():
+                    raise ValueError("the rows of states must be contiguous and not overlap")
+                whole = t[:1].numel() * size
+            # long rows in parts of a MiB, so that their sizes stay within 31 bits
+            step, at = strides[0] * size, t.data_ptr()
+            if whole <= _REORDER_ROW:
+                packed.append(_PACK_STATE(at, step, 0, 0, 1, 1, whole, 0))
+            else:
+                n = whole // _REORDER_ROW
+                packed.append(_PACK_STATE(at, step, _REORDER_ROW, 0, n, 1, _REORDER_ROW, 0))
+                if whole % _REORDER_ROW:
+                    packed.append(_PACK_STATE(at + n * _REORDER_ROW, step, 0, 0, 1, 1, whole % _REORDER_ROW, 0))
     _check((_lib or load_library()).diffattn_beam_reorder(b"".join(packed), len(packed), parents.data_ptr(),
                                                           None if lens is None else lens.data_ptr(), B, K, _raw_stream(dev.index)),
            "diffattn_beam_reorder")

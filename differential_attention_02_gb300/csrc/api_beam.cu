@@ -122,8 +122,9 @@ diffattn_status diffattn_beam_reorder(const diffattn_beam_state* states, int cou
         if (s.parts < 0 || s.rows < 0 || s.row_bytes < 0 || s.stride_state < 0 || s.stride_part < 0 || s.stride_row < 0)
             return DIFFATTN_ERR_INVALID_ARG;
         if (s.by_len && !lens) return DIFFATTN_ERR_INVALID_ARG;
-        // 2^39 units at most: 2^31 blocks of a thread each
-        if ((double)s.parts * s.rows * s.row_bytes > 0x1p38) return DIFFATTN_ERR_INVALID_ARG;
+        // units of a part, and blocks of all groups, within 31 bits
+        const int64_t part = (int64_t)s.rows * s.row_bytes;
+        if (part > INT32_MAX / 2 || (part / 128 + 1) * B > INT32_MAX) return DIFFATTN_ERR_INVALID_ARG;
         if (s.parts && s.rows && s.row_bytes && !s.ptr) return DIFFATTN_ERR_INVALID_ARG;
     }
     if (B == 0 || count == 0) return DIFFATTN_OK;

@@ -240,7 +240,7 @@ struct ReorderState {
 struct ReorderParams {
     ReorderState state[kReorderStates];
     const int32_t *parents, *lens;               // [B, K]; lens [B K] or null
-    int B, K;
+    int B, K, blocks;                            // blocks of a group's part (set by the launch)
 };
 // `unit`: bytes moved at a time (16, 4, 2 or 1), `count` states.
 cudaError_t launch_beam_reorder(const ReorderParams& p, int unit, int count, cudaStream_t stream);

@@ -59,7 +59,7 @@ def test_reorder_refusals(lib):
     for kw in (dict(B=-1), dict(B=65536), dict(K=0), dict(K=33), dict(count=-1), dict(null=True), dict(parents=None), dict(parents=0x20002),
                dict(lens=0x20001), dict(state=_state(by_len=1)), dict(state=_state(ptr=0)), dict(state=_state(parts=-1)),
                dict(state=_state(rows=-1)), dict(state=_state(width=-16)), dict(state=_state(ss=-4)), dict(state=_state(sr=-4)),
-               dict(state=_state(parts=1 << 20, rows=1 << 20))):
+               dict(state=_state(rows=1 << 20, width=1 << 12)), dict(state=_state(rows=1 << 10, width=1 << 18), B=60000)):
         assert call(**kw) == da.ERR_INVALID_ARG, kw
 
 
