@@ -4,12 +4,13 @@
 //
 // State: a table [S, M] of page numbers, the tokens of each row, and of each page the
 // number of its holders; a page without holders is free. Both planning kernels are one
-// cluster of eight blocks: the table's columns and the pages are dealt to them, and they
-// meet at cluster barriers, which every thread reaches on every path. Counts change by
-// integer atomics, whose order does not matter; free pages are handed out lowest first,
-// to the rows in order, so that equal states give equal results.
+// block, or one cluster of eight: the table's columns and the pages are dealt to them, and
+// they meet at cluster barriers, which every thread reaches on every path. Counts change
+// by integer atomics, whose order does not matter; free pages are handed out lowest
+// first, to the rows in order, so that equal states give equal results.
 // They move a few hundred kilobytes and are bound by latencies, one after the other:
-// row lengths, table, counts, begun pages, free pages.
+// row lengths, table, counts, begun pages, free pages. A cluster barrier takes 0.7 us of
+// them, so that small states are left to one block.
 #include <limits.h>
 
 #include "common.cuh"
@@ -20,17 +21,28 @@ namespace {
 
 constexpr int kPage = 64;
 constexpr int kPlanThreads = 1024;
-constexpr int kPlanBlocks = 8;  // of the cluster
+constexpr int kPlanBlocks = 8;  // of a cluster
+// Table entries and twice the pages that are left to one block (fork, compaction; us with one block against eight: 32 x 32
+// entries and 1200 pages 7.8 and 4.8 against 8.3 and 6.6, 64 x 32 and 2100 9.8 and 6.7 against 9.7 and 6.9, 64 x 61
+// and 4000 12.0 and 9.5 against 9.0 and 6.8, 192 x 128 and 18000 42 and 41 against 14 and 9.5).
+constexpr int kPlanSmall = 6000;
 
-// All threads of the cluster; what they wrote before is seen behind it.
+// All threads of the block or cluster; what they wrote before is seen behind it.
+template <int BLOCKS>
 __device__ __forceinline__ void cluster_sync() {
-    asm volatile("barrier.cluster.arrive.release;\n\tbarrier.cluster.wait.acquire;" ::: "memory");
+    if constexpr (BLOCKS == 1) __syncthreads();
+    else asm volatile("barrier.cluster.arrive.release;\n\tbarrier.cluster.wait.acquire;" ::: "memory");
 }
-// Writes v to the same place of shared memory in every block of the cluster.
+// Writes v to the same place of shared memory in every block.
+template <int BLOCKS>
 __device__ __forceinline__ void store_everywhere(int* place, int v) {
+    if constexpr (BLOCKS == 1) {
+        *place = v;
+        return;
+    }
     const uint32_t at = smem_u32(place);
 #pragma unroll
-    for (uint32_t b = 0; b < kPlanBlocks; ++b)
+    for (uint32_t b = 0; b < BLOCKS; ++b)
         asm volatile("st.shared::cluster.u32 [%0], %1;" ::"r"(mapa_shared(at, b)), "r"(v) : "memory");
 }
 
@@ -48,15 +60,32 @@ __device__ __forceinline__ int block_scan(int v, int* shared, int* total) {
     __syncthreads();  // of an earlier scan's reads
     if (lane == 31) shared[warp] = x;
     __syncthreads();
-    int w = shared[lane];  // 32 warps
-    int s = w;
+    const int w = shared[lane];  // 32 warps
+    *total = __reduce_add_sync(0xffffffffu, w);
+    return __reduce_add_sync(0xffffffffu, lane < warp ? w : 0) + x - v;
+}
+
+// The same of a flag beside it, with one pair of barriers for both.
+__device__ __forceinline__ void block_scan_flag(int v, bool flag, int* shared, int* at, int* total, int* flag_at, int* flags) {
+    const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
+    const uint32_t set = __ballot_sync(0xffffffffu, flag);
+    int x = v;
 #pragma unroll
     for (int o = 1; o < 32; o <<= 1) {
-        const int y = __shfl_up_sync(0xffffffffu, s, o);
-        if (lane >= o) s += y;
+        const int y = __shfl_up_sync(0xffffffffu, x, o);
+        if (lane >= o) x += y;
     }
-    *total = __shfl_sync(0xffffffffu, s, 31);
-    return __shfl_sync(0xffffffffu, s - w, warp) + x - v;
+    __syncthreads();
+    if (lane == 31) {
+        shared[warp] = x;
+        shared[32 + warp] = __popc(set);
+    }
+    __syncthreads();
+    const int w = shared[lane], f = shared[32 + lane];
+    *at = __reduce_add_sync(0xffffffffu, lane < warp ? w : 0) + x - v;
+    *total = __reduce_add_sync(0xffffffffu, w);
+    *flag_at = __reduce_add_sync(0xffffffffu, lane < warp ? f : 0) + __popc(set & ((1u << lane) - 1));
+    *flags = __reduce_add_sync(0xffffffffu, f);
 }
 
 struct Row {  // what becomes of a row
@@ -94,11 +123,12 @@ __host__ __device__ constexpr size_t fork_bytes(int S, int tiles) {
     return (size_t)S * 20 + (columns > rest ? columns : rest);
 }
 
+template <int BLOCKS>
 __global__ void __launch_bounds__(kPlanThreads) pages_fork_kernel(const __grid_constant__ ForkParams p, int tiles) {
     extern __shared__ int shared[];
-    __shared__ int scan[32];
+    __shared__ int scan[64];
     __shared__ int s_over;
-    __shared__ int s_free[kPlanBlocks];
+    __shared__ int s_free[BLOCKS];
     int* lens = shared;            // [S] each
     int* parent = lens + p.S;
     int* kept = parent + p.S;
@@ -110,7 +140,7 @@ __global__ void __launch_bounds__(kPlanThreads) pages_fork_kernel(const __grid_c
     int* claim_row = claim_page + places;
     int* prefix = claim_row + places;  // [S + 1]: entries that the rows before need
     int* copy_at = prefix + p.S + 1;   // [S]: a row's place among the copies, or -1
-    const int tid = threadIdx.x, rank = (int)cluster_ctarank();
+    const int tid = threadIdx.x, rank = BLOCKS == 1 ? 0 : (int)cluster_ctarank();
     pdl_trigger();  // the copies' blocks may start, and wait for the plan
     if (tid == 0) s_over = 0;
 
@@ -122,7 +152,7 @@ __global__ void __launch_bounds__(kPlanThreads) pages_fork_kernel(const __grid_c
         tokens[i] = p.done ? p.done[i] : 0;
         tail[i] = -1;
     }
-    const int share = (p.P + kPlanBlocks - 1) / kPlanBlocks, page0 = min(rank * share, p.P), page1 = min(page0 + share, p.P);
+    const int share = (p.P + BLOCKS - 1) / BLOCKS, page0 = min(rank * share, p.P), page1 = min(page0 + share, p.P);
     if (p.refs_out != p.refs)
         for (int i = page0 + tid; i < page1; i += kPlanThreads) p.refs_out[i] = p.refs[i];
     __syncthreads();
@@ -133,31 +163,33 @@ __global__ void __launch_bounds__(kPlanThreads) pages_fork_kernel(const __grid_c
         tokens[i] = r.tokens;
         if (r.over) atomicAdd(&s_over, r.over);
     }
-    cluster_sync();  // counts are there to be changed, and every block has read the lengths
+    cluster_sync<BLOCKS>();  // counts are there to be changed, and every block has read the lengths
     if (rank == 0)
         for (int i = tid; i < p.S; i += kPlanThreads) p.lens_out[i] = tokens[i];
 
     // Columns of all rows through shared memory, eight at a time and dealt to the blocks: the table may be rewritten
     // in place, and the counts follow the pages that rows lose and gain. What a row keeps of itself changes nothing.
     const int all_tiles = (p.M + kColumns - 1) / kColumns, j = tid % kColumns;
-    for (int first = rank; first < all_tiles; first += kPlanBlocks * tiles) {
-        const int n = min(tiles, (all_tiles - first + kPlanBlocks - 1) / kPlanBlocks);
+    for (int first = rank; first < all_tiles; first += BLOCKS * tiles) {
+        const int n = min(tiles, (all_tiles - first + BLOCKS - 1) / BLOCKS);
+#pragma unroll 4
         for (int t = tid / kColumns; t < p.S * n; t += kPlanThreads / kColumns) {
-            const int i = t / n, c = (first + t % n * kPlanBlocks) * kColumns + j;
+            const int i = t / n, c = (first + (t - i * n) * BLOCKS) * kColumns + j;
             const int page = c < pages_of(lens[i]) ? p.table[(int64_t)i * p.M + c] : -1;
             stage[t * kColumns + j] = page >= 0 && page < p.P ? page : -1;
         }
         __syncthreads();
+#pragma unroll 2
         for (int t = tid / kColumns; t < p.S * n; t += kPlanThreads / kColumns) {
-            const int i = t / n, c = (first + t % n * kPlanBlocks) * kColumns + j, from = parent[i], full = kept[i] / kPage;
+            const int i = t / n, tile = t - i * n, c = (first + tile * BLOCKS) * kColumns + j, from = parent[i], full = kept[i] / kPage;
             if (c >= p.M) continue;
-            const int old = stage[t * kColumns + j], taken = from >= 0 ? stage[(from * n + t % n) * kColumns + j] : -1;
+            const int old = stage[t * kColumns + j], taken = from >= 0 ? stage[(from * n + tile) * kColumns + j] : -1;
             const int got = c < full ? taken : -1;
             const bool same = from == i && c < full;
             p.table_out[(int64_t)i * p.M + c] = got;
             if (old >= 0 && !same) atomicAdd(&p.refs_out[old], -1);
             if (got >= 0 && !same) atomicAdd(&p.refs_out[got], 1);
-            if (c == full && kept[i] % kPage && taken >= 0) store_everywhere(&tail[i], taken);
+            if (c == full && kept[i] % kPage && taken >= 0) store_everywhere<BLOCKS>(&tail[i], taken);
         }
         __syncthreads();
     }
@@ -165,7 +197,7 @@ __global__ void __launch_bounds__(kPlanThreads) pages_fork_kernel(const __grid_c
         claim_page[i] = -1;
         claim_row[i] = INT_MAX;
     }
-    cluster_sync();  // the counts without the begun pages, and the begun pages
+    cluster_sync<BLOCKS>();  // the counts without the begun pages, and the begun pages
 
     // The begun page stays with the first row that has it, if it has no other holder. Every block finds that out for
     // itself: the rows' pages in a table by their low bits, with the lowest row of each.
@@ -196,8 +228,8 @@ __global__ void __launch_bounds__(kPlanThreads) pages_fork_kernel(const __grid_c
             need = pages_of(tokens[i]) - kept[i] / kPage - stays;
             if (stays) tail[i] = ~t - 1;  // (below -1)
         }
-        int total, total_copies;
-        const int at = block_scan(need, scan, &total), at_copy = block_scan(copy, scan, &total_copies);
+        int at, total, at_copy, total_copies;
+        block_scan_flag(need, copy, scan, &at, &total, &at_copy, &total_copies);
         if (i < p.S) {
             prefix[i] = base + at;
             copy_at[i] = copy ? copies + at_copy : -1;
@@ -206,7 +238,7 @@ __global__ void __launch_bounds__(kPlanThreads) pages_fork_kernel(const __grid_c
         copies += total_copies;
     }
     const int wanted = base;
-    cluster_sync();  // every block has seen the counts
+    cluster_sync<BLOCKS>();  // every block has seen the counts
     for (int i = tid; i < p.S; i += kPlanThreads) {
         if (tail[i] >= -1) continue;
         const int t = ~(tail[i] + 1);
@@ -218,31 +250,46 @@ __global__ void __launch_bounds__(kPlanThreads) pages_fork_kernel(const __grid_c
     __syncthreads();
 
     // Free pages, lowest first, to the entries that need one, in the rows' order: each block knows its own and, from
-    // the others, how many lie before them. A thread has pages side by side.
+    // the others, how many lie before them. A thread has pages side by side, 32 at a time.
     const int each = (share + kPlanThreads - 1) / kPlanThreads;
     const int first_page = min(page0 + tid * each, page1), last_page = min(first_page + each, page1);
+    const auto read = [&](int from, uint32_t* below) {  // the free ones of up to 32 pages, and those of a count below zero
+        uint32_t free = 0, neg = 0;
+#pragma unroll 4
+        for (int i = 0; i < min(last_page - from, 32); ++i) {
+            const int count = __ldcg(&p.refs_out[from + i]);
+            free |= (uint32_t)(count <= 0) << i;
+            neg |= (uint32_t)(count < 0) << i;
+        }
+        *below = neg;
+        return free;
+    };
     int mine = 0;
-    for (int i = first_page; i < last_page; ++i) mine += __ldcg(&p.refs_out[i]) <= 0;
+    uint32_t free = 0, below = 0;
+    for (int i = first_page; i < last_page; i += 32) {
+        free = read(i, &below);
+        mine += __popc(free);
+    }
     int total;
     int number = block_scan(mine, scan, &total);
-    if (tid == 0) store_everywhere(&s_free[rank], total);
-    cluster_sync();
+    if (tid == 0) store_everywhere<BLOCKS>(&s_free[rank], total);
+    cluster_sync<BLOCKS>();
     int free_pages = 0;
-    for (int i = 0; i < kPlanBlocks; ++i) {
+    for (int i = 0; i < BLOCKS; ++i) {
         number += i < rank ? s_free[i] : 0;
         free_pages += s_free[i];
     }
     if (mine > 0) {
-        for (int i = first_page; i < last_page; ++i) {
-            const int count = __ldcg(&p.refs_out[i]);
-            if (count > 0) continue;
-            if (number < wanted) {
+        for (int from = first_page; from < last_page; from += 32) {
+            if (each > 32) free = read(from, &below);
+            for (; free != 0 && number < wanted; free &= free - 1, ++number) {
                 int lo = 0, hi = p.S - 1;  // the last row whose entries begin at or before `number`
                 while (lo < hi) {
                     const int mid = (lo + hi + 1) / 2;
                     if (prefix[mid] <= number) lo = mid;
                     else hi = mid - 1;
                 }
+                const int i = from + __ffs(free) - 1;
                 const int nth = number - prefix[lo], start = kept[lo] / kPage + (tail[lo] < -1);
                 p.table_out[(int64_t)lo * p.M + start + nth] = i;
                 p.refs_out[i] = 1;
@@ -252,10 +299,8 @@ __global__ void __launch_bounds__(kPlanThreads) pages_fork_kernel(const __grid_c
                     copy[1] = i;
                     copy[2] = kept[lo] % kPage;
                 }
-            } else if (count < 0) {
-                p.refs_out[i] = 0;
             }
-            ++number;
+            for (below &= free; below != 0; below &= below - 1) p.refs_out[from + __ffs(below) - 1] = 0;
         }
     }
     if (rank > 0) return;
@@ -275,21 +320,23 @@ __global__ void __launch_bounds__(kPlanThreads) pages_fork_kernel(const __grid_c
     }
 }
 
+template <int BLOCKS>
 __global__ void __launch_bounds__(kPlanThreads) pages_compact_kernel(const __grid_constant__ CompactParams p) {
     __shared__ int scan[32];
-    __shared__ int s_used[kPlanBlocks], s_behind[kPlanBlocks];
-    const int tid = threadIdx.x, rank = (int)cluster_ctarank();
-    const int share = (p.P + kPlanBlocks - 1) / kPlanBlocks, page0 = min(rank * share, p.P), page1 = min(page0 + share, p.P);
+    __shared__ int s_used[BLOCKS], s_behind[BLOCKS];
+    const int tid = threadIdx.x, rank = BLOCKS == 1 ? 0 : (int)cluster_ctarank();
+    const int share = (p.P + BLOCKS - 1) / BLOCKS, page0 = min(rank * share, p.P), page1 = min(page0 + share, p.P);
     const int each = (share + kPlanThreads - 1) / kPlanThreads;  // a thread has pages side by side
     const int first_page = min(page0 + tid * each, page1), last_page = min(first_page + each, page1);
     pdl_trigger();
     int mine = 0, total;
+#pragma unroll 4
     for (int i = first_page; i < last_page; ++i) mine += p.refs[i] > 0;
     int below = block_scan(mine, scan, &total);
-    if (tid == 0) store_everywhere(&s_used[rank], total);
-    cluster_sync();
+    if (tid == 0) store_everywhere<BLOCKS>(&s_used[rank], total);
+    cluster_sync<BLOCKS>();
     int used = 0;
-    for (int i = 0; i < kPlanBlocks; ++i) {
+    for (int i = 0; i < BLOCKS; ++i) {
         below += i < rank ? s_used[i] : 0;
         used += s_used[i];
     }
@@ -308,12 +355,12 @@ __global__ void __launch_bounds__(kPlanThreads) pages_compact_kernel(const __gri
         below += held;
     }
     block_scan(behind, scan, &total);
-    if (tid == 0) store_everywhere(&s_behind[rank], total);
-    cluster_sync();
+    if (tid == 0) store_everywhere<BLOCKS>(&s_behind[rank], total);
+    cluster_sync<BLOCKS>();
     int moves = 0;
-    for (int i = 0; i < kPlanBlocks; ++i) moves += s_behind[i];
+    for (int i = 0; i < BLOCKS; ++i) moves += s_behind[i];
     moves = min(moves, p.max_copies);
-    for (int i = rank * kPlanThreads + tid; i < p.max_copies; i += kPlanBlocks * kPlanThreads) {
+    for (int i = rank * kPlanThreads + tid; i < p.max_copies; i += BLOCKS * kPlanThreads) {
         const bool some = i < moves;
         p.copies[3 * i + 2] = some ? kPage : -1;
         if (!some) {
@@ -325,8 +372,8 @@ __global__ void __launch_bounds__(kPlanThreads) pages_compact_kernel(const __gri
             p.refs_out[src] = 0;
         }
     }
-    cluster_sync();
-    for (int64_t t = rank * kPlanThreads + tid; t < (int64_t)p.S * p.M; t += kPlanBlocks * kPlanThreads) {
+    cluster_sync<BLOCKS>();
+    for (int64_t t = rank * kPlanThreads + tid; t < (int64_t)p.S * p.M; t += BLOCKS * kPlanThreads) {
         const int i = (int)(t / p.M), c = (int)(t % p.M);
         const int page = c < pages_of(max(p.lens[i], 0)) ? p.table[t] : -1;
         p.table_out[t] = page >= 0 && page < p.P ? __ldcg(&p.moved[page]) : -1;
@@ -372,35 +419,41 @@ __global__ void __launch_bounds__(256) pages_copy_kernel(const __grid_constant__
 
 }  // namespace
 
-// A planning kernel: one cluster.
-template <typename... KArgs, typename... Args>
+// A planning kernel of one block or one cluster.
+template <int BLOCKS, typename... KArgs, typename... Args>
 cudaError_t launch_plan(void (*kernel)(KArgs...), size_t smem, cudaStream_t stream, Args... args) {
     cudaLaunchConfig_t cfg = {};
-    cfg.gridDim = dim3(kPlanBlocks);
+    cfg.gridDim = dim3(BLOCKS);
     cfg.blockDim = dim3(kPlanThreads);
     cfg.dynamicSmemBytes = smem;
     cfg.stream = stream;
     cudaLaunchAttribute attr[1];
     attr[0].id = cudaLaunchAttributeClusterDimension;
-    attr[0].val.clusterDim.x = kPlanBlocks;
+    attr[0].val.clusterDim.x = BLOCKS;
     attr[0].val.clusterDim.y = attr[0].val.clusterDim.z = 1;
     cfg.attrs = attr;
-    cfg.numAttrs = 1;
+    cfg.numAttrs = BLOCKS > 1;
     return cudaLaunchKernelEx(&cfg, kernel, args...);
 }
 
-cudaError_t launch_pages_fork(const ForkParams& p, cudaStream_t stream) {
+template <int BLOCKS>
+cudaError_t launch_fork(const ForkParams& p, cudaStream_t stream) {
     // A block's columns at once, or as many as 128 KB hold (at 4096 rows: eight).
-    const int all = (p.M + kColumns * kPlanBlocks - 1) / (kColumns * kPlanBlocks);
+    const int all = (p.M + kColumns * BLOCKS - 1) / (kColumns * BLOCKS);
     const int room = p.S == 0 ? all : 131072 / (p.S * kColumns * 4);
     const int tiles = room < 1 ? 1 : all < room ? all : room;
-    cudaError_t e = prepare_once<pages_fork_kernel>((int)fork_bytes(kMaxPageRows, 1));
+    cudaError_t e = prepare_once<pages_fork_kernel<BLOCKS>>((int)fork_bytes(kMaxPageRows, 1));
     if (e != cudaSuccess) return e;
-    return launch_plan(pages_fork_kernel, fork_bytes(p.S, tiles), stream, p, tiles);
+    return launch_plan<BLOCKS>(pages_fork_kernel<BLOCKS>, fork_bytes(p.S, tiles), stream, p, tiles);
+}
+
+cudaError_t launch_pages_fork(const ForkParams& p, cudaStream_t stream) {
+    return (int64_t)p.S * p.M + 2 * (int64_t)p.P <= kPlanSmall ? launch_fork<1>(p, stream) : launch_fork<kPlanBlocks>(p, stream);
 }
 
 cudaError_t launch_pages_compact(const CompactParams& p, cudaStream_t stream) {
-    return launch_plan(pages_compact_kernel, 0, stream, p);
+    return (int64_t)p.S * p.M + 2 * (int64_t)p.P <= kPlanSmall ? launch_plan<1>(pages_compact_kernel<1>, 0, stream, p)
+                                                               : launch_plan<kPlanBlocks>(pages_compact_kernel<kPlanBlocks>, 0, stream, p);
 }
 
 cudaError_t launch_pages_copy(const CopyParams& p, int pools, cudaStream_t stream) {
