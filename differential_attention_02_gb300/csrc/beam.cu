@@ -217,7 +217,7 @@ constexpr int kCounted = 64;
 __device__ __forceinline__ void warp_place(const uint64_t* keys, int n, int W, int lane, uint64_t* out) {
     const uint64_t a = lane < n ? keys[lane] : 0, b = lane + 32 < n ? keys[lane + 32] : 0;
     int at = 0, bt = 0;
-#pragma unroll 2
+#pragma unroll 8
     for (int j = 0; j < n; ++j) {
         const uint64_t k = keys[j];
         at += k > a;
@@ -622,7 +622,7 @@ __global__ void __launch_bounds__(32 * kMaxBeams) beam_merge_kernel(const __grid
     }
     __syncthreads();
     // The beams' lists by their ranks, equal ones in the beams' order: a candidate's place is its own in its list and
-    // the number of better ones in each other list, found by halving, four lists at a time.
+    // the number of better ones in each other list, found by halving, two lists at a time.
     const int halves = 1 << (31 - __clz(p.W));
     int some = 0;
 #pragma unroll 1
@@ -633,19 +633,19 @@ __global__ void __launch_bounds__(32 * kMaxBeams) beam_merge_kernel(const __grid
         if (mine == 0) continue;
         int place = i;
 #pragma unroll 1
-        for (int first = 0; first < p.K; first += 4) {
-            int lo[4] = {0, 0, 0, 0};
+        for (int first = 0; first < p.K; first += 2) {
+            int lo[2] = {0, 0};
 #pragma unroll 1
             for (int step = halves; step > 0; step >>= 1) {
 #pragma unroll
-                for (int u = 0; u < 4; ++u) {
+                for (int u = 0; u < 2; ++u) {
                     const uint64_t k = ranks[min(first + u, p.K - 1) * p.W + min(lo[u] + step, p.W) - 1];
                     const int better = (int)(k > mine) | ((int)(k == mine) & (int)(first + u < warp));
                     lo[u] += step * (better & (int)(lo[u] + step <= p.W));
                 }
             }
 #pragma unroll
-            for (int u = 0; u < 4; ++u) place += first + u < p.K && first + u != warp ? lo[u] : 0;
+            for (int u = 0; u < 2; ++u) place += first + u < p.K && first + u != warp ? lo[u] : 0;
         }
         if (place >= p.W) continue;
         const int64_t out = (int64_t)b * p.W + place;
