@@ -20,7 +20,8 @@ bool workspace_ok(const void* ws, size_t bytes, size_t need) {
 
 // Chunks of a row, and the workspace of the selection: control block, a chunk's best logits, its sum and its maximum.
 struct BeamLayout {
-    int chunks, chunk_rounds, wide;
+    int chunks, rounds;
+    BeamMode mode;
     size_t keys, sums, maxima, weights, total;
 };
 bool beam_layout(int B, int K, int V, int W, int in_dtype, BeamLayout* l) {
@@ -33,13 +34,22 @@ bool beam_layout(int B, int K, int V, int W, int in_dtype, BeamLayout* l) {
     int sms = 0;
     if (device_sm_count(&sms) != cudaSuccess || sms < 1) sms = 152;
     const int least = (rounds * parts + kBeamSegments - 1) / kBeamSegments;
-    const int room = kBeamMergeBytes / (8 * K * W) - 3;  // of the merge's shared memory: 9 at K W = 2048, of which 9 are needed
-    const int most = std::min({kBeamChunks, room, (rounds + 7) / 8});
+    const int room = std::min(kBeamChunks, kBeamMergeBytes / (8 * K * W) - 3);  // of the merge: 9 at K W = 2048, of which 9 are needed
     const int want = rows > 0 ? (int)std::min<size_t>(kBeamChunks, (2 * (size_t)sms + rows - 1) / rows) : 1;
-    const int chunks = std::max(least, std::min(want, most));
-    l->chunk_rounds = (rounds + chunks - 1) / chunks;
-    l->chunks = (rounds + l->chunk_rounds - 1) / l->chunk_rounds;
-    l->wide = l->chunk_rounds >= 2 * W;
+    l->rounds = rounds;
+    l->chunks = std::max(least, std::min({want, room, (rounds + 7) / 8}));
+    // A chunk needs W segments, or all its logits are looked at one by one: vectors where it is short, else longer chunks.
+    const int each = rounds / l->chunks;  // or one more; the last may have one less
+    l->mode = each > 2 * W ? kBeamWide : kBeamNarrow;
+    if ((each - 1) * parts < W) {
+        const int vectors = (rounds + kBeamSegments / 128 - 1) / (kBeamSegments / 128);
+        if (vectors <= room) {
+            l->mode = kBeamVector;
+            l->chunks = std::max(l->chunks, vectors);
+        } else {
+            l->chunks = std::max(least, std::min(l->chunks, rounds / ((W + parts - 1) / parts + 1)));
+        }
+    }
     l->keys = kControlBytes;
     l->sums = l->keys + round256(rows * l->chunks * W * sizeof(uint64_t));
     l->maxima = l->sums + round256(rows * l->chunks * sizeof(uint64_t));
@@ -104,8 +114,8 @@ diffattn_status diffattn_beam_select(const void* logits, int64_t stride_b, int64
     p.finished_out = finished_out;
     p.lengths_out = lengths_out;
     p.chunks = l.chunks;
-    p.chunk_rounds = l.chunk_rounds;
-    p.wide = l.wide;
+    p.rounds = l.rounds;
+    p.mode = l.mode;
     p.keys = reinterpret_cast<uint64_t*>(ws + l.keys);
     p.sums = reinterpret_cast<uint64_t*>(ws + l.sums);
     p.maxima = reinterpret_cast<float*>(ws + l.maxima);

@@ -12,11 +12,11 @@
 // candidates of different beams does not hang on fp32's rounding of sums near -50.
 //
 // A row is read once. Blocks share a row in chunks; a warp reads a round of four vectors
-// a lane, adds the exponentials and keeps the maximum of each segment (256 logits, or
-// the whole round where the chunk has many). The W best logits of a chunk lie in the W
-// segments of the largest maxima (equal ones in order): any other segment has W segments
-// before it that each hold a logit to be preferred. So the selection looks at the maxima,
-// and reads W segments once more (from L2).
+// a lane, adds the exponentials and keeps the maximum of each segment: 256 logits, the
+// whole round where the chunk has many, a single vector where it has less than W. The W
+// best logits of a chunk lie in the W segments of the largest maxima (equal ones in
+// order): any other segment has W segments before it that each hold a logit to be
+// preferred. So the selection looks at the maxima, and reads W segments once more (from L2).
 #include <limits.h>
 #include <math.h>
 
@@ -31,7 +31,6 @@ namespace {
 constexpr int kThreads = 256;
 constexpr int kWarps = kThreads / 32;
 constexpr int kSegment = kBeamSegment;  // eight logits a lane
-constexpr int kFound = 512;             // logits that a chunk's selection compares with one another
 
 // ---------------------------------------------------------------- logits as keys
 // Bits whose order as unsigned numbers is that of the values; above -inf's for every candidate.
@@ -211,76 +210,60 @@ __device__ __noinline__ float any_sum(uint4 v, float m, float c) {
 }
 
 // ---------------------------------------------------------------- the W largest of a few keys
-// Keys apart from each other, in shared memory, in any order: the place of each is the number of larger ones, and
-// no step waits for the one before. Beyond 64 keys (two a lane) it is left to others.
-constexpr int kCounted = 64;
-__device__ __forceinline__ void warp_place(const uint64_t* keys, int n, int W, int lane, uint64_t* out) {
-    const uint64_t a = lane < n ? keys[lane] : 0, b = lane + 32 < n ? keys[lane + 32] : 0;
-    int at = 0, bt = 0;
-#pragma unroll 8
-    for (int j = 0; j < n; ++j) {
-        const uint64_t k = keys[j];
-        at += k > a;
-        bt += k > b;
-    }
-    if (lane < n && at < W) out[at] = a;
-    if (lane + 32 < n && bt < W) out[bt] = b;
-    for (int i = n + lane; i < W; i += 32) out[i] = 0;
-}
-
-// One warp: the segments of the W largest maxima as keys, best first, equal ones in order; places beyond the last are
-// 0. Of more than 64 segments, the W-th of the lanes' own maxima is a bound that W segments reach, and few more
-// do; where they are too many (equal maxima), or W more than the lanes, one is taken after the other (and `best` is
-// used up).
-__device__ __forceinline__ void choose_segments(uint32_t* best, int segments, int W, int lane, uint64_t* few, uint64_t* sorted) {
-    if (W <= 32 || segments <= kCounted) {
-        uint32_t bound = 1;
-        if (segments > kCounted) {
-            uint32_t u = 0;
+// One warp: the W largest of n keys in shared memory, apart from each other and in any order, best first; places
+// beyond the last are 0 (as are keys that stand for nothing). Of more than 64, the W-th of 32 or 64 groups' own maxima is a
+// bound that W keys reach, and few more do; those move to the front. A key's place is then the number of larger
+// ones, counted for two keys a lane at a time, so that no step waits for the one before. tops: 64 values.
+__device__ __forceinline__ void warp_top(uint64_t* keys, int n, int W, int lane, uint64_t* tops, uint64_t* out) {
+    if (n > 64) {
+        const int groups = W <= 32 ? 32 : 64;
+        uint64_t bound = 0;
 #pragma unroll 1
-            for (int i = 0; i < segments; i += 32) u = max(u, i + lane < segments ? best[i + lane] : 0u);
-            uint32_t* lanes = reinterpret_cast<uint32_t*>(sorted);
-            lanes[lane] = u;
-            __syncwarp();
-            int larger = 0;
+        for (int g = lane; g < groups; g += 32) {
+            uint64_t u = 0;
 #pragma unroll 2
-            for (int j = 0; j < 32; j += 4) {
-                const uint4 k = *reinterpret_cast<const uint4*>(lanes + j);
-                larger += (int)(k.x > u) | ((int)(k.x == u) & (int)(j < lane));
-                larger += (int)(k.y > u) | ((int)(k.y == u) & (int)(j + 1 < lane));
-                larger += (int)(k.z > u) | ((int)(k.z == u) & (int)(j + 2 < lane));
-                larger += (int)(k.w > u) | ((int)(k.w == u) & (int)(j + 3 < lane));
-            }
-            bound = max(__reduce_max_sync(0xffffffffu, larger == W - 1 ? u : 0u), 1u);
-            __syncwarp();
-        }
-        int n = 0;
-#pragma unroll 1
-        for (int i = 0; i < segments; i += 32) {
-            const uint32_t x = i + lane < segments ? best[i + lane] : 0;
-            const uint32_t hit = __ballot_sync(0xffffffffu, x >= bound);
-            const int at = n + __popc(hit & ((1u << lane) - 1));
-            if (x >= bound && at < kCounted) few[at] = make_key(x, i + lane);
-            n += __popc(hit);
+            for (int i = g; i < n; i += groups) u = keys[i] > u ? keys[i] : u;
+            tops[g] = u;
         }
         __syncwarp();
-        if (n <= kCounted) {
-            warp_place(few, n, W, lane, sorted);
-            return;
-        }
-    }
 #pragma unroll 1
-    for (int n = 0; n < W; ++n) {
-        uint64_t key = 0;
-#pragma unroll 1
-        for (int i = lane; i < segments; i += 32) {
-            const uint64_t k = make_key(best[i], i);
-            key = k > key ? k : key;
+        for (int g = lane; g < groups; g += 32) {
+            const uint64_t u = tops[g];
+            int larger = 0;
+#pragma unroll 8
+            for (int j = 0; j < groups; ++j) larger += tops[j] > u;
+            if (larger == W - 1) bound = u;
         }
-        key = warp_max_key(key);
-        if (lane == 0) sorted[n] = key;
-        if (key != 0 && key_token(key) % 32 == lane) best[key_token(key)] = 0;
+        bound = warp_max_key(bound);
+        if (bound == 0) bound = 1;
+        int found = 0;
+#pragma unroll 1
+        for (int i = 0; i < n; i += 32) {
+            const uint64_t k = i + lane < n ? keys[i + lane] : 0;
+            const uint32_t hit = __ballot_sync(0xffffffffu, k >= bound);
+            if (k >= bound) keys[found + __popc(hit & ((1u << lane) - 1))] = k;
+            found += __popc(hit);
+        }
+        n = found;
+        __syncwarp();
     }
+    if (lane < W) out[lane] = 0;
+    if (lane + 32 < W) out[lane + 32] = 0;
+    __syncwarp();
+#pragma unroll 1
+    for (int i = lane; i - lane < n; i += 64) {
+        const uint64_t a = i < n ? keys[i] : 0, b = i + 32 < n ? keys[i + 32] : 0;
+        int at = 0, bt = 0;
+#pragma unroll 8
+        for (int j = 0; j < n; ++j) {
+            const uint64_t k = keys[j];
+            at += k > a;
+            bt += k > b;
+        }
+        if (a != 0 && at < W) out[at] = a;
+        if (b != 0 && bt < W) out[bt] = b;
+    }
+    __syncwarp();
 }
 
 // The logarithm of a sum, within 2^-24: fp32's of a factor near one.
@@ -329,23 +312,26 @@ __device__ __forceinline__ double inverse_power(int n, double a) {
     return y * __longlong_as_double((int64_t)((int)whole + 1023) << 52);
 }
 
-// One block per chunk of a row: its sum of exponentials and its W best logits. WIDE: a segment is a whole round.
-template <typename T, bool WIDE>
+// One block per chunk of a row: its sum of exponentials and its W best logits.
+template <typename T, BeamMode MODE>
 __global__ void __launch_bounds__(kThreads, 4) beam_rows_kernel(const __grid_constant__ BeamParams p) {
     using View = RowView<T>;
-    constexpr int kParts = View::kRound / kSegment;   // pieces of 256 logits of a round
-    __shared__ uint32_t best[kBeamSegments];          // a segment's largest logit
+    // segments of a round, and vectors of a lane in a segment (of vectors alone: one lane's)
+    constexpr int kParts = MODE == kBeamWide ? 1 : MODE == kBeamVector ? 128 : View::kRound / kSegment;
+    constexpr int kVecs = MODE == kBeamWide ? 4 : View::kLoads;
+    // a segment's largest logit, as a key with its number; later the logits that may be among the W best
+    __shared__ uint64_t keys[kBeamSegments];
+    __shared__ uint64_t tops[64];
     __shared__ uint64_t sums[kWarps];
     __shared__ float maxima[kWarps];
-    __shared__ __align__(16) uint64_t chosen[kMaxBeamWidth];  // segments of the W largest maxima
+    __shared__ uint64_t chosen[kMaxBeamWidth];                // segments of the W largest maxima
     __shared__ int n_chosen, n_above, n_found;
-    __shared__ uint64_t found[kFound];                // logits that may be among the W best
     const int row = blockIdx.x / p.chunks, chunk = blockIdx.x % p.chunks;
     const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
     const bool ended = p.finished && p.finished[row];
     const View view(static_cast<const T*>(p.logits) + row / p.K * p.stride_b + row % p.K * p.stride_k, p.V);
-    const int begin = chunk * p.chunk_rounds * View::kRound;
-    const int rounds = min(p.chunk_rounds, (view.end - begin + View::kRound - 1) / View::kRound);  // may be none
+    const int first_round = chunk * p.rounds / p.chunks, begin = first_round * View::kRound;
+    const int rounds = min((chunk + 1) * p.rounds / p.chunks - first_round, (view.end - begin + View::kRound - 1) / View::kRound);
 
     float m = -INFINITY, c = 0.f, sum = 0.f;
     const auto load = [&](int r, uint4* v) {
@@ -367,17 +353,25 @@ __global__ void __launch_bounds__(kThreads, 4) beam_rows_kernel(const __grid_con
         for (int i = 0; i < 4; ++i) v[i] = next[i];
         if (r + kWarps < rounds) load(r + kWarps, next);  // the next round's are on their way
         uint32_t top = 0;
-        if constexpr (WIDE) {
+        if constexpr (MODE == kBeamVector) {
+            uint32_t u[4];
+#pragma unroll
+            for (int i = 0; i < 4; ++i) {
+                u[i] = candidate(View::largest(v[i]));
+                keys[r * kParts + i * 32 + lane] = make_key(u[i], r * kParts + i * 32 + lane);
+            }
+            top = __reduce_max_sync(0xffffffffu, max(max(u[0], u[1]), max(u[2], u[3])));
+        } else if constexpr (MODE == kBeamWide) {
             const float x = fmaxf(fmaxf(View::largest(v[0]), View::largest(v[1])), fmaxf(View::largest(v[2]), View::largest(v[3])));
             top = __reduce_max_sync(0xffffffffu, candidate(x));
-            if (lane == 0) best[r] = top;
+            if (lane == 0) keys[r] = make_key(top, r);
         } else {
 #pragma unroll
             for (int i = 0; i < kParts; ++i) {
                 float x = View::largest(v[i * View::kLoads]);
                 if (View::kLoads == 2) x = fmaxf(x, View::largest(v[i * View::kLoads + 1]));
                 const uint32_t u = __reduce_max_sync(0xffffffffu, candidate(x));
-                if (lane == 0) best[r * kParts + i] = u;
+                if (lane == 0) keys[r * kParts + i] = make_key(u, r * kParts + i);
                 top = max(top, u);
             }
         }
@@ -415,8 +409,7 @@ __global__ void __launch_bounds__(kThreads, 4) beam_rows_kernel(const __grid_con
 
     const int64_t out = (int64_t)row * p.chunks + chunk;
     if (warp == 0) {
-        choose_segments(best, max(rounds, 0) * (WIDE ? 1 : kParts), p.W, lane, found, chosen);
-        __syncwarp();
+        warp_top(keys, max(rounds, 0) * kParts, p.W, lane, tops, chosen);
         const uint32_t last = (uint32_t)(chosen[p.W - 1] >> 32);
         int n = 0, above = 0;
         for (int i = lane; i < p.W; i += 32) {
@@ -442,15 +435,22 @@ __global__ void __launch_bounds__(kThreads, 4) beam_rows_kernel(const __grid_con
 
     // The chosen segments' logits that may be among the W best, collected by a warp each: those that reach the least
     // of the chosen maxima, or all where fewer segments hold any.
-    constexpr int kVecs = WIDE ? 4 : View::kLoads;  // vectors of a lane in a segment
     const float bound = n_chosen == p.W ? key_logit(chosen[p.W - 1]) : -INFINITY;
     const auto first_of = [&](int w) { return begin + key_token(chosen[w]) * kVecs * 32 * View::kVec; };
     const auto collect = [&](int at) {
         const int to = atomicAdd(&n_found, 1);  // in any order
-        if (to < kFound) found[to] = make_key(candidate(view.at(at)), at - view.off);
+        if (to < kBeamSegments) keys[to] = make_key(candidate(view.at(at)), at - view.off);
     };
+    if constexpr (MODE == kBeamVector) {  // a thread each: 8 W logits at most
+        if (threadIdx.x < n_chosen) {
+            const int at = begin + key_token(chosen[threadIdx.x]) * View::kVec;
 #pragma unroll 1
-    for (int w = warp; w < n_chosen; w += kWarps) {
+            for (int j = max(at, view.off); j < min(at + View::kVec, view.end); ++j)
+                if (view.at(j) >= bound && view.at(j) > -INFINITY) collect(j);
+        }
+    }
+#pragma unroll 1
+    for (int w = MODE == kBeamVector ? n_chosen : warp; w < n_chosen; w += kWarps) {
         // Of those that equal the bound (many, where a mask leaves few others) the lowest W - n_above tokens are enough,
         // one less for each earlier segment that has such alone.
         int left = n_chosen < p.W ? 0 : p.W - n_above - max(0, w - n_above);
@@ -489,21 +489,11 @@ __global__ void __launch_bounds__(kThreads, 4) beam_rows_kernel(const __grid_con
     }
     __syncthreads();
     pdl_trigger();  // not before: a merge that waits beside the rows costs them more (20 us of 36) than its start
-    const int n = n_found;
-    if (n <= kCounted) {
-        if (warp == 0) warp_place(found, n, p.W, lane, p.keys + out * p.W);
-        return;
-    }
-    if (n <= kFound) {  // two to a thread (more than W: no place stays empty)
-        const uint64_t a = threadIdx.x < n ? found[threadIdx.x] : 0, b = threadIdx.x + kThreads < n ? found[threadIdx.x + kThreads] : 0;
-        int at = 0, bt = 0;
-        for (int j = 0; j < n; ++j) {
-            const uint64_t k = found[j];
-            at += k > a;
-            bt += k > b;
+    if (n_found <= kBeamSegments) {
+        if (warp == 0) {
+            warp_top(keys, n_found, p.W, lane, tops, chosen);
+            for (int i = lane; i < p.W; i += 32) p.keys[out * p.W + i] = chosen[i];
         }
-        if (a != 0 && at < p.W) p.keys[out * p.W + at] = a;
-        if (b != 0 && bt < p.W) p.keys[out * p.W + bt] = b;
         return;
     }
 
@@ -522,11 +512,11 @@ __global__ void __launch_bounds__(kThreads, 4) beam_rows_kernel(const __grid_con
         }
         key = warp_max_key(key);
         __syncthreads();  // the last round's keys have been read
-        if (lane == 0) found[warp] = key;
+        if (lane == 0) tops[warp] = key;
         __syncthreads();
         last = 0;
 #pragma unroll 1
-        for (int w = 0; w < kWarps; ++w) last = found[w] > last ? found[w] : last;
+        for (int w = 0; w < kWarps; ++w) last = tops[w] > last ? tops[w] : last;
         if (threadIdx.x == 0) p.keys[out * p.W + i] = last;
     }
 }
@@ -535,6 +525,7 @@ __global__ void __launch_bounds__(kThreads, 4) beam_rows_kernel(const __grid_con
 // beams by their ranks.
 __global__ void __launch_bounds__(32 * kMaxBeams) beam_merge_kernel(const __grid_constant__ BeamParams p) {
     extern __shared__ uint64_t shared[];  // [K][chunks W] keys, then [K][W] keys, [K][W] scores, [K][W] ranks
+    __shared__ uint64_t tops[kMaxBeams * 64];
     const int b = blockIdx.x, warp = threadIdx.x >> 5, lane = threadIdx.x & 31, row = b * p.K + warp;
     const int n = p.chunks * p.W;
     uint64_t* in = shared + (int64_t)warp * n;
@@ -542,7 +533,6 @@ __global__ void __launch_bounds__(32 * kMaxBeams) beam_merge_kernel(const __grid
     uint64_t* keys = all_keys + warp * p.W;
     double* scores = reinterpret_cast<double*>(all_keys + p.K * p.W);
     uint64_t* ranks = reinterpret_cast<uint64_t*>(scores + p.K * p.W);
-    __shared__ uint64_t few[kMaxBeams][kCounted];
     // The rows' kernel is an ordinary launch: what was written before it is there.
     const double score = p.scores[row];
     const bool ended = p.finished && p.finished[row];
@@ -567,44 +557,7 @@ __global__ void __launch_bounds__(32 * kMaxBeams) beam_merge_kernel(const __grid
         base = base_log(top);
         lse = log_sum(sum);
         __syncwarp();
-        // The W best of the chunks' lists. Of more than 64 logits, a bound that W reach is the least of what stands at
-        // place ceil(W / chunks) of each.
-        uint64_t bound = 1;
-        if (n > kCounted) {
-            const int q = (p.W - 1) / p.chunks;
-            bound = ~0ull;
-#pragma unroll 1
-            for (int i = lane; i < p.chunks; i += 32) bound = min(bound, in[i * p.W + q]);
-            bound = ~warp_max_key(~bound);
-            if (bound == 0) bound = 1;
-        }
-        int found = 0;
-#pragma unroll 1
-        for (int i0 = 0; i0 < n; i0 += 32) {
-            const uint64_t k = i0 + lane < n ? in[i0 + lane] : 0;
-            const uint32_t hit = __ballot_sync(0xffffffffu, k >= bound);
-            const int to = found + __popc(hit & ((1u << lane) - 1));
-            if (k >= bound && to < kCounted) few[warp][to] = k;
-            found += __popc(hit);
-        }
-        __syncwarp();
-        if (found <= kCounted) {
-            warp_place(few[warp], found, p.W, lane, keys);
-        } else {  // one after the other, two lists to a lane
-            int from[2] = {0, 0};
-            uint64_t head[2];
-#pragma unroll
-            for (int i = 0; i < 2; ++i) head[i] = i * 32 + lane < p.chunks ? in[(i * 32 + lane) * p.W] : 0;
-#pragma unroll 1
-            for (int w = 0; w < p.W; ++w) {
-                const uint64_t best = warp_max_key(max(head[0], head[1]));
-                if (lane == 0) keys[w] = best;
-#pragma unroll
-                for (int i = 0; i < 2; ++i)
-                    if (best != 0 && head[i] == best) head[i] = ++from[i] < p.W ? in[(i * 32 + lane) * p.W + from[i]] : 0;
-            }
-        }
-        __syncwarp();
+        warp_top(in, n, p.W, lane, tops + warp * 64, keys);
     }
     for (int w = lane; w < p.W; w += 32) {
         double s = -INFINITY;
@@ -734,8 +687,9 @@ cudaError_t launch_reorder_u(const ReorderParams& p, int64_t most, int parts, in
 
 template <typename T>
 void launch_rows(const BeamParams& p, unsigned blocks, cudaStream_t stream) {
-    if (p.wide) beam_rows_kernel<T, true><<<blocks, kThreads, 0, stream>>>(p);
-    else beam_rows_kernel<T, false><<<blocks, kThreads, 0, stream>>>(p);
+    if (p.mode == kBeamWide) beam_rows_kernel<T, kBeamWide><<<blocks, kThreads, 0, stream>>>(p);
+    else if (p.mode == kBeamVector) beam_rows_kernel<T, kBeamVector><<<blocks, kThreads, 0, stream>>>(p);
+    else beam_rows_kernel<T, kBeamNarrow><<<blocks, kThreads, 0, stream>>>(p);
 }
 
 }  // namespace

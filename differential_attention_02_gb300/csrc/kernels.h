@@ -204,6 +204,7 @@ cudaError_t launch_chunk_pair(const ChunkParams& p, cudaStream_t stream);   // d
 // Selection of the best continuations over a sequence's beams and the vocabulary (beam.cu).
 constexpr int kMaxBeams = 32;       // beams of a sequence, and of a group whose states are reordered
 constexpr int kMaxBeamWidth = 64;   // candidates kept per sequence
+enum BeamMode { kBeamNarrow, kBeamWide, kBeamVector };  // a segment is 256 logits, a round, a vector
 struct BeamParams {
     const void* logits;             // [B, K, V], rows stride_k apart, any alignment of an element
     int64_t stride_b, stride_k;
@@ -217,7 +218,8 @@ struct BeamParams {
     int32_t *tokens, *parents;
     uint8_t* finished_out;          // or null
     int32_t* lengths_out;           // or null
-    int chunks, chunk_rounds, wide; // blocks that share a row, the rounds of each; a segment is a round
+    int chunks, rounds;             // blocks that share a row, and the rounds that they share
+    BeamMode mode;
     uint64_t* keys;                 // workspace: [B K][chunks][W], a chunk's best logits
     uint64_t* sums;                 // [B K][chunks]: its sum of exponentials, scaled by its maximum's base
     float* maxima;                  // [B K][chunks]
@@ -227,7 +229,7 @@ constexpr int kBeamSegment = 256;        // logits of which a chunk keeps one ma
 constexpr int kBeamRoundBytes = 2048;    // of a row, read by a warp at a time
 constexpr int kBeamSegments = 512;       // at most, of a chunk
 constexpr int kBeamChunks = 64;          // at most, of a row
-constexpr int kBeamMergeBytes = 200 * 1024;  // shared memory of the merge, 8 K W (chunks + 3) at most, beside 17 KB
+constexpr int kBeamMergeBytes = 200 * 1024;  // shared memory of the merge, 8 K W (chunks + 3) at most, beside 16 KB
 cudaError_t launch_beam_select(const BeamParams& p, int in_dtype, cudaStream_t stream);
 
 // Rows of per-beam states moved to the places of their children, in place (beam.cu).
