@@ -71,6 +71,40 @@ def test_selection(B, K, V, W, dtype):
     assert all(torch.equal(a, b) for a, b in zip(got[:3], again[:3]))
 
 
+@pytest.mark.parametrize("dtype", [F32, BF])
+@pytest.mark.parametrize("B,K,V,W", [(1, 32, 16001, 64), (300, 2, 90, 5), (1, 2, 1 << 20, 64), (3, 1, 9000, 63), (2, 7, 40000, 33), (64, 16, 700, 32),
+                                     (1, 1, 64, 64)])
+def test_short_rows_and_many_kept(B, K, V, W, dtype):
+    """Segments of a vector, of 256 logits and of a round, rows in one chunk and in many."""
+    _, logits, scores = _inputs(B, K, V, dtype, seed=V)
+    _check(da.diffattn_beam_select(logits.cuda(), scores.cuda(), W), logits, scores, W)
+
+
+@pytest.mark.parametrize("dtype", [F32, BF, F16])
+@pytest.mark.parametrize("V,W", [(900, 9), (6000, 64), (50001, 16), (50001, 64), (262144, 8)])
+def test_logits_in_order_and_nearly_all_masked(V, W, dtype):
+    """The best side by side (ascending, descending, in blocks), a grammar's mask that leaves three tokens above the type's
+    lowest value, and steps of equal values."""
+    K = 2
+    x = torch.stack([torch.linspace(-6, 6, V), torch.linspace(6, -6, V), (torch.arange(V) // 700 * 37 % 101).float() / 9,
+                     torch.full((V,), torch.finfo(dtype).min), (torch.arange(V) % 97).float() / 10, torch.zeros(V)])
+    x[3, [V // 3, V // 2, V - 1]] = torch.tensor([1.0, 3.0, 2.0])
+    logits = x.clamp(torch.finfo(dtype).min, torch.finfo(dtype).max).to(dtype)[:, None].expand(6, K, V).contiguous()
+    logits[:, 1] = logits[:, 1].roll(5, -1)
+    scores = torch.tensor([[-1.0, -4.0]]).expand(6, K).contiguous()
+    _check(da.diffattn_beam_select(logits.cuda(), scores.cuda(), W), logits, scores, W)
+
+
+def test_scores_of_every_size():
+    """Scores far from zero, where units of fp32 hide differences of logits, and dead beams at -1e9 as some programs have them."""
+    g = torch.Generator().manual_seed(6)
+    logits = torch.randn(4, 3, 3000, generator=g) * 2
+    scores = torch.tensor([[-1e6, -1e6 - 1, -2e6], [0.0, -1e9, -1e9], [-3.0, -3e38, -INF], [1e4, 1e4, 5.0]])
+    got = da.diffattn_beam_select(logits.cuda(), scores.cuda(), 6)
+    _check(got, logits, scores, 6)
+    assert got.parents[1].tolist() == [0] * 6
+
+
 @pytest.mark.parametrize("dtype", [F32, BF, F16])
 @pytest.mark.parametrize("penalty", [0.0, 0.7, -0.5])
 @pytest.mark.parametrize("B,K,V,W", [(4, 4, 1000, 8), (3, 6, 4099, 6), (2, 16, 30000, 32)])

@@ -240,3 +240,27 @@ def test_plans_and_copies_from_a_graph():
         step() if graph is None else graph.replay()
         assert (plan.table.tolist(), plan.lens.tolist(), plan.refs.tolist(), plan.info.tolist()) == (table, lens, refs, info)
         assert all(torch.equal(t.cpu(), h) for t, h in zip(pools[0], host))
+
+
+def test_copies_alone_in_a_graph():
+    """Captured with no plan before them: after nothing, and after a copy of the list."""
+    pools = _pools(20, 2, 64, BF, 2, seed=3)
+    handle = da.page_pools(*pools)
+    host = [t.cpu() for p in pools for t in p]
+    lists = [[[1, 2, 64], [3, 4, 10]], [[2, 5, 7], [-1, 0, 64]], [[4, 6, 64], [5, 7, 33]]]
+    copies, staged = _i32(lists[0]), _i32(lists[0])
+    da.diffattn_pages_copy(handle, copies)
+    host = [ref.copied(t, lists[0]) for t in host]
+    graphs = [torch.cuda.CUDAGraph(), torch.cuda.CUDAGraph()]
+    with torch.cuda.graph(graphs[0]):
+        da.diffattn_pages_copy(handle, copies)
+    with torch.cuda.graph(graphs[1]):
+        copies.copy_(staged)
+        da.diffattn_pages_copy(handle, copies)
+    for graph, now in zip(graphs, lists[1:]):
+        staged.copy_(_i32(now))
+        if graph is graphs[0]:
+            copies.copy_(staged)
+        graph.replay()
+        host = [ref.copied(t, now) for t in host]
+        assert all(torch.equal(t.cpu(), h) for t, h in zip((t for p in pools for t in p), host))
