@@ -22,7 +22,8 @@
  *  - All pointers are device pointers unless stated otherwise. Work is
  *    enqueued on `stream` (a cudaStream_t; NULL is the legacy default stream).
  *    Some kernels (the GEMMs, the wide-head attention, add+RMSNorm, the
- *    backward's key side) are programmatic dependent launches: their CTAs may
+ *    backward's key side, the merge of beams, the copies of pages) are
+ *    programmatic dependent launches: their CTAs may
  *    start their setup while the previous kernel on the stream finishes, but
  *    they read nothing and complete nothing before it has completed, so stream
  *    order holds as for ordinary launches (also under CUDA-graph capture).
@@ -518,7 +519,7 @@ diffattn_status diffattn_beam_reorder(const diffattn_beam_state* states, int cou
  * others, grow, roll back, start or end. The state is the table [B K, max_pages], the tokens of each row
  * (a row holds its first ceil(lens / 64) entries) and of each page the number of its holders; a page
  * with a count of 0 or less is free. Others than these rows (a kept prefix, another table) hold a page
- * by one more in its count.
+ * by one more in its count. Lengths are clamped to [0, 64 max_pages].
  *
  * Row i = b K + k continues row b K + parents[b, k] (parents NULL: itself; a parent outside [0, K) or
  * done[i] != 0: no row). It keeps the first min(lens[parent], new) of its tokens, where new is
