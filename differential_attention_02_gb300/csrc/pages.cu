@@ -117,6 +117,10 @@ __host__ __device__ constexpr int claim_places(int S) {
     while (n < 2 * S) n *= 2;
     return n;
 }
+// A page's place: the high bits of a product, so that pages at even distances (a fixed reservation a sequence) do not meet.
+__device__ __forceinline__ int claim_place(int page, int places) {
+    return (int)(((uint32_t)page * 0x9e3779b1u) >> (__clz(places) + 1));
+}
 constexpr int kColumns = 8;  // of a row, read together: 32 bytes
 __host__ __device__ constexpr size_t fork_bytes(int S, int tiles) {
     const size_t columns = (size_t)S * tiles * kColumns * 4, rest = ((size_t)claim_places(S) * 2 + 2 * (size_t)S + 1) * 4;
@@ -201,11 +205,11 @@ __global__ void __launch_bounds__(kPlanThreads) pages_fork_kernel(const __grid_c
     cluster_sync<BLOCKS>();  // the counts without the begun pages, and the begun pages
 
     // The begun page stays with the first row that has it, if it has no other holder. Every block finds that out for
-    // itself: the rows' pages in a table by their low bits, with the lowest row of each.
+    // itself: the rows' pages in a hash table, with the lowest row of each.
     for (int i = tid; i < p.S; i += kPlanThreads) {
         const int t = tail[i];
         if (t < 0) continue;
-        int at = t & (places - 1);
+        int at = claim_place(t, places);
         for (int k = 0; k < places; ++k, at = (at + 1) & (places - 1)) {  // (a place is free for every row)
             const int there = atomicCAS(&claim_page[at], -1, t);
             if (there == -1 || there == t) break;
@@ -221,7 +225,7 @@ __global__ void __launch_bounds__(kPlanThreads) pages_fork_kernel(const __grid_c
             const int t = tail[i];
             bool stays = false;
             if (t >= 0) {
-                int at = t & (places - 1);
+                int at = claim_place(t, places);
                 for (int k = 0; k < places && claim_page[at] != t; ++k) at = (at + 1) & (places - 1);
                 stays = claim_row[at] == i && __ldcg(&p.refs_out[t]) <= 0;
                 copy = !stays;

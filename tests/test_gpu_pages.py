@@ -142,6 +142,34 @@ def test_sizes_at_the_limits():
     assert p.refs.tolist() == [1, 0, 0] and p.info.tolist() == [0, 0, 2, 1]
 
 
+def test_pages_at_even_distances():
+    """A fixed reservation a sequence, 128 or 8192 pages apart."""
+    for S, step in ((64, 128), (512, 128), (100, 8192)):
+        table = [[i * step, i * step + 1] for i in range(S)]
+        refs = [0] * (S * step)
+        for row in table:
+            refs[row[0]] = refs[row[1]] = 1
+        _fork(table, [100] * S, refs, [[max(0, i - i % 3) for i in range(S)]], 1)
+
+
+def test_a_pool_of_many_pages():
+    """More pages than 32 a thread."""
+    rng = random.Random(3)
+    P, S, M = 400000, 6, 40
+    refs = [rng.choice([1, 1, 1, 1, 0, -1]) for _ in range(P)]
+    table = [[rng.randrange(P) for _ in range(M)] for _ in range(S)]
+    for row in table:
+        for p in row:
+            refs[p] = max(refs[p], 0) + 1
+    lens = [M * PAGE - 5 * i for i in range(S)]
+    _fork(table, lens, refs, [[0, 0, 1, 5, 5, -1]], 3)
+    _fork(table, lens, refs, None, 0, [0, 2500, 0, 0, 2000, 10])
+    args = [_table(table, M), _i32(lens), _i32(refs)]
+    p = da.diffattn_pages_compact(*args)
+    want = ref.compact(table, lens, refs)
+    assert (p.table.tolist(), p.refs.tolist(), p.copies.tolist(), p.info.tolist(), p.moved.tolist()) == want
+
+
 @pytest.mark.parametrize("seed", range(10))
 def test_random_compactions(seed):
     rng = random.Random(seed)
