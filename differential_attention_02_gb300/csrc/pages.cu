@@ -469,7 +469,7 @@ cudaError_t launch_pages_copy(const CopyParams& p, int pools, cudaStream_t strea
     if (e != cudaSuccess) return e;
     int heads = 1;
     for (int i = 0; i < pools; ++i) heads = p.pool[i].heads > heads ? p.pool[i].heads : heads;
-    const int64_t units = (int64_t)p.max_copies * heads, most = (int64_t)sms * 8;
+    const int64_t units = (int64_t)p.max_copies * heads, most = (int64_t)sms * 16;
     const dim3 grid((unsigned)(units < most ? units : most), (unsigned)pools);
     return launch_pdl(pages_copy_kernel, grid, dim3(256), 0, stream, p);
 }
