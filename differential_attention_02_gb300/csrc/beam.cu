@@ -318,8 +318,8 @@ __device__ __forceinline__ double inverse_power(int n, double a) {
 }
 
 // One block per chunk of a row: its sum of exponentials and its W best logits. Bound by HBM while the rows come, by latencies
-// behind them: of 32 x 8 rows of 200003 bf16 logits (102 MB) the rows take 16 us (6.4 TB/s, 95% of the copy's rate) and the
-// selection of 16 each 6 more, as all blocks select at about the same time; of 4 rows of 32000 fp32 logits 1 and 3.
+// behind them: of 32 x 8 rows of 200003 bf16 logits (102 MB) the rows take 16 us (6.4 TB/s, 95% of the copy's rate), the
+// start 4 and the selection of 16 each 4 more, as all blocks select at about the same time.
 template <typename T, BeamMode MODE>
 __global__ void __launch_bounds__(kThreads, 4) beam_rows_kernel(const __grid_constant__ BeamParams p) {
     using View = RowView<T>;
@@ -535,7 +535,7 @@ __global__ void __launch_bounds__(kThreads, 4) beam_rows_kernel(const __grid_con
 }
 
 // One block per sequence, a warp per beam: the beam's chunks are merged by their logits, then the
-// beams by their ranks. Bound by latencies: 4 us for four beams and four kept, 6 for eight and 16.
+// beams by their ranks. Bound by latencies: 3 us for four beams and four kept, 5 for eight and 16.
 __global__ void __launch_bounds__(32 * kMaxBeams) beam_merge_kernel(const __grid_constant__ BeamParams p) {
     extern __shared__ uint64_t shared[];  // [K][chunks W] keys, then [K][W] keys, [K][W] scores, [K][W] ranks
     __shared__ uint64_t tops[kMaxBeams * 64];
