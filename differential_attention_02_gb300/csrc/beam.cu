@@ -7,8 +7,8 @@
 // their length n. Within a beam the ranking is that of the logits, so a row only has to
 // give its W best logits, its maximum and its sum; the beams' lists are then merged.
 //
-// The sum's terms are fp32, each within 2^-22 of itself; lanes' sums are joined in 64
-// bits, and scores are formed and compared in 64 bits, so that the order of two
+// The sum's terms are fp32, each within 2^-22 + 2^-23 |x_v - m| of itself; lanes' sums are
+// joined in 64 bits, and scores are formed and compared in 64 bits, so that the order of two
 // candidates of different beams does not hang on fp32's rounding of sums near -50.
 //
 // A row is read once. Blocks share a row in chunks; a warp reads a round of four vectors

@@ -481,8 +481,8 @@ diffattn_status diffattn_chunk_workspace_size(int T, int B, int H, int kv_group,
  *   `eos`), and its n. Places without a candidate hold score -inf, parent -1, token `eos` (0 without
  *   one), finished 1 and length 0. With W = K the outputs may be the inputs' own arrays.
  * 1 <= K <= 32, 1 <= W <= 64, W <= K V, V <= DIFFATTN_MAX_VOCABULARY, B <= 65535. B equal to 0: DIFFATTN_OK.
- * Scores are formed and compared in 64 bits from fp32 sums of exponentials (each term within 2^-22 of
- *   itself) and rounded once to fp32 (below its range to -inf). Results do not depend on scheduling.
+ * Scores are formed and compared in 64 bits from fp32 sums of exponentials (a term e^(x - m)
+ *   within 2^-22 + 2^-23 |x - m| of itself) and rounded once to fp32 (below its range to -inf). Results do not depend on scheduling.
  * workspace: diffattn_beam_workspace_size() bytes, 256-byte aligned, for one call at a time.
  */
 #define DIFFATTN_MAX_VOCABULARY (1 << 20)
