@@ -319,7 +319,7 @@ __device__ __forceinline__ double inverse_power(int n, double a) {
 
 // One block per chunk of a row: its sum of exponentials and its W best logits. Bound by HBM while the rows come, by latencies
 // behind them: of 32 x 8 rows of 200003 bf16 logits (102 MB) the rows take 16 us (6.4 TB/s, 95% of the copy's rate), the
-// start 4 and the selection of 16 each 4 more, as all blocks select at about the same time.
+// start 4 and the selection of 16 each 3 more, as all blocks select at about the same time.
 template <typename T, BeamMode MODE>
 __global__ void __launch_bounds__(kThreads, 4) beam_rows_kernel(const __grid_constant__ BeamParams p) {
     using View = RowView<T>;
@@ -470,15 +470,11 @@ __global__ void __launch_bounds__(kThreads, 4) beam_rows_kernel(const __grid_con
         const int mine = first_of(w) + lane * View::kVec;
         uint4 v[kVecs];
         view.template load<kVecs, false>(first_of(w), mine, v);
-#pragma unroll 1
-        for (int i = 0; i < kVecs; ++i) {
-            uint4 x = v[0];
 #pragma unroll
-            for (int k = 1; k < kVecs; ++k)
-                if (i == k) x = v[k];
-            if (!__any_sync(0xffffffffu, View::largest(x) >= bound)) continue;
+        for (int i = 0; i < kVecs; ++i) {
+            if (!__any_sync(0xffffffffu, View::largest(v[i]) >= bound)) continue;
             float f[View::kVec];
-            View::unpack(x, f);
+            View::unpack(v[i], f);
             uint32_t more = 0, same = 0;
 #pragma unroll
             for (int j = 0; j < View::kVec; ++j) {
