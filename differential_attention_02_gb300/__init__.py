@@ -793,6 +793,9 @@ def _typed(t, dtype, dev, shape, what):
         raise ValueError(f"{what} must be a contiguous {dtype} tensor of shape {list(shape)} on the operands' device")
 
 
+_INT_MAX = (1 << 31) - 1  # sizes and numbers beyond it would reach the library cut off
+
+
 def diffattn_beam_select(logits, scores, width: int | None = None, finished=None, lengths=None, eos: int | None = None,
                          length_penalty: float = 0.0, out: BeamChoice | None = None, ws=None, stream=None) -> BeamChoice:
     """The `width` (default: K) best continuations of each sequence over its beams and the vocabulary. logits [B, K, V]
@@ -823,6 +826,8 @@ def diffattn_beam_select(logits, scores, width: int | None = None, finished=None
     if lengths is not None:
         _typed(lengths, _INT32, dev, shape, "lengths")
     W = K if width is None else int(width)
+    if max(B, K, V, W) > _INT_MAX or W < 1 or (eos is not None and not 0 <= eos < V):
+        raise ValueError("width must be positive, eos a token of the vocabulary, and sizes within 31 bits")
     if ws is not None:
         _workspace_arg(ws, dev)
     if out is None:
@@ -871,6 +876,8 @@ def diffattn_beam_reorder(states, parents, lens=None, stream=None):
     _int32(parents, dev, shape, "parents")
     if lens is not None:
         _int32(lens, dev, (B * K,), "lens")
+    if B * K > _INT_MAX:
+        raise ValueError("states must have at most 2^31 - 1 rows")
     packed = []
     for t in states:
         if t.device != dev or t.dim() < 1 or t.shape[0] != B * K:
@@ -911,6 +918,8 @@ def _page_state(table, lens, refs):
     if table.dim() != 2 or refs.dim() != 1:
         raise ValueError("table must be [S, max_pages] and refs [num_pages]")
     (S, M), P = table.shape, refs.shape[0]
+    if max(S, M, P) > _INT_MAX:
+        raise ValueError("table and refs must have sizes within 31 bits")
     _int32(table, dev, (S, M), "table")
     _int32(lens, dev, (S,), "lens")
     _int32(refs, dev, (P,), "refs")
@@ -936,6 +945,8 @@ def diffattn_pages_fork(table, lens, refs, parents=None, grow: int = 0, new_lens
         with ctx:
             return diffattn_pages_fork(table, lens, refs, parents, grow, new_lens, done, out)
     dev, S, M, P = _page_state(table, lens, refs)
+    if not -_INT_MAX <= grow <= _INT_MAX:
+        raise ValueError("grow must be within 31 bits")
     K = max(S, 1)
     if parents is not None:
         if parents.dim() != 2 or parents.shape[0] * parents.shape[1] != S:
@@ -1032,6 +1043,8 @@ def diffattn_pages_copy(pools: PagePools, copies, info=None, stream=None) -> Non
             return diffattn_pages_copy(pools, copies, info)
     n = copies.shape[0] if copies.dim() == 2 else 0
     _int32(copies, dev, (n, 3), "copies")
+    if n > _INT_MAX:
+        raise ValueError("copies must have at most 2^31 - 1 entries")
     if info is not None:
         _int32(info, dev, (4,), "info")
     _check((_lib or load_library()).diffattn_pages_copy(pools._c, pools._n, copies.data_ptr(), None if info is None else info.data_ptr(), n,

@@ -185,6 +185,32 @@ def test_beam_step_checks_its_tensors(no_launch, monkeypatch):
             da.beam_step(*args, **kw)
 
 
+def test_numbers_beyond_31_bits_are_refused(no_launch):
+    """They would reach the library cut off: a width of 2^32 + 3 as 3."""
+    far, on = 1 << 32, dict(device=ELSEWHERE)  # (without memory)
+    logits, scores = torch.zeros(2, 3, 50), torch.zeros(2, 3)
+    for kw in (dict(width=0), dict(width=-far + 3), dict(width=far + 3), dict(eos=far + 5), dict(eos=-far + 5), dict(eos=50), dict(eos=-1)):
+        with pytest.raises(ValueError):
+            da.diffattn_beam_select(logits, scores, **kw)
+    with pytest.raises(ValueError):
+        da.diffattn_beam_select(torch.empty(1, 1, far + 50, **on), torch.empty(1, 1, **on))
+    with pytest.raises(ValueError):
+        da.diffattn_beam_select(torch.empty(far + 1, 1, 2, **on), torch.empty(far + 1, 1, **on))
+    i32 = lambda *s: torch.empty(*s, dtype=torch.int32, **on)  # noqa: E731
+    for grow in (far + 1, -far - 1, 1 << 31):
+        with pytest.raises(ValueError):
+            da.diffattn_pages_fork(i32(6, 4), i32(6), i32(20), grow=grow)
+    for state in ((i32(far + 1, 1), i32(far + 1), i32(20)), (i32(1, far + 1), i32(1), i32(20)), (i32(6, 4), i32(6), i32(far + 20))):
+        with pytest.raises(ValueError):
+            da.diffattn_pages_fork(*state)
+        with pytest.raises(ValueError):
+            da.diffattn_pages_compact(*state)
+    with pytest.raises(ValueError):
+        da.diffattn_beam_reorder([torch.empty(far + 2, 4, **on)], i32(far // 2 + 1, 2))
+    with pytest.raises(ValueError):
+        da.diffattn_pages_copy(da.page_pools(torch.empty(5, 2, 64, 64, **on)), i32(far + 3, 3))
+
+
 def test_the_reference_selects_like_a_sort():
     """beam_reference.select against torch's log_softmax and a stable sort over beams and tokens."""
     g = torch.Generator().manual_seed(1)
