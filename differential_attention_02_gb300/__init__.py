@@ -1080,7 +1080,8 @@ def beam_step(x, w_vocab, scores, pools: PagePools, table, lens, refs, finished=
         raise ValueError("vocabulary must be at most w_vocab's columns")
     if ws is None:
         ws = _serving_workspace(beam_workspace_bytes(B, K, V, K), dev)
-    logits = gemm(x, w_vocab, out_dtype=torch.float32, ws=ws).view(B, K, -1)[..., :V]
+    logits = gemm(x, w_vocab, out_dtype=torch.float32, ws=ws) if B else x.new_empty(x.shape[0], w_vocab.shape[1], dtype=torch.float32)
+    logits = logits.view(B, K, w_vocab.shape[1])[..., :V]
     choice = diffattn_beam_select(logits, scores, None, finished, lengths, eos, length_penalty, out=choice, ws=ws)
     done = None if choice.finished is None else choice.finished.view(-1)
     plan = diffattn_pages_fork(table, lens, refs, choice.parents, grow=1, done=done, out=plan)

@@ -142,3 +142,14 @@ def test_columns_beyond_the_vocabulary_are_never_chosen():
     m.head[:, 400:] *= 50
     choice, histories = _search(m, [[5, 6, 7]], 4, 4, vocabulary=400)
     assert max(t for h in histories[0] for t in h) < 400
+
+
+def test_a_step_of_no_sequences():
+    """An empty batch: empty choices, and the plan of the others' counts alone."""
+    m = Model(seed=2)
+    refs = _i32([0, 2, 0, 1])
+    choice, plan = da.beam_step(m.head.new_empty(0, m.head.shape[0]), m.head, torch.empty(0, 4, device="cuda"), da.page_pools(*m.pools(4)),
+                                torch.empty(0, 3, dtype=torch.int32, device="cuda"), _i32([]), refs, eos=EOS,
+                                finished=torch.empty(0, 4, dtype=torch.bool, device="cuda"))
+    assert choice.tokens.shape == (0, 4) and plan.table.shape == (0, 3) and plan.copies.shape == (0, 3)
+    assert torch.equal(plan.refs, refs) and plan.info.tolist() == [0, 0, 2, 2]
